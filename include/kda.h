@@ -422,6 +422,167 @@ int kda_short_conv(const uint16_t *xq, const uint16_t *xk, const uint16_t *xv,
                    uint16_t *q_out, uint16_t *k_out, uint16_t *v_out, int N, int T, int H, int d,
                    int activation, float eps, void *stream);
 
+/*
+ * ---- the softmax layers of a hybrid stack, and moves of slot entries --------
+ *
+ * A hybrid stack puts softmax-attention layers between its linear-attention
+ * layers.  With a sliding window and a few first tokens that stay visible
+ * (sinks) their cache is bounded, so it is kept like the recurrent state and
+ * the conv window: one entry of fixed size per slot, and one slot id reaches
+ * all three.  The conventions at the top hold (device pointers, asynchronous,
+ * checks before any launch, nothing allocated), with these additions:
+ *
+ *  Types      16-bit tensors are bf16 or fp16 bits, named by `dtype`
+ *             (KDA_BF16, KDA_F16).  Sums, norms, angles and softmax statistics
+ *             are fp32; each output is rounded once.
+ *  Strides    q, k and v are rows (one per token) of [heads][d] dense
+ *             elements; rows lie q_stride, k_stride, v_stride elements apart
+ *             (multiples of 8, at least heads * d), so slices of one fused
+ *             projection are taken as they are.  Outputs are dense.
+ *  Ring cache kv_pool: [num_slots][2 (k, v)][Hk][pool_rows][d].  Position p of a
+ *             sequence (0 is its first token) is kept in row p while p < sinks,
+ *             else in row sinks + (p - sinks) mod (pool_rows - sinks), which a
+ *             later position takes over.  pool_rows >= sinks + window.  Rows
+ *             that hold no visible position are never read (they may hold
+ *             anything).
+ *  Visible    the query at position p sees the positions j <= p with
+ *             j > p - window or j < sinks.  A window of at least the longest
+ *             context is plain causal attention.
+ *  Heads      Hq query heads share Hk key heads in order: query head h reads
+ *             key head h / (Hq / Hk); Hq a multiple of Hk, at most 128 times it.
+ */
+typedef enum { KDA_BF16 = 0, KDA_F16 = 1 } kda_dtype;
+typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
+
+/*
+ * kda_head_norm_rope -- RMS norm of each head of q and k and the rotation of
+ * its position, in one pass.  For every token t and head, with x the head's d
+ * elements, p = positions[t] and (c_i, s_i) = table[p]:
+ *
+ *     y = w * x / sqrt(mean(x^2) + eps)        (norm 1; y = w * x with norm 0)
+ *     (a, b) <- (a c_i - b s_i, b c_i + a s_i)  for i < rotary / 2
+ *
+ * with the pair (a, b) = (y[i], y[i + rotary/2]) (KDA_ROPE_HALF) or
+ * (y[2i], y[2i + 1]) (KDA_ROPE_INTERLEAVED).  Elements from `rotary` on are not
+ * rotated; rotary 0 is the norm alone.
+ *
+ *   q, k           16-bit rows of [Hq][d] and [Hk][d] (strides above).
+ *   q_weight, k_weight  fp32 [d], or NULL (ones).
+ *   table          fp32 [max_pos][rotary]: rotary/2 cosines, then rotary/2
+ *                  sines, of each position (any scaling for long contexts is in
+ *                  the table).  NULL with rotary 0.
+ *   positions      int32 [T], device memory.  An entry outside [0, max_pos) is
+ *                  clamped and sets bit 64 of the device error word.
+ *   q_out, k_out   [T][Hq][d], [T][Hk][d]; each may be its own input (in place)
+ *                  where that input is dense.
+ *   T >= 0; d 64 or 128; rotary a multiple of 16, at most d; eps >= 0 (an
+ *   all-zero head with eps 0 gives NaN, as the formula does).
+ * Tensor pointers must be 16-byte aligned (positions 4-byte).  Returns a
+ * kda_status.
+ */
+int kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                       const float *q_weight, const float *k_weight, const float *table, int max_pos,
+                       const int32_t *positions, void *q_out, void *k_out, int T, int Hq, int Hk, int d,
+                       int rotary, int layout, int norm, float eps, int dtype, void *stream);
+
+/*
+ * kda_window_prefill -- softmax attention of packed new tokens over a sliding
+ * window and sinks, with the earlier tokens in the ring cache:
+ *
+ *     out_t[h] = sum_j softmax_j(scale q_t[h] . k_j) v_j   over the visible j
+ *
+ * Row t of sequence n (rows cu_seqlens[n] .. cu_seqlens[n+1] - 1) is at position
+ * starts[n] + t - cu_seqlens[n].  Keys of positions before starts[n] come from
+ * the cache, the others from the call's own rows; afterwards the cache holds
+ * the sequence's sinks and its last pool_rows - sinks positions.  Serves a
+ * whole prompt, a chunk of a long one, and the verification of drafted tokens
+ * (a few rows for each sequence).  A rejected draft needs no undo while
+ * pool_rows >= sinks + window + rejected tokens: the next call starts at the
+ * kept position and overwrites the rest.
+ *
+ *   starts      int32 [N], device memory, or NULL (all 0).  starts[n] >= 0 and
+ *               starts[n] + rows <= 2^31 - 1; otherwise clamped, setting bit 64.
+ *   slots       int32 [N], device memory, or NULL (entry n).  -1 marks a padded
+ *               sequence: neither its rows of out nor the cache are written.  An id
+ *               outside [-1, num_slots) is treated like -1 and sets bit 8.
+ *               Valid ids must be distinct.
+ *   kv_pool     the ring cache, read and updated in place, or NULL: nothing is
+ *               cached before or after (starts and slots must then be NULL).
+ *   out         [T][Hq][d]; every row of an unpadded sequence is written.
+ *   scale       > 0, finite.
+ * A masked key never reaches an output, whatever its score.  A value row that
+ * is not finite reaches, besides the rows that see it, rows of the same
+ * sequence in the same tile (up to 128 keys by 256 query rows); it reaches no
+ * other sequence.  Runs on the tensor cores with 16-bit
+ * probabilities (rounded by at most 2^-8 bf16, 2^-11 fp16 of each) and fp32 sums.
+ * Tensor pointers must be 16-byte aligned (tables 4-byte); out and kv_pool must
+ * not overlap an input's span or each other.  Returns a kda_status.
+ */
+int kda_window_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const int32_t *cu_seqlens, const int32_t *starts,
+                       const int32_t *slots, void *kv_pool, int num_slots, int pool_rows, void *out, int N,
+                       int T, int Hq, int Hk, int d, int window, int sinks, float scale, int dtype,
+                       void *stream);
+
+/*
+ * kda_window_decode -- kda_window_prefill for one new token of each of N
+ * sequences: row n of q, k, v is at position positions[n] (the length of the
+ * context before it); k and v enter the cache.
+ *
+ *   positions   int32 [N], device memory, >= 0 (else clamped, setting bit 64).
+ *   kv_pool     as above, not NULL.  With slots NULL, num_slots >= N.
+ *   out         [N][Hq][d].
+ * All else as kda_window_prefill.
+ */
+int kda_window_decode(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const int32_t *positions, const int32_t *slots, void *kv_pool,
+                      int num_slots, int pool_rows, void *out, int N, int Hq, int Hk, int d, int window,
+                      int sinks, float scale, int dtype, void *stream);
+
+/*
+ * One pool of slot entries: num_slots entries of entry_bytes bytes each, one
+ * behind the other (a state pool, a conv window pool, a ring cache, ...).
+ */
+typedef struct {
+    void *base;           /* device memory, 16-byte aligned     */
+    int64_t entry_bytes;  /* a multiple of 16                   */
+} kda_pool;
+#define KDA_MAX_POOLS 128
+#define KDA_MAX_POOL_SLOTS 524288
+
+/*
+ * kda_slots_copy -- copies entries between slots in all the given pools at once:
+ * entry dst[i] of every pool becomes entry src[i] (fork a sequence, keep a
+ * prefix, put a sequence elsewhere), or zeros where src[i] is -1 (a fresh
+ * sequence, a freed slot).
+ *
+ *   pools       HOST array of num_pools (at most KDA_MAX_POOLS) pools, read
+ *               before the call returns; they must not overlap.
+ *   src, dst    int32 [M], device memory.  dst[i] = -1 skips row i.  Several
+ *               rows may name one source; the targets must be distinct, and no
+ *               target may be a source of another row.  An id outside
+ *               [-1, num_slots) skips its row and sets bit 8.
+ *   num_slots   entries in every pool, at most KDA_MAX_POOL_SLOTS.
+ * Returns a kda_status.
+ */
+int kda_slots_copy(const kda_pool *pools, int num_pools, int num_slots, const int32_t *src,
+                   const int32_t *dst, int M, void *stream);
+
+/*
+ * kda_slots_compact -- moves the live entries to the front of the pools.  With m
+ * the number of table entries slots[i] >= 0, ids below m stay, and the ids from m
+ * on, in ascending order, take the free ids below m in ascending order.
+ * new_slots[i] is where slots[i] went (-1 stays -1); entries that were moved
+ * away keep their old bytes.
+ *
+ *   slots       int32 [N], device memory: every live slot once, -1 elsewhere.
+ *               An id outside [-1, num_slots) becomes -1 and sets bit 8.
+ *   new_slots   int32 [N], device memory, not overlapping slots.
+ * All else as kda_slots_copy.
+ */
+int kda_slots_compact(const kda_pool *pools, int num_pools, int num_slots, const int32_t *slots,
+                      int32_t *new_slots, int N, void *stream);
+
 /* Human-readable name of a kda_status value (static string, never NULL). */
 const char *kda_status_string(int status);
 
@@ -434,8 +595,9 @@ const char *kda_status_string(int status);
  * sequence was skipped).  Bit 16: an accepted count of kda_fold_commit was
  * outside [0, W] (clamped).  Bit 32: the tensor-core prefill met a chunk whose
  * decay is outside its fp16 operand range (see "Range" above; use
- * kda_chunk_prefill_fullrange for such inputs).  0 means no kernel of this
- * library has reported an error.
+ * kda_chunk_prefill_fullrange for such inputs).  Bit 64: a position or context
+ * length was outside its range (clamped).  0 means no kernel of this library
+ * has reported an error.
  * Synchronises the current device.  If `reset` is nonzero the word is
  * cleared after reading.  Returns KDA_OK or KDA_ERR_CUDA.
  */

@@ -21,13 +21,19 @@ KDA_NOALLOC_MAX_SEQS = 16384
 
 EXPORTED = ("kda_chunk_prefill", "kda_chunk_prefill_f32", "kda_chunk_prefill_fullrange", "kda_status_string",
             "kda_device_error", "kda_chunk_prefill_noalloc", "kda_chunk_prefill_slots", "kda_chunk_prefill_conv",
-            "kda_decode", "kda_fold_commit", "kda_short_conv", "kda_decode_conv")
+            "kda_decode", "kda_fold_commit", "kda_short_conv", "kda_decode_conv", "kda_head_norm_rope",
+            "kda_window_prefill", "kda_window_decode", "kda_slots_copy", "kda_slots_compact")
 # device error word bits (kda_device_error)
 ERR_WAIT_TIMEOUT = 1    # a bounded wait ran out; the kernel wound down early
 ERR_BAD_SEQLENS = 2     # a cu_seqlens entry broke its contract (clamped)
 ERR_BAD_SLOT = 8        # a state slot id outside [-1, num_slots)
 ERR_BAD_ACCEPTED = 16   # an accepted count outside [0, window]
 ERR_DECAY_RANGE = 32    # the tensor-core prefill met a decay beyond its fp16 operand range
+ERR_BAD_POSITION = 64   # a position or context length outside its range (clamped)
+
+KDA_BF16, KDA_F16 = 0, 1
+KDA_ROPE_HALF, KDA_ROPE_INTERLEAVED = 0, 1
+KDA_MAX_POOLS, KDA_MAX_POOL_SLOTS = 128, 524288
 
 _lib = None
 
@@ -66,6 +72,14 @@ def load(path: str = LIB_PATH):
     lib.kda_short_conv.restype = I
     lib.kda_decode_conv.argtypes = [P, P, P, P, P, P, I, P, P, P, P, I, P, I, I, I, I, I, ctypes.c_float, P]
     lib.kda_decode_conv.restype = I
+    L, F = ctypes.c_int64, ctypes.c_float
+    lib.kda_head_norm_rope.argtypes = [P, L, P, L, P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, I, P]
+    lib.kda_window_prefill.argtypes = [P, L, P, L, P, L, P, P, P, P, I, I, P, I, I, I, I, I, I, I, F, I, P]
+    lib.kda_window_decode.argtypes = [P, L, P, L, P, L, P, P, P, I, I, P, I, I, I, I, I, I, F, I, P]
+    lib.kda_slots_copy.argtypes = [P, I, I, P, P, I, P]
+    lib.kda_slots_compact.argtypes = [P, I, I, P, P, I, P]
+    for name in EXPORTED[-5:]:
+        getattr(lib, name).restype = I
     lib.kda_status_string.argtypes = [I]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), I]
@@ -155,6 +169,41 @@ def kda_decode_conv(xq, xk, xv, conv_weight, conv_slots, conv_pool, conv_num_slo
     """Raw C-ABI call: the decode step with the short conv fused in front of it."""
     return load().kda_decode_conv(xq, xk, xv, conv_weight, conv_slots, conv_pool, conv_num_slots, g, beta,
                                   state_slots, state_pool, num_slots, out, N, H, dk, dv, activation, eps, stream)
+
+
+def kda_head_norm_rope(q, q_stride: int, k, k_stride: int, q_weight, k_weight, table, max_pos: int, positions, q_out,
+                       k_out, T: int, Hq: int, Hk: int, d: int, rotary: int, layout: int, norm: int, eps: float,
+                       dtype: int, stream) -> int:
+    """Raw C-ABI call: per-head RMS norm and rotation of q and k."""
+    return load().kda_head_norm_rope(q, q_stride, k, k_stride, q_weight, k_weight, table, max_pos, positions, q_out,
+                                     k_out, T, Hq, Hk, d, rotary, layout, norm, eps, dtype, stream)
+
+
+def kda_window_prefill(q, q_stride: int, k, k_stride: int, v, v_stride: int, cu_seqlens, starts, slots, kv_pool,
+                       num_slots: int, pool_rows: int, out, N: int, T: int, Hq: int, Hk: int, d: int, window: int,
+                       sinks: int, scale: float, dtype: int, stream) -> int:
+    """Raw C-ABI call: window attention of packed new tokens over the ring cache and themselves."""
+    return load().kda_window_prefill(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, starts, slots, kv_pool,
+                                     num_slots, pool_rows, out, N, T, Hq, Hk, d, window, sinks, scale, dtype, stream)
+
+
+def kda_window_decode(q, q_stride: int, k, k_stride: int, v, v_stride: int, positions, slots, kv_pool,
+                      num_slots: int, pool_rows: int, out, N: int, Hq: int, Hk: int, d: int, window: int, sinks: int,
+                      scale: float, dtype: int, stream) -> int:
+    """Raw C-ABI call: window attention of one new token per sequence over the ring cache."""
+    return load().kda_window_decode(q, q_stride, k, k_stride, v, v_stride, positions, slots, kv_pool, num_slots,
+                                    pool_rows, out, N, Hq, Hk, d, window, sinks, scale, dtype, stream)
+
+
+def kda_slots_copy(pools, num_pools: int, num_slots: int, src, dst, M: int, stream) -> int:
+    """Raw C-ABI call: copies (or clears) slot entries in every pool; pools is the address of a host array of
+    (base, entry_bytes) pairs of 64-bit integers."""
+    return load().kda_slots_copy(pools, num_pools, num_slots, src, dst, M, stream)
+
+
+def kda_slots_compact(pools, num_pools: int, num_slots: int, slots, new_slots, N: int, stream) -> int:
+    """Raw C-ABI call: moves the live slot entries to the front of every pool."""
+    return load().kda_slots_compact(pools, num_pools, num_slots, slots, new_slots, N, stream)
 
 
 def device_error(reset: bool = False) -> int:
@@ -458,3 +507,235 @@ def decode_conv(xq, xk, xv, conv_weight, conv_pool, g, beta, state_pool, conv_sl
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_conv")
     return out
+
+
+ROPE_LAYOUTS = {"half": KDA_ROPE_HALF, "interleaved": KDA_ROPE_INTERLEAVED}
+
+
+def _handle(stream, device) -> int:
+    import torch
+
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return int(s.cuda_stream) if hasattr(s, "cuda_stream") else int(s)
+
+
+def _dtype16(t, name: str) -> int:
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return KDA_BF16
+    if t.dtype == torch.float16:
+        return KDA_F16
+    raise ValueError(f"{name} must be bfloat16 or float16")
+
+
+def _rows_of_heads(name: str, t, dtype):
+    """Checks rows of [heads][d] dense elements; returns the rows' distance in elements."""
+    if not t.is_cuda or t.dim() != 3 or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor [rows][heads][d] of q's dtype")
+    (_, h, d), (row, head, one) = t.shape, t.stride()
+    if one != 1 or (h > 1 and head != d):
+        raise ValueError(f"{name} must be dense within each row")
+    return row if t.shape[0] > 1 else h * d
+
+
+def _table32(name: str, t, n: int):
+    import torch
+
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.shape != (n,):
+        raise ValueError(f"{name} must be int32 [{n}] on the device")
+
+
+def _dense(name: str, t, shape, dtype):
+    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+
+
+def rope_table(max_pos: int, rotary: int, base: float = 10000.0, stretch: float = 1.0, trained: int = 0,
+               fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Cosines and sines of the positions 0 .. max_pos-1 for head_norm_rope: float32 [max_pos][rotary], computed in
+    float64.  Pair i of a head turns by base^(-2i/rotary) per position.
+
+    A context ``stretch`` times the trained one: with ``trained`` 0 every frequency is divided by ``stretch``
+    (positions are interpolated).  With ``trained`` the trained context's length, frequencies are interpolated by
+    parts (the YaRN method): a pair that turns at least ``fast`` times within the trained context keeps its
+    frequency, one that turns at most ``slow`` times has it divided, those between are blended linearly in the pair's
+    index, and the table is scaled by 1 + 0.1 ln(stretch), so that logits grow with its square.
+    """
+    import math
+
+    import torch
+
+    if max_pos < 1 or rotary < 2 or rotary % 2 or not base > 1.0 or not stretch >= 1.0 or trained < 0:
+        raise ValueError("rope_table needs max_pos >= 1, an even rotary >= 2, base > 1, stretch >= 1, trained >= 0")
+    i = torch.arange(rotary // 2, dtype=torch.float64, device=device)
+    f = base ** (-2.0 * i / rotary)
+    size = 1.0
+    if trained and stretch > 1.0:
+        def pair_of(turns):   # the (real-valued) pair that turns so often within the trained context
+            return rotary * math.log(trained / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo, hi = max(0.0, math.floor(pair_of(fast))), min(rotary - 1.0, math.ceil(pair_of(slow)))
+        part = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1.0 - part) + f / stretch * part
+        size = 1.0 + 0.1 * math.log(stretch)
+    else:
+        f = f / stretch
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([angle.cos(), angle.sin()], 1).mul_(size).float()
+
+
+def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=None, layout: str = "half",
+                   eps: float = 1e-6, norm: bool = True, out=None, stream=None):
+    """Per-head RMS norm and rotation of q and k in one pass, on torch CUDA tensors.
+
+    q: [T][Hq][d], k: [T][Hk][d], bfloat16 or float16, d 64 or 128, dense within a row (rows may be slices of a fused
+    projection); q_weight, k_weight: [d] float32 or None; positions: [T] int32 and table: [max_pos][rotary] float32
+    (rope_table), or both None (no rotation); layout "half" or "interleaved".  ``norm`` False rotates only.  Returns
+    (q, k), dense; ``out`` may name them (in place where the inputs are dense).
+    """
+    import torch
+
+    dt = _dtype16(q, "q")
+    sq, sk = _rows_of_heads("q", q, q.dtype), _rows_of_heads("k", k, q.dtype)
+    (T, Hq, d), Hk = q.shape, k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("k must have q's rows and head size")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _dense(name, w, (d,), torch.float32)
+    rotary = max_pos = 0
+    if (positions is None) != (table is None):
+        raise ValueError("positions and table go together")
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must be [max_pos][rotary]")
+        max_pos, rotary = table.shape
+        _dense("table", table, (max_pos, rotary), torch.float32)
+        _table32("positions", positions, T)
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    if out is None:
+        q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        k_out = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device)
+    else:
+        q_out, k_out = out
+        _dense("out[0]", q_out, (T, Hq, d), q.dtype)
+        _dense("out[1]", k_out, (T, Hk, d), q.dtype)
+    st = load().kda_head_norm_rope(_ptr(q), sq, _ptr(k), sk, _ptr(q_weight), _ptr(k_weight), _ptr(table), max_pos,
+                                   _ptr(positions), _ptr(q_out), _ptr(k_out), T, Hq, Hk, d, rotary,
+                                   ROPE_LAYOUTS[layout], int(norm), eps, dt, _handle(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_head_norm_rope")
+    return q_out, k_out
+
+
+def _window_args(q, k, v, kv_pool, slots, N, out):
+    """The checks that the two window-attention calls share; returns what both pass on."""
+    import torch
+
+    dt = _dtype16(q, "q")
+    strides = _rows_of_heads("q", q, q.dtype), _rows_of_heads("k", k, q.dtype), _rows_of_heads("v", v, q.dtype)
+    (T, Hq, d), Hk = q.shape, k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d or v.shape != k.shape:
+        raise ValueError("k and v must have q's rows and head size, and the same heads")
+    num_slots = rows = 0
+    if kv_pool is not None:
+        if kv_pool.dim() != 5:
+            raise ValueError("kv_pool must be [num_slots][2][Hk][rows][d]")
+        num_slots, rows = kv_pool.shape[0], kv_pool.shape[3]
+        _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), q.dtype)
+    if slots is not None:
+        _table32("slots", slots, N)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    else:
+        _dense("out", out, (T, Hq, d), q.dtype)
+    return dt, strides, T, Hq, Hk, d, num_slots, rows, out
+
+
+def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=None, slots=None, starts=None,
+                   scale: Optional[float] = None, out=None, stream=None):
+    """Attention of packed new tokens over a sliding window and the first ``sinks`` positions, on torch CUDA tensors.
+
+    q: [T][Hq][d], k, v: [T][Hk][d], bfloat16 or float16, d 64 or 128, dense within a row; cu_seqlens: [N+1] int32 on
+    the device; kv_pool: [num_slots][2][Hk][rows][d], the ring caches (rows >= sinks + window), read and updated in
+    place, or None (nothing cached); slots: [N] int32 (-1 = padded sequence, skipped) or None for entry n; starts: [N]
+    int32, the tokens of each sequence already cached, or None for 0; scale: d^-0.5 by default.  Returns out
+    [T][Hq][d] (rows of padded sequences keep what ``out`` held).
+    """
+    N = int(cu_seqlens.shape[0]) - 1
+    dt, (sq, sk, sv), T, Hq, Hk, d, num_slots, rows, out = _window_args(q, k, v, kv_pool, slots, N, out)
+    _table32("cu_seqlens", cu_seqlens, N + 1)
+    if starts is not None:
+        _table32("starts", starts, N)
+    st = load().kda_window_prefill(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(cu_seqlens), _ptr(starts), _ptr(slots),
+                                   _ptr(kv_pool), num_slots, rows, _ptr(out), N, T, Hq, Hk, d, window, sinks,
+                                   d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_window_prefill")
+    return out
+
+
+def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slots=None,
+                  scale: Optional[float] = None, out=None, stream=None):
+    """window_prefill for one new token per sequence, on torch CUDA tensors: row n of q [N][Hq][d], k and v
+    [N][Hk][d] is at position positions[n] ([N] int32 on the device, the tokens cached before it); k and v enter
+    kv_pool in place.  Returns out [N][Hq][d] (rows of padded sequences, slot -1, keep what ``out`` held).
+    """
+    N = q.shape[0]
+    dt, (sq, sk, sv), _, Hq, Hk, d, num_slots, rows, out = _window_args(q, k, v, kv_pool, slots, N, out)
+    _table32("positions", positions, N)
+    st = load().kda_window_decode(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(positions), _ptr(slots), _ptr(kv_pool),
+                                  num_slots, rows, _ptr(out), N, Hq, Hk, d, window, sinks,
+                                  d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_window_decode")
+    return out
+
+
+def _pools(pools):
+    """A host array of (base, entry_bytes) pairs, the number of slots and the device of a list of pool tensors."""
+    n = int(pools[0].shape[0])
+    flat = []
+    for p in pools:
+        if not p.is_cuda or not p.is_contiguous() or p.dim() < 2 or p.shape[0] != n:
+            raise ValueError("every pool must be a contiguous CUDA tensor [num_slots][...] of the same num_slots")
+        flat += (p.data_ptr(), p.stride(0) * p.element_size())
+    return (ctypes.c_int64 * len(flat))(*flat), n, pools[0].device
+
+
+def slots_copy(pools, src, dst, stream=None) -> None:
+    """Copies slot entries in every pool of a list at once, on torch CUDA tensors: entry dst[i] becomes entry src[i],
+    or zeros where src[i] is -1; dst[i] = -1 skips a row.  pools: contiguous [num_slots][...] tensors; src, dst: [M]
+    int32 on the device (targets distinct and no other row's source).
+    """
+    array, n, device = _pools(pools)
+    M = int(src.shape[0])
+    _table32("src", src, M)
+    _table32("dst", dst, M)
+    st = load().kda_slots_copy(ctypes.addressof(array), len(array) // 2, n, _ptr(src), _ptr(dst), M,
+                               _handle(stream, device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_slots_copy")
+
+
+def slots_compact(pools, slots, new_slots=None, stream=None):
+    """Moves the live entries (slots[i] >= 0, each once) to the front of every pool of a list, on torch CUDA tensors:
+    with m live entries, ids from m on take the free ids below m, both in ascending order.  slots: [N] int32 on the
+    device.  Returns new_slots [N] int32, where each went (-1 stays).
+    """
+    import torch
+
+    array, n, device = _pools(pools)
+    N = int(slots.shape[0])
+    _table32("slots", slots, N)
+    if new_slots is None:
+        new_slots = torch.empty_like(slots)
+    else:
+        _table32("new_slots", new_slots, N)
+    st = load().kda_slots_compact(ctypes.addressof(array), len(array) // 2, n, _ptr(slots), _ptr(new_slots), N,
+                                  _handle(stream, device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_slots_compact")
+    return new_slots

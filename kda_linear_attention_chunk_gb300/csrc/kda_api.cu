@@ -12,6 +12,7 @@
 #include "kda.h"
 #include "kda_conv.h"
 #include "kda_decode.h"
+#include "kda_hybrid.h"
 #include "kda_internal.h"
 
 namespace {
@@ -189,6 +190,17 @@ int error_word_address(int **out)
     DevInfo *d = nullptr;
     const int st = device_info(&d);
     if (st == KDA_OK) *out = d->err;
+    return st;
+}
+
+int device_facts(int *num_sms, int **err_word)
+{
+    DevInfo *d = nullptr;
+    const int st = device_info(&d);
+    if (st == KDA_OK) {
+        *num_sms = d->num_sms;
+        *err_word = d->err;
+    }
     return st;
 }
 

@@ -1,0 +1,365 @@
+// kda_window_decode.cu -- window attention of one new token per sequence over
+// the ring cache; the token's key and value enter the cache.
+//
+// For a sequence at position p and key head h, with the visible list of p's sinks
+// and window, o = sum_j softmax_j(scale q . k_j) v_j for the G query heads of h.
+// Each cached row is read once for all G heads (2 x 2 d bytes against 4 G d
+// operations), so HBM bounds it as long as enough loads are in flight.
+//
+// A CTA of eight warps takes (sequence, key head, up to 16 query heads); a
+// cluster of CTAs shares one such unit where there are too few units to fill the
+// SMs.  The list of visible rows is dealt to all warps in steps of 16 keys.  The
+// heads are the 16 rows of the warp MMA: S = Q K^T, then O += P V with a running
+// maximum and sum per warp.  Both products take their operands straight from
+// global memory into registers:  the order of the summed index is free, so a
+// lane loads 16 contiguous bytes of a key row and uses them as the operands of
+// two MMAs (q is held in the same order); of the value rows it loads 16 bytes of
+// two neighbouring keys and interleaves them, which permutes only the output
+// columns.  Warps, then CTAs of a cluster (through distributed shared memory),
+// join their (maximum, sum, O) at the end.  The new token's rows are taken from
+// the call's arguments by everyone, so nobody reads the cache row being written.
+#include <cooperative_groups.h>
+#include <stdint.h>
+
+#include "kda_window.h"
+
+namespace cg = cooperative_groups;
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kHeads = 16;      // query heads of a CTA: the rows of the MMA
+constexpr int kStep = 16;       // keys of a warp at a time
+
+struct DecodeWinParams {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *positions, *slots;
+    uint16_t *pool, *out;
+    int N, Hq, Hk, groups;      // groups of up to 16 query heads per key head
+    int num_slots, pool_rows, window, sinks;
+    float scale_log2;
+    int *err;
+};
+
+template <typename E>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                        uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// shared memory of a CTA: every warp's O, then maxima and sums; after the warps
+// are joined, the CTA's own in part[0]
+template <int D> struct DecodeSmem {
+    float o[kWarps][kHeads][D];
+    float m[kWarps][kHeads], l[kWarps][kHeads];
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+window_decode_kernel(const __grid_constant__ DecodeWinParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(smem_raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+
+    int unit = blockIdx.x / ranks;
+    const int group = unit % p.groups;
+    unit /= p.groups;
+    const int hk = unit % p.Hk, n = unit / p.Hk;
+    const bool reports = threadIdx.x == 0 && rank == 0 && hk == 0 && group == 0;
+    const int entry = entry_of(p.slots, n, p.num_slots, p.err, reports);
+    if (entry < 0) return;      // the whole cluster
+    int pos = p.positions[n];
+    if (pos < 0) {
+        if (reports) atomicOr(p.err, kErrBadPosition);
+        pos = 0;
+    }
+    const int G = p.Hq / p.Hk, head0 = hk * G + group * kHeads, heads = min(kHeads, G - group * kHeads);
+
+    // list of visible positions: sinks before the window, then the window
+    const int lo = max(0, pos - p.window + 1), ns = min(p.sinks, lo), count = ns + pos - lo + 1;
+    const int ring = p.pool_rows - p.sinks, wrap0 = max(lo, p.sinks);
+    const int ring0 = (wrap0 - p.sinks) % ring;
+    const int64_t head_rows = (int64_t)p.pool_rows * D;
+    uint16_t *kc = p.pool + ((int64_t)entry * 2 * p.Hk + hk) * head_rows, *vc = kc + p.Hk * head_rows;
+    const uint16_t *kn = p.k + n * p.k_stride + hk * D, *vn = p.v + n * p.v_stride + hk * D;
+    // element offset of list item i's row in the cache, -1 for the new token
+    auto row_of = [&](int i) -> int64_t {
+        if (i >= count - 1) return -1;             // also past the end: any valid row will do
+        int at = i;                                // a sink
+        if (i >= ns) {
+            const int pp = lo + i - ns;
+            if (pp < p.sinks) at = pp;
+            else {
+                at = ring0 + (pp - wrap0);
+                at = p.sinks + (at >= ring ? at - ring : at);
+            }
+        }
+        return (int64_t)at * D;
+    };
+    if (rank == 0 && group == 0 && threadIdx.x < D / 4) {   // the new rows enter the cache
+        const int64_t at = (int64_t)ring_row(pos, p.sinks, p.pool_rows) * D;
+        const int e = (threadIdx.x & (D / 8 - 1)) * 8;
+        if (threadIdx.x < D / 8) *reinterpret_cast<uint4 *>(kc + at + e) = *reinterpret_cast<const uint4 *>(kn + e);
+        else *reinterpret_cast<uint4 *>(vc + at + e) = *reinterpret_cast<const uint4 *>(vn + e);
+    }
+
+    // q in the order of the key loads: rows g and g + 8, elements 32 kk + 8c .. + 7
+    uint4 qa[D / 32], qb[D / 32];
+    const uint16_t *qp = p.q + n * p.q_stride + (int64_t)head0 * D + 8 * c;
+#pragma unroll
+    for (int kk = 0; kk < D / 32; kk++) {
+        qa[kk] = g < heads ? *reinterpret_cast<const uint4 *>(qp + g * D + 32 * kk) : make_uint4(0, 0, 0, 0);
+        qb[kk] = g + 8 < heads ? *reinterpret_cast<const uint4 *>(qp + (g + 8) * D + 32 * kk) : make_uint4(0, 0, 0, 0);
+    }
+
+    float o[D / 64][8][4];
+#pragma unroll
+    for (int i = 0; i < D / 64; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    uint4 kr[2][D / 32], vr[4][D / 64];
+    auto load_k = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const int64_t r = row_of(i0 + 8 * j + g);
+            const uint16_t *src = (r < 0 ? kn : kc + r) + 8 * c;
+#pragma unroll
+            for (int kk = 0; kk < D / 32; kk++) kr[j][kk] = *reinterpret_cast<const uint4 *>(src + 32 * kk);
+        }
+    };
+    auto load_v = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int64_t r = row_of(i0 + 2 * c + (j & 1) + 8 * (j >> 1));
+            const uint16_t *src = (r < 0 ? vn : vc + r) + 8 * g;
+#pragma unroll
+            for (int hh = 0; hh < D / 64; hh++) vr[j][hh] = *reinterpret_cast<const uint4 *>(src + 64 * hh);
+        }
+    };
+    const int stride = ranks * kWarps * kStep;
+    int i0 = (rank * kWarps + warp) * kStep;
+    if (i0 < count) {
+        load_k(i0);
+        load_v(i0);
+    }
+    for (; i0 < count; i0 += stride) {
+        float s[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < D / 32; kk++) {
+                mma16816<E>(s[j], qa[kk].x, qb[kk].x, qa[kk].y, qb[kk].y, kr[j][kk].x, kr[j][kk].y);
+                mma16816<E>(s[j], qa[kk].z, qb[kk].z, qa[kk].w, qb[kk].w, kr[j][kk].z, kr[j][kk].w);
+            }
+        }
+        const int next = i0 + stride;
+        if (next < count) load_k(next);
+        if (i0 + kStep > count) {
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    if (i0 + 8 * j + 2 * c + e >= count) s[j][e] = s[j][2 + e] = -INFINITY;
+        }
+        float a = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float b = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
+        a = fmaxf(a, m0);
+        b = fmaxf(b, m1);
+        if (__any_sync(0xffffffffu, a > m0 || b > m1)) {
+            // a row whose maximum is still -inf keeps zeros: 2^(-inf - 0) = 0
+            const float f0 = a == -INFINITY ? 1.f : ex2((m0 - a) * p.scale_log2);
+            const float f1 = b == -INFINITY ? 1.f : ex2((m1 - b) * p.scale_log2);
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int i = 0; i < D / 64; i++)
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    o[i][j][0] *= f0;
+                    o[i][j][1] *= f0;
+                    o[i][j][2] *= f1;
+                    o[i][j][3] *= f1;
+                }
+            m0 = a;
+            m1 = b;
+        }
+        const float z0 = m0 == -INFINITY ? 0.f : m0 * p.scale_log2, z1 = m1 == -INFINITY ? 0.f : m1 * p.scale_log2;
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            s[j][0] = ex2(fmaf(s[j][0], p.scale_log2, -z0));
+            s[j][1] = ex2(fmaf(s[j][1], p.scale_log2, -z0));
+            s[j][2] = ex2(fmaf(s[j][2], p.scale_log2, -z1));
+            s[j][3] = ex2(fmaf(s[j][3], p.scale_log2, -z1));
+            l0 += s[j][0] + s[j][1];
+            l1 += s[j][2] + s[j][3];
+        }
+        // probabilities in 16 bits, as the tensor cores take them; their sum stays fp32
+        const uint32_t p0 = Half2<E>::pack(s[0][0], s[0][1]), p1 = Half2<E>::pack(s[0][2], s[0][3]);
+        const uint32_t p2 = Half2<E>::pack(s[1][0], s[1][1]), p3 = Half2<E>::pack(s[1][2], s[1][3]);
+#pragma unroll
+        for (int hh = 0; hh < D / 64; hh++) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+                const uint32_t *r0 = &vr[0][hh].x, *r1 = &vr[1][hh].x, *r2 = &vr[2][hh].x, *r3 = &vr[3][hh].x;
+                mma16816<E>(o[hh][j], p0, p1, p2, p3, __byte_perm(r0[j / 2], r1[j / 2], sel),
+                            __byte_perm(r2[j / 2], r3[j / 2], sel));
+            }
+        }
+        if (next < count) load_v(next);
+    }
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (c == 0) {
+        sm.m[warp][g] = m0;
+        sm.m[warp][g + 8] = m1;
+        sm.l[warp][g] = l0;
+        sm.l[warp][g + 8] = l1;
+    }
+    // column 2c (+1) of the tile (hh, j) is element 64 hh + 16 c (+ 8) + j
+#pragma unroll
+    for (int hh = 0; hh < D / 64; hh++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                float *to = &sm.o[warp][g + 8 * e][64 * hh + 16 * c + 8 * q];
+                float4 x, y;
+                x.x = o[hh][0][2 * e + q]; x.y = o[hh][1][2 * e + q]; x.z = o[hh][2][2 * e + q]; x.w = o[hh][3][2 * e + q];
+                y.x = o[hh][4][2 * e + q]; y.y = o[hh][5][2 * e + q]; y.z = o[hh][6][2 * e + q]; y.w = o[hh][7][2 * e + q];
+                reinterpret_cast<float4 *>(to)[0] = x;
+                reinterpret_cast<float4 *>(to)[1] = y;
+            }
+    __syncthreads();
+    // join the warps: this CTA's maximum, sum and O into part 0 (each element is
+    // read and written by one thread; the factors are read before part 0's are replaced)
+    constexpr int kQuads = D / 4;
+    float mm[kHeads * kQuads / (kWarps * 32)], ll[kHeads * kQuads / (kWarps * 32)];
+#pragma unroll
+    for (int it = 0; it < kHeads * kQuads / (kWarps * 32); it++) {
+        const int e = threadIdx.x + it * kWarps * 32, h = e / kQuads, d4 = e % kQuads;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) m = fmaxf(m, sm.m[w][h]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const float f = m == -INFINITY ? 0.f : ex2((sm.m[w][h] - m) * p.scale_log2);
+            const float4 x = reinterpret_cast<const float4 *>(sm.o[w][h])[d4];
+            l += sm.l[w][h] * f;
+            acc.x += x.x * f;
+            acc.y += x.y * f;
+            acc.z += x.z * f;
+            acc.w += x.w * f;
+        }
+        mm[it] = m;
+        ll[it] = l;
+        reinterpret_cast<float4 *>(sm.o[0][h])[d4] = acc;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < kHeads * kQuads / (kWarps * 32); it++) {
+        const int e = threadIdx.x + it * kWarps * 32;
+        if (e % kQuads == 0) {
+            sm.m[0][e / kQuads] = mm[it];
+            sm.l[0][e / kQuads] = ll[it];
+        }
+    }
+    if (ranks > 1) cluster.sync();
+    else __syncthreads();
+    // join the CTAs: the cluster's threads share the output's elements
+    for (int e = rank * kWarps * 32 + threadIdx.x; e < heads * kQuads; e += ranks * kWarps * 32) {
+        const int h = e / kQuads, d4 = e % kQuads;
+        float m = -INFINITY, l = 0.f;
+        for (int r = 0; r < ranks; r++) m = fmaxf(m, cluster.map_shared_rank(&sm.m[0][h], r)[0]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < ranks; r++) {
+            const float f = m == -INFINITY ? 0.f : ex2((cluster.map_shared_rank(&sm.m[0][h], r)[0] - m) * p.scale_log2);
+            const float4 x = *cluster.map_shared_rank(reinterpret_cast<float4 *>(sm.o[0][h]) + d4, r);
+            l += cluster.map_shared_rank(&sm.l[0][h], r)[0] * f;
+            acc.x += x.x * f;
+            acc.y += x.y * f;
+            acc.z += x.z * f;
+            acc.w += x.w * f;
+        }
+        const float inv = 1.f / l;
+        uint2 r2;
+        r2.x = Half2<E>::pack(acc.x * inv, acc.y * inv);
+        r2.y = Half2<E>::pack(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(p.out + ((int64_t)n * p.Hq + head0 + h) * D + 4 * d4) = r2;
+    }
+    if (ranks > 1) cluster.sync();      // nobody leaves while its shared memory is being read
+}
+
+template <typename E, int D>
+cudaError_t launch(const WindowArgs &a, const DecodeWinParams &p)
+{
+    const int64_t units = (int64_t)p.N * p.Hk * p.groups;
+    int64_t steps = ((int64_t)p.window + p.sinks + kStep - 1) / kStep;   // at most, of one unit
+    if (steps > (p.pool_rows + kStep - 1) / kStep) steps = (p.pool_rows + kStep - 1) / kStep;
+    int ranks = 1;
+    while (ranks < 8 && units * ranks * 2 <= a.num_sms && ranks * kWarps < steps) ranks *= 2;
+    const int smem = sizeof(DecodeSmem<D>);
+    cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * ranks));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, window_decode_kernel<E, D>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+cudaError_t launch_window_decode(const WindowArgs &a)
+{
+    DecodeWinParams p;
+    p.q = (const uint16_t *)a.q; p.k = (const uint16_t *)a.k; p.v = (const uint16_t *)a.v;
+    p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
+    p.positions = a.starts; p.slots = a.slots;
+    p.pool = (uint16_t *)a.pool; p.out = (uint16_t *)a.out;
+    p.N = a.N; p.Hq = a.Hq; p.Hk = a.Hk; p.groups = (a.Hq / a.Hk + kHeads - 1) / kHeads;
+    p.num_slots = a.num_slots; p.pool_rows = a.pool_rows; p.window = a.window; p.sinks = a.sinks;
+    p.scale_log2 = a.scale * kLog2e;
+    p.err = a.err_word;
+    if (a.d == 128) return a.f16 ? launch<__half, 128>(a, p) : launch<__nv_bfloat16, 128>(a, p);
+    return a.f16 ? launch<__half, 64>(a, p) : launch<__nv_bfloat16, 64>(a, p);
+}
+
+}  // namespace kda
