@@ -1,37 +1,103 @@
 // kda_window.cu -- window attention of packed new tokens over the ring cache and
-// themselves (prefill, and the verification of drafts).
+// themselves (prefill, and the verification of drafts), on the tensor cores.
 //
 // For the query at position p:  o = sum_j softmax_j(scale q . k_j) v_j  over the
-// positions j <= p with j > p - window or j < sinks.  One warp takes one (token,
-// query head) and walks the visible keys with a running maximum and sum; keys of
-// positions before the call's come from the cache, the others from the call's
-// rows.  A second kernel then writes the rows that the cache keeps.
+// positions j <= p with j > p - window or j < sinks.  Keys of positions before
+// the call's come from the cache, the others from the call's rows.
+//
+// A CTA takes two tiles of up to 128 query rows of one key head: the G query
+// heads that share it for floor(128 / G) consecutive tokens each, so that each
+// key and value tile serves G heads and a tile spans few positions (little of
+// the window's edges is computed and masked away).  The visible positions are a
+// few runs of consecutive rows (sinks, the ring before and after its wrap, the
+// call's rows), cut into tiles of up to 128 keys.  Per tile and query tile, with
+// S, P and O in TMEM:
+//
+//     S = Q K^T            (tcgen05.mma, both operands in shared memory)
+//     P = 2^(c S - c m)    one thread per query row: 128 scores in registers
+//     O += P V             (P from TMEM in place of S, V MN-major as loaded)
+//
+// The two query tiles take turns on the tensor core: while one's scores are
+// exponentiated, the other's products run.  The maximum m only follows the true
+// one when it falls behind by more than 2^8 (all sums stay in fp32 and the final
+// division makes the result independent of m), so O is rarely rescaled, and the
+// threads that own the rows do it themselves.
+//
+// Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 the TMA
+// loads (a ring of five key / value tiles), warp 9 the MMAs (10 and 11 complete
+// their warpgroup).  A second kernel then writes the rows that the cache keeps.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include "kda_sm100.cuh"
 #include "kda_window.h"
 
 namespace kda {
 namespace {
 
+using namespace sm100;
+
 struct PrefillParams {
-    const uint16_t *q, *k, *v;
-    int64_t q_stride, k_stride, v_stride;
+    const uint16_t *k, *v;           // the call's rows (for the cache kernel)
+    int64_t k_stride, v_stride;
     const int32_t *cu, *starts, *slots;
     uint16_t *pool, *out;
     int N, T, Hq, Hk, num_slots, pool_rows, window, sinks;
+    int G, tile_tokens;              // query heads per key head; tokens of a query tile
     float scale_log2;
     int *err;
 };
 
-// the last sequence that starts at or before row t (the one that holds it, if any does)
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int t)
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;           // keys of a tile
+constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is rounded up to
+constexpr int kStages = 5;
+constexpr int kMaxRuns = 6;
+// Registers: a softmax thread holds a row of 128 scores.  The block starts with
+// kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
+// 384 x 168 (the launch checks that the kernel was built with that number).
+constexpr int kRegs = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegs, "more registers than the block has");
+constexpr float kLag = 8.f;          // log2 of what the running maximum may lag behind
+
+struct Run {
+    int cached;                      // 1: rows of the ring cache, 0: rows of the call
+    int row, pos, len;               // first row, its position, rows
+};
+
+struct Ctl {
+    Run runs[kMaxRuns];
+    int nruns;
+    int n, bos, t0, tokens, first, entry;   // sequence, its first row, the CTA's first row, rows, position of t0
+    int abort;
+    uint32_t tmem;
+    uint64_t bars[2 * kStages + 8];
+};
+
+// TMEM columns
+constexpr int kTmS = 0, kTmO = 256;
+
+__host__ __device__ constexpr uint32_t idesc(int N, int b_mn, bool f16)
 {
-    int a = 0, b = N - 1;
-    while (a < b) {
-        const int c = (a + b + 1) / 2;
-        if (cu[c] <= t) a = c; else b = c - 1;
-    }
-    return a;
+    return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 // positions before the first row of sequence n, which has L rows
@@ -46,69 +112,424 @@ __device__ __forceinline__ int start_of(const PrefillParams &p, int n, int L, bo
     return s;
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(256) window_prefill_kernel(const __grid_constant__ PrefillParams p)
+// The CTAs of a key head are numbered so that sequence n has the numbers from
+// cu[n] / span + n on: at least as many as it has spans of `span` rows, without
+// a pass over the table.  The last sequence whose numbers start at or before s,
+// by one warp, 32 probes at a time.
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int span, int s, int lane)
 {
-    constexpr int kPer = D / 32;     // elements of a lane
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = (int)(w / p.Hq), h = (int)(w % p.Hq);
-    if (t >= p.T) return;
-    const int n = sequence_of(p.cu, p.N, t);
-    const int bos = clamp_row(p.cu[n], p.T, p.err), eos = clamp_row(p.cu[n + 1], p.T, p.err);
-    if (t < bos || t >= eos) return;
-    const bool reports = t == bos && h == 0 && lane == 0;
-    const int entry = entry_of(p.slots, n, p.num_slots, p.err, reports);
-    if (entry < 0) return;
-    const int start = start_of(p, n, eos - bos, reports), pos = start + t - bos;
-    const int hk = h / (p.Hq / p.Hk);
-    const uint16_t *kc = nullptr, *vc = nullptr;
-    if (p.pool) {
-        kc = p.pool + ((int64_t)entry * 2 * p.Hk + hk) * p.pool_rows * D;
-        vc = kc + (int64_t)p.Hk * p.pool_rows * D;
+    int a = 0, n = N;                // the answer is in [a, a + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = a + lane * step;
+        const bool le = lane * step < n && cu[at] / span + at <= s;
+        const uint32_t votes = __ballot_sync(0xffffffffu, le || lane == 0);
+        const int last = 31 - __clz(votes);
+        n = min(step, n - last * step);
+        a += last * step;
     }
-    float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-    auto load = [&](const uint16_t *src, float (&x)[kPer]) {
-        const uint32_t *s = reinterpret_cast<const uint32_t *>(src) + lane * (kPer / 2);
-#pragma unroll
-        for (int i = 0; i < kPer / 2; i++) {
-            const float2 f = Half2<E>::unpack(s[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+    return a;
+}
+
+// runs of consecutive rows that hold the positions [a, b) of the sequence
+__device__ __forceinline__ void add_runs(Ctl &c, const PrefillParams &p, int start, int a, int b)
+{
+    auto add = [&](int cached, int row, int pos, int len) {
+        if (len > 0) c.runs[c.nruns++] = {cached, row, pos, len};
     };
-    load(p.q + t * p.q_stride + (int64_t)h * D, q);
-#pragma unroll
-    for (int i = 0; i < kPer; i++) o[i] = 0.f;
-    const int lo = pos - p.window + 1 < 0 ? 0 : pos - p.window + 1, ns = min(p.sinks, lo);
-    for (int64_t i = 0; i < (int64_t)ns + (pos - lo) + 1; i++) {
-        const int j = i < ns ? (int)i : lo + (int)(i - ns);
-        const uint16_t *kr, *vr;
-        if (j >= start) {
-            kr = p.k + (bos + j - start) * p.k_stride + hk * D;
-            vr = p.v + (bos + j - start) * p.v_stride + hk * D;
+    const int end = min(b, start);   // of the cached part
+    if (a < end) {
+        const int ring = p.pool_rows - p.sinks;
+        if (end <= p.pool_rows) {
+            add(1, a, a, end - a);   // nothing has wrapped: row = position
         } else {
-            const int64_t r = (int64_t)ring_row(j, p.sinks, p.pool_rows) * D;
-            kr = kc + r;
-            vr = vc + r;
+            const int cut = min(end, max(a, p.sinks));
+            add(1, a, a, cut - a);
+            if (cut < end) {
+                const int at = (cut - p.sinks) % ring, len = min(end - cut, ring - at);
+                add(1, p.sinks + at, cut, len);
+                add(1, p.sinks, cut + len, end - cut - len);
+            }
         }
-        float x[kPer], s = 0.f;
-        load(kr, x);
-#pragma unroll
-        for (int e = 0; e < kPer; e++) s = fmaf(q[e], x[e], s);
-#pragma unroll
-        for (int b = 16; b; b /= 2) s += __shfl_xor_sync(0xffffffffu, s, b);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), f = mn == -INFINITY ? 1.f : ex2(m - mn), e = mn == -INFINITY ? 0.f : ex2(s - mn);
-        m = mn;
-        l = l * f + e;
-        load(vr, x);
-#pragma unroll
-        for (int k = 0; k < kPer; k++) o[k] = o[k] * f + e * x[k];
     }
-    uint32_t *to = reinterpret_cast<uint32_t *>(p.out + ((int64_t)t * p.Hq + h) * D) + lane * (kPer / 2);
+    const int from = max(a, start);
+    add(0, c.bos + from - start, from, b - from);
+}
+
+// walks the tiles of the runs
+struct Tiles {
+    const Ctl &c;
+    int run = 0, off = 0;
+    int cached, row, pos, count;
+    __device__ explicit Tiles(const Ctl &ctl) : c(ctl) {}
+    __device__ bool next()
+    {
+        if (run >= c.nruns) return false;
+        const Run &r = c.runs[run];
+        cached = r.cached;
+        row = r.row + off;
+        pos = r.pos + off;
+        count = min(kKeys, r.len - off);
+        off += count;
+        if (off >= r.len) {
+            run++;
+            off = 0;
+        }
+        return true;
+    }
+};
+
+// whether any of the positions [first, last] sees any key of the tile
+__device__ __forceinline__ bool sees(const Tiles &t, int first, int last, int window, int sinks)
+{
+    return first <= last && t.pos <= last && (t.pos + t.count - 1 > first - window || t.pos < sinks);
+}
+
+template <typename E, int D> struct Layout {
+    static constexpr int kTile = 128 * D * 2;            // bytes of a query, key or value tile
+    static constexpr int kHalf = 128 * 128;              // bytes of its 64 leftmost columns
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTile + sizeof(Ctl);
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mpool,
+                      const __grid_constant__ PrefillParams p)
+{
+    using L = Layout<E, D>;
+    constexpr bool kF16 = sizeof(E) == 2 && !__is_same(E, __nv_bfloat16);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *aligned = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t sq = base, skv = base + 2 * L::kTile;
+    Ctl &c = *reinterpret_cast<Ctl *>(aligned + (2 + kStages) * L::kTile);
+    const uint32_t bars = smem_u32(c.bars);
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    const uint32_t q_full = bars + 8 * (2 * kStages);
+    auto s_full = [&](int t) { return bars + 8 * (2 * kStages + 1 + t); };
+    auto p_ready = [&](int t) { return bars + 8 * (2 * kStages + 3 + t); };
+    auto o_done = [&](int t) { return bars + 8 * (2 * kStages + 5 + t); };
+    const uint32_t drained = bars + 8 * (2 * kStages + 7);
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int hk = blockIdx.x % p.Hk, slot = gridDim.x / p.Hk - 1 - blockIdx.x / p.Hk;   // late positions first
+    const int span = 2 * p.tile_tokens;
+    if (warp == 8) {
+        const int n = sequence_of(p.cu, p.N, span, slot, lane);
+        if (lane == 0) {
+            const int bos = clamp_row(p.cu[n], p.T, p.err), eos = clamp_row(p.cu[n + 1], p.T, p.err);
+            const int i = slot - (p.cu[n] / span + n);
+            const bool reports = i == 0 && hk == 0;
+            const int len = max(0, eos - bos);
+            const int start = start_of(p, n, len, reports);
+            c.entry = entry_of(p.slots, n, p.num_slots, p.err, reports);
+            c.nruns = 0;
+            c.abort = 0;
+            c.bos = bos;
+            // rows at or past the end: nothing to do
+            c.tokens = i < 0 || (int64_t)i * span >= len || c.entry < 0 ? 0 : min(span, len - i * span);
+            if (c.tokens) {
+                c.t0 = bos + i * span;
+                c.first = start + i * span;
+                const int last = c.first + c.tokens - 1;
+                const int lo = max(0, c.first - p.window + 1);
+                if (lo > p.sinks) {
+                    add_runs(c, p, start, 0, p.sinks);
+                    add_runs(c, p, start, lo, last + 1);
+                } else {
+                    add_runs(c, p, start, 0, last + 1);
+                }
+            }
+            for (int s = 0; s < kStages; s++) {
+                mbar_init(full(s), 1);
+                mbar_init(empty(s), 1);
+            }
+            mbar_init(q_full, 1);
+            for (int t = 0; t < 2; t++) {
+                mbar_init(s_full(t), 1);
+                mbar_init(p_ready(t), 4);
+                mbar_init(o_done(t), 1);
+            }
+            mbar_init(drained, 1);
+            mbar_fence_init();
+        }
+    }
+    __syncthreads();
+    if (c.tokens == 0) return;
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&c.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    volatile int *abort = &c.abort;
+    auto give_up = [&]() {
+        atomicOr(p.err, kErrWaitTimeout);
+        *abort = 1;
+    };
+    // positions of the two query tiles
+    const int tokens0 = min(p.tile_tokens, c.tokens), tokens1 = c.tokens - tokens0;
+    const int first0 = c.first, last0 = first0 + tokens0 - 1;
+    const int first1 = tokens1 > 0 ? first0 + p.tile_tokens : 1, last1 = tokens1 > 0 ? first1 + tokens1 - 1 : 0;
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) {                                     // ---- loads
+        if (lane == 0) {
+            const int box = p.G * p.tile_tokens * 128;   // bytes of half a query tile
+            mbar_arrive_expect_tx(q_full, (uint32_t)(box * (D / 64) * (tokens1 > 0 ? 2 : 1)));
+            for (int t = 0; t < (tokens1 > 0 ? 2 : 1); t++)
+                for (int h = 0; h < D / 64; h++)
+                    tma_load_3d(sq + t * L::kTile + h * L::kHalf, &mq, 64 * h, hk * p.G, c.t0 + t * p.tile_tokens, q_full);
+            int it = 0;
+            bool ok = true;
+            Tiles t(c);
+            while (ok && t.next()) {
+                const int boxes = (t.count + kBox - 1) / kBox;
+                for (int kv = 0; kv < 2 && ok; kv++, it++) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait(empty(s), (it / kStages - 1) & 1, abort)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full(s), (uint32_t)(boxes * kBox * 128 * (D / 64)));
+                    const uint32_t to = skv + s * L::kTile;
+                    for (int h = 0; h < D / 64; h++)
+                        for (int b = 0; b < boxes; b++) {
+                            const uint32_t dst = to + h * L::kHalf + b * (kBox * 128);
+                            if (t.cached)
+                                tma_load_3d(dst, &mpool, 64 * h, t.row + b * kBox, (c.entry * 2 + kv) * p.Hk + hk, full(s));
+                            else
+                                tma_load_3d(dst, kv ? &mv : &mk, 64 * h, hk, t.row + b * kBox, full(s));
+                        }
+                }
+            }
+            // nothing may still be on its way into shared memory when the CTA ends
+            mbar_wait_drain(q_full, 0);
+            for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(full(i % kStages), (i / kStages) & 1);
+        }
+    } else if (warp == 9) {                              // ---- products
+        int it = 0, done[2] = {0, 0};                    // loads consumed; products O += P V issued per query tile
+        bool ok = mbar_wait(q_full, 0, abort);
+        Tiles t(c);
+        auto scores = [&](int q, int s, int keys) {      // S of query tile q from the key tile in stage s
+            if (lane == 0) {
+                const uint32_t id = idesc(keys, 0, kF16);
 #pragma unroll
-    for (int i = 0; i < kPer / 2; i++) to[i] = Half2<E>::pack(o[2 * i] / l, o[2 * i + 1] / l);
+                for (int k = 0; k < D / 16; k++) {
+                    const uint32_t at = (k / 4) * L::kHalf + (k % 4) * 32;
+                    mma_ss(tmem + kTmS + 128 * q, smem_desc_sw128(sq + q * L::kTile + at, 16, 1024),
+                           smem_desc_sw128(skv + s * L::kTile + at, 16, 1024), id, k > 0);
+                }
+                mma_commit(s_full(q));
+            }
+        };
+        auto release = [&](int s) {
+            if (lane == 0) mma_commit(empty(s));
+        };
+        bool have = ok && t.next();
+        bool now[2] = {false, false};
+        int keys = 0, count = 0;
+        if (have) {
+            ok = mbar_wait(full(0), 0, abort);
+            tc_fence_after();
+            count = t.count;
+            keys = (count + 15) & ~15;
+            now[0] = sees(t, first0, last0, p.window, p.sinks);
+            now[1] = sees(t, first1, last1, p.window, p.sinks);
+            for (int q = 0; q < 2 && ok; q++)
+                if (now[q]) scores(q, 0, keys);
+            release(0);
+            it = 1;
+        }
+        while (have && ok) {
+            const int sv = it % kStages;                 // this tile's values
+            ok = mbar_wait(full(sv), (it / kStages) & 1, abort);
+            if (!ok) break;
+            it++;
+            if (count < keys) {
+                // value rows past the run hold anything (0 x NaN is NaN): zeros
+                for (int e = lane; e < (keys - count) * (D / 8); e += 32) {
+                    const int r = count + e / (D / 8), v = e % (D / 8);
+                    *reinterpret_cast<uint4 *>(aligned + (2 + sv) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after();
+            const bool was[2] = {now[0], now[1]};
+            const int steps = keys / 16, sk = it % kStages;
+            have = t.next();
+            if (have) {
+                count = t.count;
+                keys = (count + 15) & ~15;
+                now[0] = sees(t, first0, last0, p.window, p.sinks);
+                now[1] = sees(t, first1, last1, p.window, p.sinks);
+            }
+            bool key_here = false;
+            for (int q = 0; q < 2 && ok; q++) {
+                if (was[q]) {
+                    ok = mbar_wait(p_ready(q), done[q] & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t id = idesc(D, 1, kF16);
+                        for (int k = 0; k < steps; k++)
+                            mma_ts(tmem + kTmO + 128 * q, tmem + kTmS + 128 * q + 8 * k,
+                                   smem_desc_sw128(skv + sv * L::kTile + k * 2048, L::kHalf, 1024), id,
+                                   done[q] > 0 || k > 0);
+                        mma_commit(o_done(q));
+                    }
+                    done[q]++;
+                }
+                if (q == 1) release(sv);
+                if (have && now[q]) {
+                    if (!key_here) {
+                        ok = mbar_wait(full(sk), (it / kStages) & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        key_here = true;
+                    }
+                    scores(q, sk, keys);
+                }
+            }
+            if (have && ok) {
+                if (!key_here) {                         // no query tile sees it: still consumed
+                    ok = mbar_wait(full(sk), (it / kStages) & 1, abort);
+                }
+                release(sk);
+                it++;
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        // every product is finished before the TMEM and shared memory go
+        if (lane == 0) mma_commit(drained);
+        mbar_wait_drain(drained, 0);
+    }
+    } else {                                             // ---- softmax, one thread per query row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int q = warp >> 2, row = threadIdx.x & 127;
+        const int first = q ? first1 : first0, last = q ? last1 : last0, tokens = q ? tokens1 : tokens0;
+        const int token = row / p.G, pos = first + token;
+        const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + kTmS + 128 * q;
+        const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kTmO + 128 * q;
+        const float c2 = p.scale_log2;
+        float m = -INFINITY, sum = 0.f;
+        int it = 0;
+        bool ok = true;
+        Tiles t(c);
+        while (ok && t.next()) {
+            if (!sees(t, first, last, p.window, p.sinks)) continue;
+            ok = mbar_wait(s_full(q), it & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const int chunks = (t.count + 31) / 32;
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (i < chunks) tmem_ld32(ts + 32 * i, s[i]);
+            tmem_wait_ld();
+            // every key of the tile visible to every row: no test per key
+            const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= first &&
+                               (t.pos > last - p.window || t.pos + kKeys <= p.sinks);
+            if (!whole) {
+                const int hi = min(pos - t.pos, t.count - 1);        // last visible column
+                const int lo = max(pos - p.window, -1) - t.pos;      // columns up to here are behind the window
+                const int sk = p.sinks - t.pos;                      // unless they are sinks
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        const int col = 32 * i + j;
+                        if (col > hi || (col <= lo && col >= sk)) s[i][j] = 0xff800000u;   // -inf
+                    }
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                for (int j = 1; j < 32; j++) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][j]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool behind = m != -INFINITY && (top - m) * c2 > kLag;
+            if (__any_sync(0xffffffffu, behind)) {
+                // O of the products so far is complete and the next one waits for this warp
+                ok = mbar_wait(o_done(q), (it - 1) & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                const float f = behind ? ex2((m - top) * c2) : 1.f;
+                for (int i = 0; i < D / 32; i++) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * i, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st32(to + 32 * i, o);
+                }
+                tmem_wait_st();
+                sum *= f;
+                if (behind) m = top;
+            }
+            if (m == -INFINITY) m = top;                 // the row's first visible keys: its O is still zero
+            const float z = m == -INFINITY ? 0.f : -m * c2;
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (i < chunks) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        float2 e = fma2(make_float2(__uint_as_float(s[i][2 * j]), __uint_as_float(s[i][2 * j + 1])),
+                                        make_float2(c2, c2), make_float2(z, z));
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        part[j & 1] = add2(part[j & 1], e);
+                        w[j] = Half2<E>::pack(e.x, e.y);
+                    }
+                    tmem_st16(ts + 16 * i, w);
+                }
+            }
+            sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_ready(q));
+            it++;
+        }
+        if (ok && it > 0) ok = mbar_wait(o_done(q), (it - 1) & 1, abort);
+        if (!ok) give_up();
+        tc_fence_after();
+        if (ok && it > 0) {
+            const float inv = 1.f / sum;
+            const bool live = token < tokens && row < p.tile_tokens * p.G;
+            uint16_t *o = p.out + ((int64_t)(c.t0 + q * p.tile_tokens + token) * p.Hq + hk * p.G + row % p.G) * D;
+            for (int i = 0; i < D / 32; i++) {
+                uint32_t x[32];
+                tmem_ld32(to + 32 * i, x);
+                tmem_wait_ld();
+                if (live)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        uint4 r;
+                        r.x = Half2<E>::pack(__uint_as_float(x[8 * j]) * inv, __uint_as_float(x[8 * j + 1]) * inv);
+                        r.y = Half2<E>::pack(__uint_as_float(x[8 * j + 2]) * inv, __uint_as_float(x[8 * j + 3]) * inv);
+                        r.z = Half2<E>::pack(__uint_as_float(x[8 * j + 4]) * inv, __uint_as_float(x[8 * j + 5]) * inv);
+                        r.w = Half2<E>::pack(__uint_as_float(x[8 * j + 6]) * inv, __uint_as_float(x[8 * j + 7]) * inv);
+                        reinterpret_cast<uint4 *>(o + 32 * i)[j] = r;
+                    }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
 // Writes the rows that the cache keeps: sinks, and the sequence's last pool_rows
@@ -120,7 +541,11 @@ __global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant_
     const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int t = (int)(w / per), e = (int)(w % per);
     if (t >= p.T) return;
-    const int n = sequence_of(p.cu, p.N, t);
+    int n = 0;                       // the last sequence that starts at or before row t
+    for (int b = p.N - 1; n < b;) {
+        const int m = (n + b + 1) / 2;
+        if (p.cu[m] <= t) n = m; else b = m - 1;
+    }
     const int bos = clamp_row(p.cu[n], p.T, nullptr), eos = clamp_row(p.cu[n + 1], p.T, nullptr);
     if (t < bos || t >= eos) return;
     const int entry = entry_of(p.slots, n, p.num_slots, nullptr, false);
@@ -135,12 +560,58 @@ __global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant_
     *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + hk * D + at);
 }
 
+// The driver's tensor-map encoder, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess && q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// a dense innermost axis of d elements, two more with the given extents and
+// strides (elements); boxes of 64 x b1 x b2, 128-byte swizzled
+bool make_map(CUtensorMap *m, const void *base, bool f16, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int b1,
+              int b2)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2}, es[3] = {1, 1, 1};
+    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename E, int D>
 cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
 {
-    window_prefill_kernel<E, D><<<(unsigned)(((int64_t)p.T * p.Hq + 7) / 8), 256, 0, a.stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !p.pool) return e;
+    CUtensorMap mq, mk, mv, mpool;
+    if (!make_map(&mq, a.q, a.f16, D, a.Hq, D, a.T, a.q_stride, p.G, p.tile_tokens) ||
+        !make_map(&mk, a.k, a.f16, D, a.Hk, D, a.T, a.k_stride, 1, kBox) ||
+        !make_map(&mv, a.v, a.f16, D, a.Hk, D, a.T, a.v_stride, 1, kBox))
+        return cudaErrorInvalidValue;
+    if (!a.pool) mpool = mk;         // never used: no position is before the call's
+    else if (!make_map(&mpool, a.pool, a.f16, D, a.pool_rows, D, (int64_t)a.num_slots * 2 * a.Hk, (int64_t)a.pool_rows * D,
+                       kBox, 1))
+        return cudaErrorInvalidValue;
+    const int smem = Layout<E, D>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes built;
+    if ((e = cudaFuncGetAttributes(&built, window_prefill_kernel<E, D>)) != cudaSuccess) return e;
+    if (built.numRegs != kRegs) return cudaErrorInvalidConfiguration;
+    const int64_t blocks = ((int64_t)a.T / (2 * p.tile_tokens) + a.N) * a.Hk;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    window_prefill_kernel<E, D><<<(unsigned)blocks, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !a.pool) return e;
     ring_commit_kernel<D><<<(unsigned)(((int64_t)p.T * p.Hk * (D / 8) + 255) / 256), 256, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
@@ -150,12 +621,14 @@ cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
 cudaError_t launch_window_prefill(const WindowArgs &a)
 {
     PrefillParams p;
-    p.q = (const uint16_t *)a.q; p.k = (const uint16_t *)a.k; p.v = (const uint16_t *)a.v;
-    p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
+    p.k = (const uint16_t *)a.k; p.v = (const uint16_t *)a.v;
+    p.k_stride = a.k_stride; p.v_stride = a.v_stride;
     p.cu = a.cu_seqlens; p.starts = a.starts; p.slots = a.slots;
     p.pool = (uint16_t *)a.pool; p.out = (uint16_t *)a.out;
     p.N = a.N; p.T = a.T; p.Hq = a.Hq; p.Hk = a.Hk; p.num_slots = a.num_slots; p.pool_rows = a.pool_rows;
     p.window = a.window; p.sinks = a.sinks;
+    p.G = a.Hq / a.Hk;
+    p.tile_tokens = 128 / p.G;
     p.scale_log2 = a.scale * kLog2e;
     p.err = a.err_word;
     if (a.d == 128) return a.f16 ? launch<__half, 128>(a, p) : launch<__nv_bfloat16, 128>(a, p);
