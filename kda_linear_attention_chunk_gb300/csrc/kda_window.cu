@@ -24,8 +24,8 @@
 // threads that own the rows do it themselves.
 //
 // Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 the TMA
-// loads (a ring of five key / value tiles), warp 9 the MMAs (10 and 11 complete
-// their warpgroup).  A second kernel then writes the rows that the cache keeps.
+// loads (a ring of five key / value tiles), warp 9 the MMAs, warp 10 the zeros
+// behind ragged value tiles (11 completes the warpgroup).  A second kernel then writes the rows that the cache keeps.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <stdint.h>
@@ -52,7 +52,7 @@ struct PrefillParams {
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is rounded up to
-constexpr int kStages = 5;
+constexpr int kStages = 5;           // odd: a stage holds keys and values in turn
 constexpr int kMaxRuns = 6;
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
@@ -72,7 +72,7 @@ struct Ctl {
     int n, bos, t0, tokens, first, entry;   // sequence, its first row, the CTA's first row, rows, position of t0
     int abort;
     uint32_t tmem;
-    uint64_t bars[2 * kStages + 8];
+    uint64_t bars[3 * kStages + 11];
 };
 
 // TMEM columns
@@ -82,6 +82,60 @@ __host__ __device__ constexpr uint32_t idesc(int N, int b_mn, bool f16)
 {
     return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Upper halves of the matrix descriptors (8-row groups 1024 bytes apart, version
+// 1, 128-byte swizzle); a lower half is the address / 16 and the leading offset.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void mma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc),
+                 "r"(kDescHi)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc),
+                 "r"(kDescHi)
+                 : "memory");
+}
+
+// One lane of the (converged) warp, the same every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(yes));
+    return yes != 0;
+}
+
+// S = Q K^T: both operands K-major, halves of 64 columns 16 KB apart
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t s, uint32_t q, uint32_t k, uint32_t id)
+{
+    const uint32_t a = (q >> 4) | (1u << 16), b = (k >> 4) | (1u << 16);
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) {
+        const uint32_t at = (i / 4) * 1024 + (i % 4) * 2;
+        mma_ss_lo(s, a + at, b + at, id, i > 0);
+    }
+}
+
+// O += P V for the four 16-key steps from `from` on: P in TMEM, V MN-major, 16
+// keys are 2048 bytes of it
+template <int D>
+__device__ __forceinline__ void mma_values(uint32_t o, uint32_t pt, uint32_t v, uint32_t id, int from, int steps, bool more)
+{
+    const uint32_t b = (v >> 4) | (1024u << 16);
+    if (steps >= from + 4) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) mma_ts_lo(o, pt + 8 * (from + i), b + 128 * (from + i), id, i > 0 ? 1 : more);
+    } else {
+#pragma unroll 1
+        for (int i = from; i < steps; i++) mma_ts_lo(o, pt + 8 * i, b + 128 * i, id, i > from || more);
+    }
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
@@ -98,6 +152,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+// Waits for the TMEM loads, as seen by whatever uses these registers.
+__device__ __forceinline__ void loaded(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t (&c)[32], uint32_t (&d)[32])
+{
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; i++) asm volatile("" : "+r"(a[i]), "+r"(b[i]), "+r"(c[i]), "+r"(d[i]));
 }
 
 // positions before the first row of sequence n, which has L rows
@@ -210,7 +272,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     auto s_full = [&](int t) { return bars + 8 * (2 * kStages + 1 + t); };
     auto p_ready = [&](int t) { return bars + 8 * (2 * kStages + 3 + t); };
     auto o_done = [&](int t) { return bars + 8 * (2 * kStages + 5 + t); };
-    const uint32_t drained = bars + 8 * (2 * kStages + 7);
+    auto p_half = [&](int t) { return bars + 8 * (2 * kStages + 7 + t); };
+    auto turn = [&](int t) { return bars + 8 * (2 * kStages + 9 + t); };
+    auto values = [&](int s) { return bars + 8 * (2 * kStages + 11 + s); };
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hk = blockIdx.x % p.Hk, slot = gridDim.x / p.Hk - 1 - blockIdx.x / p.Hk;   // late positions first
@@ -243,15 +307,17 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             }
             for (int s = 0; s < kStages; s++) {
                 mbar_init(full(s), 1);
-                mbar_init(empty(s), 1);
+                mbar_init(empty(s), 2);
+                mbar_init(values(s), 1);
             }
             mbar_init(q_full, 1);
             for (int t = 0; t < 2; t++) {
                 mbar_init(s_full(t), 1);
                 mbar_init(p_ready(t), 4);
+                mbar_init(p_half(t), 4);
+                mbar_init(turn(t), 1);
                 mbar_init(o_done(t), 1);
             }
-            mbar_init(drained, 1);
             mbar_fence_init();
         }
     }
@@ -278,138 +344,140 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {                                     // ---- loads
-        if (lane == 0) {
-            const int box = p.G * p.tile_tokens * 128;   // bytes of half a query tile
-            mbar_arrive_expect_tx(q_full, (uint32_t)(box * (D / 64) * (tokens1 > 0 ? 2 : 1)));
-            for (int t = 0; t < (tokens1 > 0 ? 2 : 1); t++)
+        const int nq = __shfl_sync(0xffffffffu, tokens1 > 0 ? 2 : 1, 0), t0 = __shfl_sync(0xffffffffu, c.t0, 0);
+        const int entry_head = __shfl_sync(0xffffffffu, c.entry, 0) * 2 * p.Hk + hk;
+        if (elect_one()) {
+            // half a query tile is G tile_tokens rows of 128 bytes
+            mbar_arrive_expect_tx(q_full, (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64) * nq));
+            for (int t = 0; t < nq; t++)
                 for (int h = 0; h < D / 64; h++)
-                    tma_load_3d(sq + t * L::kTile + h * L::kHalf, &mq, 64 * h, hk * p.G, c.t0 + t * p.tile_tokens, q_full);
-            int it = 0;
-            bool ok = true;
-            Tiles t(c);
-            while (ok && t.next()) {
-                const int boxes = (t.count + kBox - 1) / kBox;
-                for (int kv = 0; kv < 2 && ok; kv++, it++) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait(empty(s), (it / kStages - 1) & 1, abort)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
+                    tma_load_3d(sq + t * L::kTile + h * L::kHalf, &mq, 64 * h, hk * p.G, t0 + t * p.tile_tokens, q_full);
+        }
+        int it = 0;
+        bool ok = true;
+        Tiles t(c);
+        while (ok && __shfl_sync(0xffffffffu, t.next(), 0)) {
+            const int boxes = __shfl_sync(0xffffffffu, (t.count + kBox - 1) / kBox, 0);
+            const int row = __shfl_sync(0xffffffffu, t.row, 0);
+            const bool cached = __shfl_sync(0xffffffffu, t.cached, 0);
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                const int s = it % kStages;
+                if (ok && it >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(empty(s), (it / kStages - 1) & 1, abort));
+                if (!ok) break;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(full(s), (uint32_t)(boxes * kBox * 128 * (D / 64)));
                     const uint32_t to = skv + s * L::kTile;
-                    for (int h = 0; h < D / 64; h++)
-                        for (int b = 0; b < boxes; b++) {
-                            const uint32_t dst = to + h * L::kHalf + b * (kBox * 128);
-                            if (t.cached)
-                                tma_load_3d(dst, &mpool, 64 * h, t.row + b * kBox, (c.entry * 2 + kv) * p.Hk + hk, full(s));
-                            else
-                                tma_load_3d(dst, kv ? &mv : &mk, 64 * h, hk, t.row + b * kBox, full(s));
-                        }
-                }
-            }
-            // nothing may still be on its way into shared memory when the CTA ends
-            mbar_wait_drain(q_full, 0);
-            for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(full(i % kStages), (i / kStages) & 1);
-        }
-    } else if (warp == 9) {                              // ---- products
-        int it = 0, done[2] = {0, 0};                    // loads consumed; products O += P V issued per query tile
-        bool ok = mbar_wait(q_full, 0, abort);
-        Tiles t(c);
-        auto scores = [&](int q, int s, int keys) {      // S of query tile q from the key tile in stage s
-            if (lane == 0) {
-                const uint32_t id = idesc(keys, 0, kF16);
+                    if (cached) {
+                        for (int b = 0; b < boxes; b++)
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint32_t at = (k / 4) * L::kHalf + (k % 4) * 32;
-                    mma_ss(tmem + kTmS + 128 * q, smem_desc_sw128(sq + q * L::kTile + at, 16, 1024),
-                           smem_desc_sw128(skv + s * L::kTile + at, 16, 1024), id, k > 0);
+                            for (int h = 0; h < D / 64; h++)
+                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), &mpool, 64 * h, row + b * kBox,
+                                            entry_head + kv * p.Hk, full(s));
+                    } else {
+                        for (int b = 0; b < boxes; b++)
+#pragma unroll
+                            for (int h = 0; h < D / 64; h++)
+                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), kv ? &mv : &mk, 64 * h, hk,
+                                            row + b * kBox, full(s));
+                    }
                 }
+                it++;
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        // nothing may still be on its way into shared memory when the CTA ends
+        mbar_wait_drain(q_full, 0);
+        for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(full(i % kStages), (i / kStages) & 1);
+    } else if (warp == 9 || warp == 11) {                // ---- products of one query tile
+        // The whole warp walks the loop and one elected lane issues: operands that are
+        // uniform over the warp stay in uniform registers, where the instruction takes
+        // them (85 cycles an MMA from a loop that one lane runs alone).
+        const int q = __shfl_sync(0xffffffffu, warp == 11, 0);
+        const int first = q ? first1 : first0, last = q ? last1 : last0;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q, qs = sq + q * L::kTile;
+        auto wait = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort)) != 0; };
+        // The query tiles take turns, so that one's scores are exponentiated during
+        // the other's products: left alone they fall into step (4100 cycles a tile of
+        // keys instead of 3600).
+        const bool both = __shfl_sync(0xffffffffu, tokens1 > 0, 0);
+        int it = 1, done = 0, round = 0;                 // loads consumed; products O += P V issued; tiles
+        Tiles t(c);
+        bool have = t.next(), now = __shfl_sync(0xffffffffu, sees(t, first, last, p.window, p.sinks), 0);
+        int count = __shfl_sync(0xffffffffu, t.count, 0);
+        bool ok = wait(q_full, 0) && wait(full(0), 0);
+        if (elect_one()) {
+            if (ok && now) {
+                mma_scores<D>(ts, qs, skv, idesc((count + 15) & ~15, 0, kF16));
                 mma_commit(s_full(q));
             }
-        };
-        auto release = [&](int s) {
-            if (lane == 0) mma_commit(empty(s));
-        };
-        bool have = ok && t.next();
-        bool now[2] = {false, false};
-        int keys = 0, count = 0;
-        if (have) {
-            ok = mbar_wait(full(0), 0, abort);
-            tc_fence_after();
-            count = t.count;
-            keys = (count + 15) & ~15;
-            now[0] = sees(t, first0, last0, p.window, p.sinks);
-            now[1] = sees(t, first1, last1, p.window, p.sinks);
-            for (int q = 0; q < 2 && ok; q++)
-                if (now[q]) scores(q, 0, keys);
-            release(0);
-            it = 1;
+            mma_commit(empty(0));
         }
         while (have && ok) {
-            const int sv = it % kStages;                 // this tile's values
-            ok = mbar_wait(full(sv), (it / kStages) & 1, abort);
-            if (!ok) break;
+            const int sv = it % kStages, steps = (count + 15) / 16;   // this tile's values
+            const bool was = now;
+            ok = wait(values(sv), it / (2 * kStages));
             it++;
-            if (count < keys) {
-                // value rows past the run hold anything (0 x NaN is NaN): zeros
-                for (int e = lane; e < (keys - count) * (D / 8); e += 32) {
-                    const int r = count + e / (D / 8), v = e % (D / 8);
-                    *reinterpret_cast<uint4 *>(aligned + (2 + sv) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
+            const int sk = it % kStages;                 // the next tile's keys
+            have = __shfl_sync(0xffffffffu, t.next(), 0);
+            if (have) {
+                now = __shfl_sync(0xffffffffu, sees(t, first, last, p.window, p.sinks), 0);
+                count = __shfl_sync(0xffffffffu, t.count, 0);
+                ok = ok && wait(full(sk), it / kStages);
+                it++;
+            }
+            if (both && ok && (q || round)) ok = wait(turn(q), q ? round : round - 1);
+            if (ok && was) {
+                ok = wait(p_half(q), done);
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, kF16), 0, steps, done > 0);
+                    ok = wait(p_ready(q), done);
+                }
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, kF16), 4, steps, true);
+                    done++;
+                }
+            }
+            if (elect_one()) {
+                if (ok && have && now) {
+                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc((count + 15) & ~15, 0, kF16));
+                    mma_commit(s_full(q));
+                }
+                if (both) mbar_arrive(turn(!q));
+                mma_commit(empty(sv));
+                if (have) mma_commit(empty(sk));
+            }
+            round++;
+        }
+        if (!ok && lane == 0) give_up();
+        // every product is finished before O is read, and before the TMEM and shared memory go
+        if (elect_one()) mma_commit(o_done(q));
+        mbar_wait_drain(o_done(q), 0);
+    } else if (warp == 10) {                             // ---- zeros behind ragged runs
+        // Value rows past a run hold anything, and 0 x NaN is NaN: the rows that the
+        // last 16 keys of its tile are rounded up to become zeros.  Every value tile
+        // passes through here (in an odd ring a stage holds keys and values in turn).
+        Tiles t(c);
+        bool ok = true;
+        for (int it = 1; ok && t.next(); it += 2) {
+            const int s = it % kStages;
+            ok = mbar_wait(full(s), (it / kStages) & 1, abort);
+            if (!ok) break;
+            if (t.count & 15) {
+                for (int e = lane; e < (16 - (t.count & 15)) * (D / 8); e += 32) {
+                    const int r = t.count + e / (D / 8), v = e % (D / 8);
+                    *reinterpret_cast<uint4 *>(aligned + (2 + s) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            tc_fence_after();
-            const bool was[2] = {now[0], now[1]};
-            const int steps = keys / 16, sk = it % kStages;
-            have = t.next();
-            if (have) {
-                count = t.count;
-                keys = (count + 15) & ~15;
-                now[0] = sees(t, first0, last0, p.window, p.sinks);
-                now[1] = sees(t, first1, last1, p.window, p.sinks);
-            }
-            bool key_here = false;
-            for (int q = 0; q < 2 && ok; q++) {
-                if (was[q]) {
-                    ok = mbar_wait(p_ready(q), done[q] & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t id = idesc(D, 1, kF16);
-                        for (int k = 0; k < steps; k++)
-                            mma_ts(tmem + kTmO + 128 * q, tmem + kTmS + 128 * q + 8 * k,
-                                   smem_desc_sw128(skv + sv * L::kTile + k * 2048, L::kHalf, 1024), id,
-                                   done[q] > 0 || k > 0);
-                        mma_commit(o_done(q));
-                    }
-                    done[q]++;
-                }
-                if (q == 1) release(sv);
-                if (have && now[q]) {
-                    if (!key_here) {
-                        ok = mbar_wait(full(sk), (it / kStages) & 1, abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        key_here = true;
-                    }
-                    scores(q, sk, keys);
-                }
-            }
-            if (have && ok) {
-                if (!key_here) {                         // no query tile sees it: still consumed
-                    ok = mbar_wait(full(sk), (it / kStages) & 1, abort);
-                }
-                release(sk);
-                it++;
-            }
+            if (lane == 0) mbar_arrive(values(s));
         }
         if (!ok && lane == 0) give_up();
-        // every product is finished before the TMEM and shared memory go
-        if (lane == 0) mma_commit(drained);
-        mbar_wait_drain(drained, 0);
     }
     } else {                                             // ---- softmax, one thread per query row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -432,8 +500,10 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             uint32_t s[4][32];
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                if (i < chunks) tmem_ld32(ts + 32 * i, s[i]);
-            tmem_wait_ld();
+                if (i < chunks) {
+                    tmem_ld32(ts + 32 * i, s[i]);
+                }
+            loaded(s[0], s[1], s[2], s[3]);
             // every key of the tile visible to every row: no test per key
             const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= first &&
                                (t.pos > last - p.window || t.pos + kKeys <= p.sinks);
@@ -459,10 +529,8 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             const bool behind = m != -INFINITY && (top - m) * c2 > kLag;
             if (__any_sync(0xffffffffu, behind)) {
-                // O of the products so far is complete and the next one waits for this warp
-                ok = mbar_wait(o_done(q), (it - 1) & 1, abort);
-                if (!ok) break;
-                tc_fence_after();
+                // the products into O so far were complete before these scores were, and
+                // the next one waits for this warp
                 const float f = behind ? ex2((m - top) * c2) : 1.f;
                 for (int i = 0; i < D / 32; i++) {
                     uint32_t o[32];
@@ -481,6 +549,12 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
+                if (i == 2) {                            // the first 64 keys are in TMEM: their product can start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_half(q));
+                }
                 if (i < chunks) {
                     uint32_t w[16];
 #pragma unroll
@@ -502,7 +576,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             if (lane == 0) mbar_arrive(p_ready(q));
             it++;
         }
-        if (ok && it > 0) ok = mbar_wait(o_done(q), (it - 1) & 1, abort);
+        if (ok && it > 0) ok = mbar_wait(o_done(q), 0, abort);
         if (!ok) give_up();
         tc_fence_after();
         if (ok && it > 0) {
