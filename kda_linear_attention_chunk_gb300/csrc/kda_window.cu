@@ -45,6 +45,8 @@ struct PrefillParams {
     uint16_t *pool, *out;
     int N, T, Hq, Hk, num_slots, pool_rows, window, sinks;
     int G, tile_tokens;              // query heads per key head; tokens of a query tile
+    int inv_G;                       // ceil(2^16 / G): r / G = r inv_G >> 16 for r < 128
+    int items;                       // numbers of items, at least as many as there are
     float scale_log2;
     int *err;
 };
@@ -52,8 +54,10 @@ struct PrefillParams {
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is rounded up to
-constexpr int kStages = 5;           // odd: a stage holds keys and values in turn
+constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
 constexpr int kMaxRuns = 6;
+constexpr int kBars = 3 * kStages + 22;
+constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
 // 384 x 168 (the launch checks that the kernel was built with that number).
@@ -66,13 +70,20 @@ struct Run {
     int row, pos, len;               // first row, its position, rows
 };
 
-struct Ctl {
+// One item of work: two query tiles of one key head.
+struct Item {
     Run runs[kMaxRuns];
     int nruns;
-    int n, bos, t0, tokens, first, entry;   // sequence, its first row, the CTA's first row, rows, position of t0
+    int tokens;                      // rows of the item; 0: there are no more items
+    int t0, first;                   // its first row and that row's position
+    int hk, entry;                   // key head, cache entry
+};
+
+struct Ctl {
+    Item items[2];
     int abort;
     uint32_t tmem;
-    uint64_t bars[3 * kStages + 11];
+    uint64_t bars[kBars];
 };
 
 // TMEM columns
@@ -193,7 +204,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int span, i
 }
 
 // runs of consecutive rows that hold the positions [a, b) of the sequence
-__device__ __forceinline__ void add_runs(Ctl &c, const PrefillParams &p, int start, int a, int b)
+__device__ __forceinline__ void add_runs(Item &c, const PrefillParams &p, int bos, int start, int a, int b)
 {
     auto add = [&](int cached, int row, int pos, int len) {
         if (len > 0) c.runs[c.nruns++] = {cached, row, pos, len};
@@ -214,15 +225,15 @@ __device__ __forceinline__ void add_runs(Ctl &c, const PrefillParams &p, int sta
         }
     }
     const int from = max(a, start);
-    add(0, c.bos + from - start, from, b - from);
+    add(0, bos + from - start, from, b - from);
 }
 
 // walks the tiles of the runs
 struct Tiles {
-    const Ctl &c;
+    const Item &c;
     int run = 0, off = 0;
     int cached, row, pos, count;
-    __device__ explicit Tiles(const Ctl &ctl) : c(ctl) {}
+    __device__ explicit Tiles(const Item &item) : c(item) {}
     __device__ bool next()
     {
         if (run >= c.nruns) return false;
@@ -246,116 +257,142 @@ __device__ __forceinline__ bool sees(const Tiles &t, int first, int last, int wi
     return first <= last && t.pos <= last && (t.pos + t.count - 1 > first - window || t.pos < sinks);
 }
 
+// positions of an item's query tile q
+struct Span {
+    int first, last, tokens;
+    __device__ Span(const Item &item, int tile_tokens, int q)
+    {
+        tokens = q ? item.tokens - tile_tokens : min(item.tokens, tile_tokens);
+        if (tokens <= 0) tokens = 0;
+        first = tokens ? item.first + q * tile_tokens : 1;
+        last = tokens ? first + tokens - 1 : 0;
+    }
+};
+
 template <typename E, int D> struct Layout {
     static constexpr int kTile = 128 * D * 2;            // bytes of a query, key or value tile
     static constexpr int kHalf = 128 * 128;              // bytes of its 64 leftmost columns
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTile + sizeof(Ctl);
+    static constexpr int kOut = (2 + kStages) * kTile, kCtl = kOut + 8 * kStage;
+    static constexpr int kSmem = 1024 + kCtl + sizeof(Ctl);
+    static_assert(kSmem <= 227 * 1024, "more shared memory than a CTA has");
+    static constexpr bool kF16 = !__is_same(E, __nv_bfloat16);
 };
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mpool,
-                      const __grid_constant__ PrefillParams p)
-{
-    using L = Layout<E, D>;
-    constexpr bool kF16 = sizeof(E) == 2 && !__is_same(E, __nv_bfloat16);
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t *aligned = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t sq = base, skv = base + 2 * L::kTile;
-    Ctl &c = *reinterpret_cast<Ctl *>(aligned + (2 + kStages) * L::kTile);
-    const uint32_t bars = smem_u32(c.bars);
-    auto full = [&](int s) { return bars + 8 * s; };
-    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-    const uint32_t q_full = bars + 8 * (2 * kStages);
-    auto s_full = [&](int t) { return bars + 8 * (2 * kStages + 1 + t); };
-    auto p_ready = [&](int t) { return bars + 8 * (2 * kStages + 3 + t); };
-    auto o_done = [&](int t) { return bars + 8 * (2 * kStages + 5 + t); };
-    auto p_half = [&](int t) { return bars + 8 * (2 * kStages + 7 + t); };
-    auto turn = [&](int t) { return bars + 8 * (2 * kStages + 9 + t); };
-    auto values = [&](int s) { return bars + 8 * (2 * kStages + 11 + s); };
+// The barriers; q is a query tile, s a stage of the key / value ring, i a place of
+// the item ring.
+struct Bars {
+    uint32_t at;
+    __device__ uint32_t full(int s) const { return at + 8 * s; }                    // tile loaded
+    __device__ uint32_t empty(int s) const { return at + 8 * (kStages + s); }       // tile consumed by both products
+    __device__ uint32_t values(int s) const { return at + 8 * (2 * kStages + s); }  // value tile without garbage
+    __device__ uint32_t q_full(int q) const { return at + 8 * (3 * kStages + q); }
+    __device__ uint32_t q_empty(int q) const { return at + 8 * (3 * kStages + 2 + q); }
+    __device__ uint32_t s_full(int q) const { return at + 8 * (3 * kStages + 4 + q); }    // scores in TMEM
+    __device__ uint32_t p_half(int q) const { return at + 8 * (3 * kStages + 6 + q); }    // probabilities of 64 keys
+    __device__ uint32_t p_ready(int q) const { return at + 8 * (3 * kStages + 8 + q); }   // of all
+    __device__ uint32_t o_done(int q) const { return at + 8 * (3 * kStages + 10 + q); }   // O complete
+    __device__ uint32_t o_free(int q) const { return at + 8 * (3 * kStages + 12 + q); }   // O read
+    __device__ uint32_t turn(int q) const { return at + 8 * (3 * kStages + 14 + q); }
+    __device__ uint32_t drained(int q) const { return at + 8 * (3 * kStages + 16 + q); }
+    __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kStages + 18 + i); }
+    __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kStages + 20 + i); }
+};
+constexpr int kItemReaders = 8 + 2 + 1;   // softmax warps, product warps, patch warp
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int hk = blockIdx.x % p.Hk, slot = gridDim.x / p.Hk - 1 - blockIdx.x / p.Hk;   // late positions first
-    const int span = 2 * p.tile_tokens;
-    if (warp == 8) {
-        const int n = sequence_of(p.cu, p.N, span, slot, lane);
-        if (lane == 0) {
-            const int bos = clamp_row(p.cu[n], p.T, p.err), eos = clamp_row(p.cu[n + 1], p.T, p.err);
-            const int i = slot - (p.cu[n] / span + n);
-            const bool reports = i == 0 && hk == 0;
-            const int len = max(0, eos - bos);
-            const int start = start_of(p, n, len, reports);
-            c.entry = entry_of(p.slots, n, p.num_slots, p.err, reports);
-            c.nruns = 0;
-            c.abort = 0;
-            c.bos = bos;
-            // rows at or past the end: nothing to do
-            c.tokens = i < 0 || (int64_t)i * span >= len || c.entry < 0 ? 0 : min(span, len - i * span);
-            if (c.tokens) {
-                c.t0 = bos + i * span;
-                c.first = start + i * span;
-                const int last = c.first + c.tokens - 1;
-                const int lo = max(0, c.first - p.window + 1);
-                if (lo > p.sinks) {
-                    add_runs(c, p, start, 0, p.sinks);
-                    add_runs(c, p, start, lo, last + 1);
-                } else {
-                    add_runs(c, p, start, 0, last + 1);
-                }
-            }
-            for (int s = 0; s < kStages; s++) {
-                mbar_init(full(s), 1);
-                mbar_init(empty(s), 2);
-                mbar_init(values(s), 1);
-            }
-            mbar_init(q_full, 1);
-            for (int t = 0; t < 2; t++) {
-                mbar_init(s_full(t), 1);
-                mbar_init(p_ready(t), 4);
-                mbar_init(p_half(t), 4);
-                mbar_init(turn(t), 1);
-                mbar_init(o_done(t), 1);
-            }
-            mbar_fence_init();
-        }
-    }
-    __syncthreads();
-    if (c.tokens == 0) return;
-    if (warp == 9) {
-        tmem_alloc(smem_u32(&c.tmem), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = c.tmem;
-    volatile int *abort = &c.abort;
-    auto give_up = [&]() {
+struct Maps {
+    const CUtensorMap *q, *k, *v, *pool;
+};
+
+// What every role knows.
+struct Ctx {
+    const PrefillParams &p;
+    Ctl &c;
+    Bars bars;
+    uint8_t *smem;                   // 1024-byte aligned
+    uint32_t base;                   // its shared-memory address
+    uint32_t tmem;
+    int lane;
+    volatile int *abort;
+    __device__ void give_up() const
+    {
         atomicOr(p.err, kErrWaitTimeout);
         *abort = 1;
-    };
-    // positions of the two query tiles
-    const int tokens0 = min(p.tile_tokens, c.tokens), tokens1 = c.tokens - tokens0;
-    const int first0 = c.first, last0 = first0 + tokens0 - 1;
-    const int first1 = tokens1 > 0 ? first0 + p.tile_tokens : 1, last1 = tokens1 > 0 ? first1 + tokens1 - 1 : 0;
+    }
+    // a wait of the whole warp, the same answer in every lane
+    __device__ bool wait(uint32_t bar, int phase) const
+    {
+        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort)) != 0;
+    }
+};
 
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) {                                     // ---- loads
-        const int nq = __shfl_sync(0xffffffffu, tokens1 > 0 ? 2 : 1, 0), t0 = __shfl_sync(0xffffffffu, c.t0, 0);
-        const int entry_head = __shfl_sync(0xffffffffu, c.entry, 0) * 2 * p.Hk + hk;
-        if (elect_one()) {
-            // half a query tile is G tile_tokens rows of 128 bytes
-            mbar_arrive_expect_tx(q_full, (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64) * nq));
-            for (int t = 0; t < nq; t++)
-                for (int h = 0; h < D / 64; h++)
-                    tma_load_3d(sq + t * L::kTile + h * L::kHalf, &mq, 64 * h, hk * p.G, t0 + t * p.tile_tokens, q_full);
+// Finds the CTA's next item from number `at` on (numbers go up by gridDim.x, every
+// other round in reverse order, so that late ones, which have most keys, are dealt
+// evenly) and writes it to `item`; the warp's lanes agree on what is returned.
+// False: there is none.
+__device__ __forceinline__ bool find_item(const PrefillParams &p, int &round, Item &item, int lane)
+{
+    const int span = 2 * p.tile_tokens;
+    for (;; round++) {
+        const int64_t at = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        if ((int64_t)round * gridDim.x >= p.items) return false;
+        if (at >= p.items) continue;
+        const int number = p.items - 1 - (int)at, slot = number / p.Hk, hk = number - slot * p.Hk;
+        const int n = sequence_of(p.cu, p.N, span, slot, lane);
+        const int cu0 = p.cu[n], cu1 = p.cu[n + 1];
+        const int i = slot - (cu0 / span + n);
+        const bool reports = lane == 0 && i == 0 && hk == 0;
+        const int entry = entry_of(p.slots, n, p.num_slots, p.err, reports);
+        const int bos = clamp_row(cu0, p.T, lane == 0 ? p.err : nullptr);
+        const int eos = clamp_row(cu1, p.T, lane == 0 ? p.err : nullptr);
+        const int len = max(0, eos - bos);
+        const int start = start_of(p, n, len, reports);
+        if (i < 0 || (int64_t)i * span >= len || entry < 0) continue;   // past the sequence's rows, or padded
+        if (lane == 0) {
+            item.nruns = 0;
+            item.hk = hk;
+            item.entry = entry;
+            item.tokens = min(span, len - i * span);
+            item.t0 = bos + i * span;
+            item.first = start + i * span;
+            const int last = item.first + item.tokens - 1, lo = max(0, item.first - p.window + 1);
+            if (lo > p.sinks) {
+                add_runs(item, p, bos, start, 0, p.sinks);
+                add_runs(item, p, bos, start, lo, last + 1);
+            } else {
+                add_runs(item, p, bos, start, 0, last + 1);
+            }
         }
-        int it = 0;
-        bool ok = true;
-        Tiles t(c);
+        __syncwarp();
+        round++;
+        return true;
+    }
+}
+
+// ---- items and loads ---------------------------------------------------------
+template <typename E, int D>
+__device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
+{
+    using L = Layout<E, D>;
+    const PrefillParams &p = x.p;
+    const uint32_t sq = x.base, skv = x.base + 2 * L::kTile;
+    int it = 0, round = 0, item = 0, qs[2] = {0, 0};     // tiles and query tiles loaded, items written
+    bool ok = true, more = true;
+    while (ok && more) {
+        Item &now = x.c.items[item & 1];
+        if (item >= 2) ok = x.wait(x.bars.item_empty(item & 1), item / 2 - 1);
+        if (!ok) break;
+        more = find_item(p, round, now, x.lane);
+        if (x.lane == 0) {
+            if (!more) now.tokens = 0;
+            mbar_arrive(x.bars.item_full(item & 1));
+        }
+        item++;
+        if (!more) break;
+        const int nq = __shfl_sync(0xffffffffu, now.tokens > p.tile_tokens ? 2 : 1, 0);
+        const int t0 = __shfl_sync(0xffffffffu, now.t0, 0), hk = __shfl_sync(0xffffffffu, now.hk, 0);
+        const int entry_head = __shfl_sync(0xffffffffu, now.entry, 0) * 2 * p.Hk + hk;
+        bool queries = false;
+        Tiles t(now);
         while (ok && __shfl_sync(0xffffffffu, t.next(), 0)) {
             const int boxes = __shfl_sync(0xffffffffu, (t.count + kBox - 1) / kBox, 0);
             const int row = __shfl_sync(0xffffffffu, t.row, 0);
@@ -363,150 +400,214 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 #pragma unroll
             for (int kv = 0; kv < 2; kv++) {
                 const int s = it % kStages;
-                if (ok && it >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(empty(s), (it / kStages - 1) & 1, abort));
+                if (ok && it >= kStages) ok = x.wait(x.bars.empty(s), it / kStages - 1);
                 if (!ok) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(full(s), (uint32_t)(boxes * kBox * 128 * (D / 64)));
-                    const uint32_t to = skv + s * L::kTile;
+                    const uint32_t bar = x.bars.full(s), to = skv + s * L::kTile;
+                    mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kBox * 128 * (D / 64)));
                     if (cached) {
                         for (int b = 0; b < boxes; b++)
 #pragma unroll
                             for (int h = 0; h < D / 64; h++)
-                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), &mpool, 64 * h, row + b * kBox,
-                                            entry_head + kv * p.Hk, full(s));
+                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), maps.pool, 64 * h, row + b * kBox,
+                                            entry_head + kv * p.Hk, bar);
                     } else {
                         for (int b = 0; b < boxes; b++)
 #pragma unroll
                             for (int h = 0; h < D / 64; h++)
-                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), kv ? &mv : &mk, 64 * h, hk,
-                                            row + b * kBox, full(s));
+                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), kv ? maps.v : maps.k, 64 * h, hk,
+                                            row + b * kBox, bar);
                     }
                 }
                 it++;
+                if (queries) continue;
+                queries = true;                          // after the first keys, which need not wait for their room
+                for (int q = 0; q < nq && ok; q++) {
+                    if (qs[q]) ok = x.wait(x.bars.q_empty(q), qs[q] - 1);
+                    if (ok && elect_one()) {
+                        // half a query tile is G tile_tokens rows of 128 bytes
+                        mbar_arrive_expect_tx(x.bars.q_full(q), (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64)));
+#pragma unroll
+                        for (int h = 0; h < D / 64; h++)
+                            tma_load_3d(sq + q * L::kTile + h * L::kHalf, maps.q, 64 * h, hk * p.G,
+                                        t0 + q * p.tile_tokens, x.bars.q_full(q));
+                    }
+                    if (ok) qs[q]++;
+                }
             }
         }
-        if (!ok && lane == 0) give_up();
-        // nothing may still be on its way into shared memory when the CTA ends
-        mbar_wait_drain(q_full, 0);
-        for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(full(i % kStages), (i / kStages) & 1);
-    } else if (warp == 9 || warp == 11) {                // ---- products of one query tile
-        // The whole warp walks the loop and one elected lane issues: operands that are
-        // uniform over the warp stay in uniform registers, where the instruction takes
-        // them (85 cycles an MMA from a loop that one lane runs alone).
-        const int q = __shfl_sync(0xffffffffu, warp == 11, 0);
-        const int first = q ? first1 : first0, last = q ? last1 : last0;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q, qs = sq + q * L::kTile;
-        auto wait = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort)) != 0; };
-        // The query tiles take turns, so that one's scores are exponentiated during
-        // the other's products: left alone they fall into step (4100 cycles a tile of
-        // keys instead of 3600).
-        const bool both = __shfl_sync(0xffffffffu, tokens1 > 0, 0);
-        int it = 1, done = 0, round = 0;                 // loads consumed; products O += P V issued; tiles
-        Tiles t(c);
-        bool have = t.next(), now = __shfl_sync(0xffffffffu, sees(t, first, last, p.window, p.sinks), 0);
+    }
+    if (!ok && x.lane == 0) x.give_up();
+    // nothing may still be on its way into shared memory when the CTA ends
+    for (int q = 0; q < 2; q++)
+        if (qs[q]) mbar_wait_drain(x.bars.q_full(q), (qs[q] - 1) & 1);
+    for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(x.bars.full(i % kStages), (i / kStages) & 1);
+}
+
+// ---- products of one query tile ---------------------------------------------------
+// The whole warp walks the loop and one elected lane issues: operands that are
+// uniform over the warp stay in uniform registers, where the instruction takes them
+// (85 cycles an MMA from a loop that one lane runs alone).  The two query tiles take
+// turns, so that one's scores are exponentiated during the other's products: left
+// alone they fall into step (4100 cycles a tile of keys instead of 2700).
+template <typename E, int D>
+__device__ __forceinline__ void product_role(const Ctx &x, int which)
+{
+    using L = Layout<E, D>;
+    const PrefillParams &p = x.p;
+    const int q = __shfl_sync(0xffffffffu, which, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
+    const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q;
+    const uint32_t qs = x.base + q * L::kTile, skv = x.base + 2 * L::kTile;
+    int it = 0, parts = 0, turns = 0, mine = 0;          // tiles consumed; products P V issued; turns taken; items with rows
+    bool ok = true;
+    for (int item = 0; ok; item++) {
+        const Item &now = x.c.items[item & 1];
+        ok = x.wait(x.bars.item_full(item & 1), item / 2);
+        const int tokens = __shfl_sync(0xffffffffu, now.tokens, 0);
+        if (!ok || tokens == 0) break;
+        const Span rows(now, p.tile_tokens, q);
+        const bool both = tokens > p.tile_tokens, any = __shfl_sync(0xffffffffu, rows.tokens > 0, 0);
+        int done = 0;                                    // products P V of this item
+        Tiles t(now);
+        bool have = __shfl_sync(0xffffffffu, t.next(), 0);
+        bool sees_now = __shfl_sync(0xffffffffu, sees(t, rows.first, rows.last, p.window, p.sinks), 0);
         int count = __shfl_sync(0xffffffffu, t.count, 0);
-        bool ok = wait(q_full, 0) && wait(full(0), 0);
+        ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), mine));
         if (elect_one()) {
-            if (ok && now) {
-                mma_scores<D>(ts, qs, skv, idesc((count + 15) & ~15, 0, kF16));
-                mma_commit(s_full(q));
+            if (ok && sees_now) {
+                mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc((count + 15) & ~15, 0, L::kF16));
+                mma_commit(x.bars.s_full(q));
             }
-            mma_commit(empty(0));
+            mma_commit(x.bars.empty(it % kStages));
         }
+        it++;
         while (have && ok) {
             const int sv = it % kStages, steps = (count + 15) / 16;   // this tile's values
-            const bool was = now;
-            ok = wait(values(sv), it / (2 * kStages));
+            const bool saw = sees_now;
+            ok = x.wait(x.bars.values(sv), it / kStages);
             it++;
             const int sk = it % kStages;                 // the next tile's keys
             have = __shfl_sync(0xffffffffu, t.next(), 0);
             if (have) {
-                now = __shfl_sync(0xffffffffu, sees(t, first, last, p.window, p.sinks), 0);
+                sees_now = __shfl_sync(0xffffffffu, sees(t, rows.first, rows.last, p.window, p.sinks), 0);
                 count = __shfl_sync(0xffffffffu, t.count, 0);
-                ok = ok && wait(full(sk), it / kStages);
+                ok = ok && x.wait(x.bars.full(sk), it / kStages);
                 it++;
+            } else if (any && elect_one()) {
+                mma_commit(x.bars.q_empty(q));           // every product with the query tile is issued
             }
-            if (both && ok && (q || round)) ok = wait(turn(q), q ? round : round - 1);
-            if (ok && was) {
-                ok = wait(p_half(q), done);
+            __syncwarp();
+            if (both && ok && (q || turns)) ok = x.wait(x.bars.turn(q), q ? turns : turns - 1);
+            if (ok && saw) {
+                if (done == 0 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
+                ok = ok && x.wait(x.bars.p_half(q), parts);
                 if (ok) {
                     tc_fence_after();
-                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, kF16), 0, steps, done > 0);
-                    ok = wait(p_ready(q), done);
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 0, steps, done > 0);
+                    ok = x.wait(x.bars.p_ready(q), parts);
                 }
                 if (ok) {
                     tc_fence_after();
-                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, kF16), 4, steps, true);
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 4, steps, true);
                     done++;
+                    parts++;
                 }
             }
             if (elect_one()) {
-                if (ok && have && now) {
-                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc((count + 15) & ~15, 0, kF16));
-                    mma_commit(s_full(q));
+                if (ok && have && sees_now) {
+                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc((count + 15) & ~15, 0, L::kF16));
+                    mma_commit(x.bars.s_full(q));
                 }
-                if (both) mbar_arrive(turn(!q));
-                mma_commit(empty(sv));
-                if (have) mma_commit(empty(sk));
+                if (both) mbar_arrive(x.bars.turn(!q));
+                mma_commit(x.bars.empty(sv));
+                if (have) mma_commit(x.bars.empty(sk));
+                else if (any) mma_commit(x.bars.o_done(q));
             }
-            round++;
+            __syncwarp();
+            if (both) turns++;
         }
-        if (!ok && lane == 0) give_up();
-        // every product is finished before O is read, and before the TMEM and shared memory go
-        if (elect_one()) mma_commit(o_done(q));
-        mbar_wait_drain(o_done(q), 0);
-    } else if (warp == 10) {                             // ---- zeros behind ragged runs
-        // Value rows past a run hold anything, and 0 x NaN is NaN: the rows that the
-        // last 16 keys of its tile are rounded up to become zeros.  Every value tile
-        // passes through here (in an odd ring a stage holds keys and values in turn).
-        Tiles t(c);
-        bool ok = true;
-        for (int it = 1; ok && t.next(); it += 2) {
+        if (any) mine++;
+        __syncwarp();
+        if (x.lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
+    }
+    if (!ok && x.lane == 0) x.give_up();
+    // every product is finished before the TMEM and shared memory go
+    if (elect_one()) mma_commit(x.bars.drained(q));
+    mbar_wait_drain(x.bars.drained(q), 0);
+}
+
+// ---- zeros behind ragged runs ------------------------------------------------------
+// Value rows past a run hold anything, and 0 x NaN is NaN: the rows that the last 16
+// keys of its tile are rounded up to become zeros.  Every value tile passes through
+// here.
+template <typename E, int D>
+__device__ __forceinline__ void patch_role(const Ctx &x)
+{
+    using L = Layout<E, D>;
+    bool ok = true;
+    for (int item = 0, it = 1; ok; item++) {
+        const Item &now = x.c.items[item & 1];
+        ok = x.wait(x.bars.item_full(item & 1), item / 2);
+        if (!ok || now.tokens == 0) break;
+        Tiles t(now);
+        for (; ok && t.next(); it += 2) {
             const int s = it % kStages;
-            ok = mbar_wait(full(s), (it / kStages) & 1, abort);
+            ok = x.wait(x.bars.full(s), it / kStages);
             if (!ok) break;
             if (t.count & 15) {
-                for (int e = lane; e < (16 - (t.count & 15)) * (D / 8); e += 32) {
+                for (int e = x.lane; e < (16 - (t.count & 15)) * (D / 8); e += 32) {
                     const int r = t.count + e / (D / 8), v = e % (D / 8);
-                    *reinterpret_cast<uint4 *>(aligned + (2 + s) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
+                    *reinterpret_cast<uint4 *>(x.smem + (2 + s) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
             }
-            if (lane == 0) mbar_arrive(values(s));
+            __syncwarp();
+            if (x.lane == 0) mbar_arrive(x.bars.values(s));
         }
-        if (!ok && lane == 0) give_up();
+        __syncwarp();
+        if (x.lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
     }
-    } else {                                             // ---- softmax, one thread per query row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int q = warp >> 2, row = threadIdx.x & 127;
-        const int first = q ? first1 : first0, last = q ? last1 : last0, tokens = q ? tokens1 : tokens0;
-        const int token = row / p.G, pos = first + token;
-        const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + kTmS + 128 * q;
-        const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kTmO + 128 * q;
-        const float c2 = p.scale_log2;
+    if (!ok && x.lane == 0) x.give_up();
+}
+
+// ---- softmax, one thread per query row, and the output -------------------------------
+template <typename E, int D>
+__device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
+{
+    using L = Layout<E, D>;
+    const PrefillParams &p = x.p;
+    const int q = warp >> 2, row = 32 * (warp & 3) + x.lane, lane = x.lane;
+    const int token = row * p.inv_G >> 16;               // row / G
+    const uint32_t lanes = x.tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t ts = lanes + kTmS + 128 * q, to = lanes + kTmO + 128 * q;
+    const float c2 = p.scale_log2;
+    uint8_t *stage = x.smem + L::kOut + warp * kStage;
+    int it = 0, mine = 0;                                // score tiles, items with rows
+    bool ok = true;
+    for (int item = 0; ok; item++) {
+        const Item &now = x.c.items[item & 1];
+        ok = mbar_wait(x.bars.item_full(item & 1), (item / 2) & 1, x.abort);
+        if (!ok || now.tokens == 0) break;
+        const Span rows(now, p.tile_tokens, q);
+        const int pos = rows.first + token, t0 = now.t0 + q * p.tile_tokens, hk = now.hk;
         float m = -INFINITY, sum = 0.f;
-        int it = 0;
-        bool ok = true;
-        Tiles t(c);
-        while (ok && t.next()) {
-            if (!sees(t, first, last, p.window, p.sinks)) continue;
-            ok = mbar_wait(s_full(q), it & 1, abort);
+        Tiles t(now);
+        while (rows.tokens && t.next()) {
+            if (!sees(t, rows.first, rows.last, p.window, p.sinks)) continue;
+            ok = mbar_wait(x.bars.s_full(q), it & 1, x.abort);
             if (!ok) break;
             tc_fence_after();
             const int chunks = (t.count + 31) / 32;
             uint32_t s[4][32];
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                if (i < chunks) {
-                    tmem_ld32(ts + 32 * i, s[i]);
-                }
+                if (i < chunks) tmem_ld32(ts + 32 * i, s[i]);
             loaded(s[0], s[1], s[2], s[3]);
             // every key of the tile visible to every row: no test per key
-            const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= first &&
-                               (t.pos > last - p.window || t.pos + kKeys <= p.sinks);
+            const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= rows.first &&
+                               (t.pos > rows.last - p.window || t.pos + kKeys <= p.sinks);
             if (!whole) {
                 const int hi = min(pos - t.pos, t.count - 1);        // last visible column
                 const int lo = max(pos - p.window, -1) - t.pos;      // columns up to here are behind the window
@@ -553,7 +654,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(p_half(q));
+                    if (lane == 0) mbar_arrive(x.bars.p_half(q));
                 }
                 if (i < chunks) {
                     uint32_t w[16];
@@ -573,37 +674,116 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready(q));
+            if (lane == 0) mbar_arrive(x.bars.p_ready(q));
             it++;
         }
-        if (ok && it > 0) ok = mbar_wait(o_done(q), 0, abort);
-        if (!ok) give_up();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
+        if (!ok || !rows.tokens) continue;
+        ok = mbar_wait(x.bars.o_done(q), mine & 1, x.abort);
+        if (!ok) break;
         tc_fence_after();
-        if (ok && it > 0) {
-            const float inv = 1.f / sum;
-            const bool live = token < tokens && row < p.tile_tokens * p.G;
-            uint16_t *o = p.out + ((int64_t)(c.t0 + q * p.tile_tokens + token) * p.Hq + hk * p.G + row % p.G) * D;
-            for (int i = 0; i < D / 32; i++) {
-                uint32_t x[32];
-                tmem_ld32(to + 32 * i, x);
-                tmem_wait_ld();
-                if (live)
+        mine++;
+        // O / sum in 16 bits, 64 columns at a time through shared memory, so that a
+        // store instruction writes four rows of 128 bytes
+        const float inv = 1.f / sum;
+        const int live = rows.tokens * p.G;              // rows of the tile
+        uint16_t *out = p.out + ((int64_t)t0 * p.Hq + hk * p.G) * D + 8 * (lane & 7);
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        uint4 r;
-                        r.x = Half2<E>::pack(__uint_as_float(x[8 * j]) * inv, __uint_as_float(x[8 * j + 1]) * inv);
-                        r.y = Half2<E>::pack(__uint_as_float(x[8 * j + 2]) * inv, __uint_as_float(x[8 * j + 3]) * inv);
-                        r.z = Half2<E>::pack(__uint_as_float(x[8 * j + 4]) * inv, __uint_as_float(x[8 * j + 5]) * inv);
-                        r.w = Half2<E>::pack(__uint_as_float(x[8 * j + 6]) * inv, __uint_as_float(x[8 * j + 7]) * inv);
-                        reinterpret_cast<uint4 *>(o + 32 * i)[j] = r;
-                    }
+        for (int h = 0; h < D / 64; h++) {
+            uint32_t o[2][32];
+            tmem_ld32(to + 64 * h, o[0]);
+            tmem_ld32(to + 64 * h + 32, o[1]);
+            tmem_wait_ld();
+            if (h == D / 64 - 1) {                       // O is free for the next item
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x.bars.o_free(q));
             }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t *v = &o[j / 4][8 * (j & 3)];
+                uint4 r;
+                r.x = Half2<E>::pack(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
+                r.y = Half2<E>::pack(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
+                r.z = Half2<E>::pack(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
+                r.w = Half2<E>::pack(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = r;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int rr = 4 * j + (lane >> 3), r = 32 * (warp & 3) + rr;
+                const int tok = r * p.inv_G >> 16, head = r - tok * p.G;
+                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                if (r < live) *reinterpret_cast<uint4 *>(out + ((int64_t)tok * p.Hq + head) * D + 64 * h) = v;
+            }
+            __syncwarp();
         }
+    }
+    if (!ok) x.give_up();
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mpool,
+                      const __grid_constant__ PrefillParams p)
+{
+    using L = Layout<E, D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));
+    Ctl &c = *reinterpret_cast<Ctl *>(smem + L::kCtl);
+    const Bars bars{smem_u32(c.bars)};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp == 8 && lane == 0) {
+        c.abort = 0;
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(bars.full(s), 1);
+            mbar_init(bars.empty(s), 2);
+            mbar_init(bars.values(s), 1);
+        }
+        for (int q = 0; q < 2; q++) {
+            mbar_init(bars.q_full(q), 1);
+            mbar_init(bars.q_empty(q), 1);
+            mbar_init(bars.s_full(q), 1);
+            mbar_init(bars.p_half(q), 4);
+            mbar_init(bars.p_ready(q), 4);
+            mbar_init(bars.o_done(q), 1);
+            mbar_init(bars.o_free(q), 4);
+            mbar_init(bars.turn(q), 1);
+            mbar_init(bars.drained(q), 1);
+            mbar_init(bars.item_full(q), 1);
+            mbar_init(bars.item_empty(q), kItemReaders);
+        }
+        mbar_fence_init();
+        tma_prefetch_desc(&mq);
+        tma_prefetch_desc(&mk);
+        tma_prefetch_desc(&mv);
+        tma_prefetch_desc(&mpool);
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&c.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Ctx x{p, c, bars, smem, base, c.tmem, lane, &c.abort};
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 8) load_role<E, D>(x, Maps{&mq, &mk, &mv, &mpool});
+        else if (warp == 10) patch_role<E, D>(x);
+        else product_role<E, D>(x, warp == 11);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        softmax_role<E, D>(x, warp);
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 9) tmem_dealloc(x.tmem, 512);
 }
 
 // Writes the rows that the cache keeps: sinks, and the sequence's last pool_rows
@@ -681,9 +861,7 @@ cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
     cudaFuncAttributes built;
     if ((e = cudaFuncGetAttributes(&built, window_prefill_kernel<E, D>)) != cudaSuccess) return e;
     if (built.numRegs != kRegs) return cudaErrorInvalidConfiguration;
-    const int64_t blocks = ((int64_t)a.T / (2 * p.tile_tokens) + a.N) * a.Hk;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    window_prefill_kernel<E, D><<<(unsigned)blocks, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
+    window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.pool) return e;
     ring_commit_kernel<D><<<(unsigned)(((int64_t)p.T * p.Hk * (D / 8) + 255) / 256), 256, 0, a.stream>>>(p);
@@ -703,6 +881,10 @@ cudaError_t launch_window_prefill(const WindowArgs &a)
     p.window = a.window; p.sinks = a.sinks;
     p.G = a.Hq / a.Hk;
     p.tile_tokens = 128 / p.G;
+    p.inv_G = (65536 + p.G - 1) / p.G;
+    const int64_t items = ((int64_t)a.T / (2 * p.tile_tokens) + a.N) * a.Hk;
+    if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    p.items = (int)items;
     p.scale_log2 = a.scale * kLog2e;
     p.err = a.err_word;
     if (a.d == 128) return a.f16 ? launch<__half, 128>(a, p) : launch<__nv_bfloat16, 128>(a, p);
