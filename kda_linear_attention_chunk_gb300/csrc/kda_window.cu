@@ -57,7 +57,7 @@ constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is
 constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
 constexpr int kMaxRuns = 6;
 constexpr int kBars = 3 * kStages + 22;
-constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
+constexpr int kStage = 2048;         // bytes in which a softmax warp turns its rows of O around
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
 // 384 x 168 (the launch checks that the kernel was built with that number).
@@ -165,6 +165,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+// The n lowest bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) { return ~__funnelshift_lc(0u, ~0u, (uint32_t)max(n, 0)); }
+
 // Waits for the TMEM loads, as seen by whatever uses these registers.
 __device__ __forceinline__ void loaded(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t (&c)[32], uint32_t (&d)[32])
 {
@@ -173,34 +176,67 @@ __device__ __forceinline__ void loaded(uint32_t (&a)[32], uint32_t (&b)[32], uin
     for (int i = 0; i < 32; i++) asm volatile("" : "+r"(a[i]), "+r"(b[i]), "+r"(c[i]), "+r"(d[i]));
 }
 
-// positions before the first row of sequence n, which has L rows
-__device__ __forceinline__ int start_of(const PrefillParams &p, int n, int L, bool reports)
-{
-    if (!p.starts) return 0;
-    const int s = p.starts[n], most = 0x7fffffff - L;
-    if (s < 0 || s > most) {
-        if (reports) atomicOr(p.err, kErrBadPosition);
-        return s < 0 ? 0 : most;
-    }
-    return s;
-}
+// The spans of `span` rows of a packed batch are numbered so that sequence n has the
+// numbers from cu[n] / span + n on: at least as many as it has spans, without a
+// pass over the table.  A sequence's facts:
+struct Sequence {
+    int cu0, cu1, start, slot;       // its two table entries, context length and slot, as they are
+    int part;                        // the number's place among the sequence's spans (may be past its rows)
+};
 
-// The CTAs of a key head are numbered so that sequence n has the numbers from
-// cu[n] / span + n on: at least as many as it has spans of `span` rows, without
-// a pass over the table.  The last sequence whose numbers start at or before s,
-// by one warp, 32 probes at a time.
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int span, int s, int lane)
+// The last sequence whose numbers start at or before `number`, by a converged warp:
+// 32 probes at a time, the last of which bring the facts along.
+__device__ __forceinline__ Sequence sequence_of(const PrefillParams &p, int span, int number, int lane)
 {
-    int a = 0, n = N;                // the answer is in [a, a + n)
-    while (n > 1) {
+    int a = 0, n = p.N;              // the answer is in [a, a + n)
+    while (n > 32) {
         const int step = (n + 31) / 32, at = a + lane * step;
-        const bool le = lane * step < n && cu[at] / span + at <= s;
-        const uint32_t votes = __ballot_sync(0xffffffffu, le || lane == 0);
-        const int last = 31 - __clz(votes);
+        const bool le = lane * step < n && p.cu[at] / span + at <= number;
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, le || lane == 0));
         n = min(step, n - last * step);
         a += last * step;
     }
-    return a;
+    const int at = a + min(lane, n - 1);
+    Sequence s;
+    s.cu0 = p.cu[at];
+    s.cu1 = p.cu[at + 1];
+    s.start = p.starts ? p.starts[at] : 0;
+    s.slot = p.slots ? p.slots[at] : at;
+    s.part = number - (s.cu0 / span + at);
+    const int who = 31 - __clz(__ballot_sync(0xffffffffu, (lane < n && s.part >= 0) || lane == 0));
+    s.cu0 = __shfl_sync(0xffffffffu, s.cu0, who);
+    s.cu1 = __shfl_sync(0xffffffffu, s.cu1, who);
+    s.start = __shfl_sync(0xffffffffu, s.start, who);
+    s.slot = __shfl_sync(0xffffffffu, s.slot, who);
+    s.part = __shfl_sync(0xffffffffu, s.part, who);
+    return s;
+}
+
+// The rows that number `number` stands for, all checked; `reports`: whether this
+// warp tells of entries out of range.
+struct Rows {
+    int bos, len, start, entry;      // the sequence's first row, rows, context length, cache entry
+    int from, n;                     // the span's first row within the sequence, and its rows (0: none)
+};
+__device__ __forceinline__ Rows rows_of(const PrefillParams &p, int span, int number, int lane, bool reports)
+{
+    const Sequence s = sequence_of(p, span, number, lane);
+    reports = reports && lane == 0 && s.part == 0;
+    Rows r;
+    r.bos = clamp_row(s.cu0, p.T, reports ? p.err : nullptr);
+    r.len = max(0, clamp_row(s.cu1, p.T, reports ? p.err : nullptr) - r.bos);
+    const int most = 0x7fffffff - r.len;
+    r.start = min(max(s.start, 0), most);
+    if (r.start != s.start && reports) atomicOr(p.err, kErrBadPosition);
+    r.entry = s.slot;
+    if (p.slots && (s.slot < 0 || s.slot >= p.num_slots)) {
+        if (s.slot != -1 && reports) atomicOr(p.err, kErrBadSlot);
+        r.entry = -1;
+    }
+    const int64_t from = (int64_t)s.part * span;
+    r.n = s.part < 0 || from >= r.len || r.entry < 0 ? 0 : (int)min((int64_t)span, r.len - from);
+    r.from = r.n ? (int)from : 0;
+    return r;
 }
 
 // runs of consecutive rows that hold the positions [a, b) of the sequence
@@ -337,29 +373,21 @@ __device__ __forceinline__ bool find_item(const PrefillParams &p, int &round, It
         if ((int64_t)round * gridDim.x >= p.items) return false;
         if (at >= p.items) continue;
         const int number = p.items - 1 - (int)at, slot = number / p.Hk, hk = number - slot * p.Hk;
-        const int n = sequence_of(p.cu, p.N, span, slot, lane);
-        const int cu0 = p.cu[n], cu1 = p.cu[n + 1];
-        const int i = slot - (cu0 / span + n);
-        const bool reports = lane == 0 && i == 0 && hk == 0;
-        const int entry = entry_of(p.slots, n, p.num_slots, p.err, reports);
-        const int bos = clamp_row(cu0, p.T, lane == 0 ? p.err : nullptr);
-        const int eos = clamp_row(cu1, p.T, lane == 0 ? p.err : nullptr);
-        const int len = max(0, eos - bos);
-        const int start = start_of(p, n, len, reports);
-        if (i < 0 || (int64_t)i * span >= len || entry < 0) continue;   // past the sequence's rows, or padded
+        const Rows r = rows_of(p, span, slot, lane, hk == 0);
+        if (!r.n) continue;          // past the sequence's rows, or padded
         if (lane == 0) {
             item.nruns = 0;
             item.hk = hk;
-            item.entry = entry;
-            item.tokens = min(span, len - i * span);
-            item.t0 = bos + i * span;
-            item.first = start + i * span;
+            item.entry = r.entry;
+            item.tokens = r.n;
+            item.t0 = r.bos + r.from;
+            item.first = r.start + r.from;
             const int last = item.first + item.tokens - 1, lo = max(0, item.first - p.window + 1);
             if (lo > p.sinks) {
-                add_runs(item, p, bos, start, 0, p.sinks);
-                add_runs(item, p, bos, start, lo, last + 1);
+                add_runs(item, p, r.bos, r.start, 0, p.sinks);
+                add_runs(item, p, r.bos, r.start, lo, last + 1);
             } else {
-                add_runs(item, p, bos, start, 0, last + 1);
+                add_runs(item, p, r.bos, r.start, 0, last + 1);
             }
         }
         __syncwarp();
@@ -591,34 +619,44 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         ok = mbar_wait(x.bars.item_full(item & 1), (item / 2) & 1, x.abort);
         if (!ok || now.tokens == 0) break;
         const Span rows(now, p.tile_tokens, q);
+        const int lo_row = rows.first + (32 * (warp & 3) * p.inv_G >> 16);
+        const int hi_row = rows.first + ((32 * (warp & 3) + 31) * p.inv_G >> 16);
+        const bool dead = 32 * (warp & 3) >= rows.tokens * p.G;      // no row of this warp is one: O may be anything
         const int pos = rows.first + token, t0 = now.t0 + q * p.tile_tokens, hk = now.hk;
         float m = -INFINITY, sum = 0.f;
         Tiles t(now);
         while (rows.tokens && t.next()) {
             if (!sees(t, rows.first, rows.last, p.window, p.sinks)) continue;
+            // every key of the tile visible to every row of the warp: no test per key
+            const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= lo_row &&
+                               (t.pos > hi_row - p.window || t.pos + kKeys <= p.sinks);
             ok = mbar_wait(x.bars.s_full(q), it & 1, x.abort);
             if (!ok) break;
+            it++;
+            if (dead) {                                  // whatever is there will do as these rows' P
+                if (lane == 0) {
+                    mbar_arrive(x.bars.p_half(q));
+                    mbar_arrive(x.bars.p_ready(q));
+                }
+                continue;
+            }
             tc_fence_after();
-            const int chunks = (t.count + 31) / 32;
             uint32_t s[4][32];
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                if (i < chunks) tmem_ld32(ts + 32 * i, s[i]);
+                if (32 * i < t.count) tmem_ld32(ts + 32 * i, s[i]);
             loaded(s[0], s[1], s[2], s[3]);
-            // every key of the tile visible to every row: no test per key
-            const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= rows.first &&
-                               (t.pos > rows.last - p.window || t.pos + kKeys <= p.sinks);
             if (!whole) {
                 const int hi = min(pos - t.pos, t.count - 1);        // last visible column
                 const int lo = max(pos - p.window, -1) - t.pos;      // columns up to here are behind the window
                 const int sk = p.sinks - t.pos;                      // unless they are sinks
 #pragma unroll
-                for (int i = 0; i < 4; i++)
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t seen = below(hi + 1 - 32 * i) & ~(below(lo + 1 - 32 * i) & ~below(sk - 32 * i));
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const int col = 32 * i + j;
-                        if (col > hi || (col <= lo && col >= sk)) s[i][j] = 0xff800000u;   // -inf
-                    }
+                    for (int j = 0; j < 32; j++)
+                        if (!(seen & (1u << j))) s[i][j] = 0xff800000u;   // -inf
+                }
             }
             float mx[4];
 #pragma unroll
@@ -656,7 +694,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(x.bars.p_half(q));
                 }
-                if (i < chunks) {
+                if (32 * i < t.count) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
@@ -675,7 +713,6 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(x.bars.p_ready(q));
-            it++;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
@@ -684,39 +721,38 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         if (!ok) break;
         tc_fence_after();
         mine++;
-        // O / sum in 16 bits, 64 columns at a time through shared memory, so that a
-        // store instruction writes four rows of 128 bytes
+        // O / sum in 16 bits, 32 columns at a time through shared memory, so that a
+        // store instruction writes eight rows of 64 bytes.  A short loop: code that runs
+        // once an item waits for its instructions.
         const float inv = 1.f / sum;
-        const int live = rows.tokens * p.G;              // rows of the tile
-        uint16_t *out = p.out + ((int64_t)t0 * p.Hq + hk * p.G) * D + 8 * (lane & 7);
-#pragma unroll
-        for (int h = 0; h < D / 64; h++) {
-            uint32_t o[2][32];
-            tmem_ld32(to + 64 * h, o[0]);
-            tmem_ld32(to + 64 * h + 32, o[1]);
+        const int live = rows.tokens * p.G - 32 * (warp & 3);        // of this warp's rows
+        uint16_t *out = p.out + ((int64_t)t0 * p.Hq + hk * p.G) * D + 8 * (lane & 3);
+#pragma unroll 1
+        for (int h = 0; h < D / 32; h++) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * h, o);
             tmem_wait_ld();
-            if (h == D / 64 - 1) {                       // O is free for the next item
+            if (h == D / 32 - 1) {                       // O is free for the next item
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x.bars.o_free(q));
             }
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const uint32_t *v = &o[j / 4][8 * (j & 3)];
+            for (int j = 0; j < 4; j++) {
                 uint4 r;
-                r.x = Half2<E>::pack(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
-                r.y = Half2<E>::pack(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
-                r.z = Half2<E>::pack(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
-                r.w = Half2<E>::pack(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
-                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = r;
+                r.x = Half2<E>::pack(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
+                r.y = Half2<E>::pack(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
+                r.z = Half2<E>::pack(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
+                r.w = Half2<E>::pack(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
+                *reinterpret_cast<uint4 *>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = r;
             }
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int rr = 4 * j + (lane >> 3), r = 32 * (warp & 3) + rr;
+            for (int j = 0; j < 4; j++) {
+                const int rr = 8 * j + (lane >> 2), r = 32 * (warp & 3) + rr;
                 const int tok = r * p.inv_G >> 16, head = r - tok * p.G;
-                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                if (r < live) *reinterpret_cast<uint4 *>(out + ((int64_t)tok * p.Hq + head) * D + 64 * h) = v;
+                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                if (rr < live) *reinterpret_cast<uint4 *>(out + ((int64_t)tok * p.Hq + head) * D + 32 * h) = v;
             }
             __syncwarp();
         }
@@ -786,32 +822,28 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (warp == 9) tmem_dealloc(x.tmem, 512);
 }
 
-// Writes the rows that the cache keeps: sinks, and the sequence's last pool_rows
-// - sinks positions.  16 bytes a thread.
+// Writes the rows that the cache keeps: sinks, and each sequence's last pool_rows -
+// sinks positions.  A CTA takes kCommitRows consecutive rows of a sequence, a warp
+// one of them at a time.
+constexpr int kCommitRows = 8;
+
 template <int D>
 __global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant__ PrefillParams p)
 {
-    const int per = p.Hk * (D / 8);
-    const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int t = (int)(w / per), e = (int)(w % per);
-    if (t >= p.T) return;
-    int n = 0;                       // the last sequence that starts at or before row t
-    for (int b = p.N - 1; n < b;) {
-        const int m = (n + b + 1) / 2;
-        if (p.cu[m] <= t) n = m; else b = m - 1;
+    const int lane = threadIdx.x & 31;
+    const Rows r = rows_of(p, kCommitRows, blockIdx.x, lane, false);
+    const int i = r.from + (threadIdx.x >> 5);           // this warp's row of the sequence
+    if (i >= r.from + r.n) return;
+    const int pos = r.start + i, ring = p.pool_rows - p.sinks;
+    if (pos >= p.sinks && r.len - i > ring) return;      // a later row of the call takes its place
+    const uint16_t *k = p.k + (r.bos + i) * p.k_stride, *v = p.v + (r.bos + i) * p.v_stride;
+    uint16_t *to = p.pool + (int64_t)r.entry * 2 * p.Hk * p.pool_rows * D + (int64_t)ring_row(pos, p.sinks, p.pool_rows) * D;
+    const int64_t head = (int64_t)p.pool_rows * D;
+    for (int e = lane; e < 2 * p.Hk * (D / 8); e += 32) {
+        const int h = e / (D / 8), at = e % (D / 8) * 8;
+        const uint16_t *from = h < p.Hk ? k + h * D : v + (h - p.Hk) * D;
+        *reinterpret_cast<uint4 *>(to + h * head + at) = *reinterpret_cast<const uint4 *>(from + at);
     }
-    const int bos = clamp_row(p.cu[n], p.T, nullptr), eos = clamp_row(p.cu[n + 1], p.T, nullptr);
-    if (t < bos || t >= eos) return;
-    const int entry = entry_of(p.slots, n, p.num_slots, nullptr, false);
-    if (entry < 0) return;
-    const int start = start_of(p, n, eos - bos, false), pos = start + t - bos;
-    if (pos >= p.sinks && eos - t > p.pool_rows - p.sinks) return;
-    const int hk = e / (D / 8), at = (e % (D / 8)) * 8;
-    uint16_t *to = p.pool + ((int64_t)entry * 2 * p.Hk + hk) * p.pool_rows * D +
-                   (int64_t)ring_row(pos, p.sinks, p.pool_rows) * D + at;
-    *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + hk * D + at);
-    to += (int64_t)p.Hk * p.pool_rows * D;
-    *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + hk * D + at);
 }
 
 // The driver's tensor-map encoder, looked up once.
@@ -864,7 +896,7 @@ cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
     window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.pool) return e;
-    ring_commit_kernel<D><<<(unsigned)(((int64_t)p.T * p.Hk * (D / 8) + 255) / 256), 256, 0, a.stream>>>(p);
+    ring_commit_kernel<D><<<p.T / kCommitRows + p.N, 256, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
 
