@@ -57,7 +57,7 @@ constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is
 constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
 constexpr int kMaxRuns = 6;
 constexpr int kBars = 3 * kStages + 22;
-constexpr int kStage = 2048;         // bytes in which a softmax warp turns its rows of O around
+constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
 // 384 x 168 (the launch checks that the kernel was built with that number).
@@ -721,38 +721,43 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         if (!ok) break;
         tc_fence_after();
         mine++;
-        // O / sum in 16 bits, 32 columns at a time through shared memory, so that a
-        // store instruction writes eight rows of 64 bytes.  A short loop: code that runs
-        // once an item waits for its instructions.
+        // O / sum in 16 bits, 64 columns at a time through shared memory, so that a
+        // store instruction writes four rows of 128 bytes
         const float inv = 1.f / sum;
         const int live = rows.tokens * p.G - 32 * (warp & 3);        // of this warp's rows
-        uint16_t *out = p.out + ((int64_t)t0 * p.Hq + hk * p.G) * D + 8 * (lane & 3);
+        uint16_t *out = p.out + ((int64_t)t0 * p.Hq + hk * p.G) * D + 8 * (lane & 7);
 #pragma unroll 1
-        for (int h = 0; h < D / 32; h++) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * h, o);
+        for (int h = 0; h < D / 64; h++) {
+            uint32_t o[2][32];
+            tmem_ld32(to + 64 * h, o[0]);
+            tmem_ld32(to + 64 * h + 32, o[1]);
             tmem_wait_ld();
-            if (h == D / 32 - 1) {                       // O is free for the next item
+            if (h == D / 64 - 1) {                       // O is free for the next item
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x.bars.o_free(q));
             }
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
+            for (int j = 0; j < 8; j++) {
+                const uint32_t *v = &o[j / 4][8 * (j & 3)];
                 uint4 r;
-                r.x = Half2<E>::pack(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
-                r.y = Half2<E>::pack(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
-                r.z = Half2<E>::pack(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
-                r.w = Half2<E>::pack(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
-                *reinterpret_cast<uint4 *>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = r;
+                r.x = Half2<E>::pack(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
+                r.y = Half2<E>::pack(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
+                r.z = Half2<E>::pack(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
+                r.w = Half2<E>::pack(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = r;
             }
             __syncwarp();
+            uint4 v[8];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int rr = 8 * j + (lane >> 2), r = 32 * (warp & 3) + rr;
-                const int tok = r * p.inv_G >> 16, head = r - tok * p.G;
-                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-                if (rr < live) *reinterpret_cast<uint4 *>(out + ((int64_t)tok * p.Hq + head) * D + 32 * h) = v;
+            for (int j = 0; j < 8; j++) {
+                const int r = 4 * j + (lane >> 3);
+                v[j] = *reinterpret_cast<const uint4 *>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int rr = 4 * j + (lane >> 3), r = 32 * (warp & 3) + rr, tok = r * p.inv_G >> 16;
+                if (rr < live) *reinterpret_cast<uint4 *>(out + (tok * (p.Hq - p.G) + r) * D + 64 * h) = v[j];
             }
             __syncwarp();
         }
@@ -839,10 +844,19 @@ __global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant_
     const uint16_t *k = p.k + (r.bos + i) * p.k_stride, *v = p.v + (r.bos + i) * p.v_stride;
     uint16_t *to = p.pool + (int64_t)r.entry * 2 * p.Hk * p.pool_rows * D + (int64_t)ring_row(pos, p.sinks, p.pool_rows) * D;
     const int64_t head = (int64_t)p.pool_rows * D;
-    for (int e = lane; e < 2 * p.Hk * (D / 8); e += 32) {
-        const int h = e / (D / 8), at = e % (D / 8) * 8;
-        const uint16_t *from = h < p.Hk ? k + h * D : v + (h - p.Hk) * D;
-        *reinterpret_cast<uint4 *>(to + h * head + at) = *reinterpret_cast<const uint4 *>(from + at);
+    const int n = 2 * p.Hk * (D / 8);                    // vectors of 16 bytes: keys, then values
+    for (int e0 = lane; e0 < n; e0 += 32 * 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int e = e0 + 32 * j, h = e / (D / 8), at = e % (D / 8) * 8;
+            if (e < n) x[j] = *reinterpret_cast<const uint4 *>((h < p.Hk ? k + h * D : v + (h - p.Hk) * D) + at);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int e = e0 + 32 * j, h = e / (D / 8), at = e % (D / 8) * 8;
+            if (e < n) *reinterpret_cast<uint4 *>(to + h * head + at) = x[j];
+        }
     }
 }
 
