@@ -513,10 +513,13 @@ ROPE_LAYOUTS = {"half": KDA_ROPE_HALF, "interleaved": KDA_ROPE_INTERLEAVED}
 
 
 def _handle(stream, device) -> int:
-    import torch
+    """The stream's handle; without one, torch's current stream of the device (its raw handle: building a Stream object
+    for it would cost as much as the rest of a call)."""
+    if stream is None:
+        import torch
 
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return int(s.cuda_stream) if hasattr(s, "cuda_stream") else int(s)
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype16(t, name: str) -> int:
@@ -530,25 +533,30 @@ def _dtype16(t, name: str) -> int:
 
 
 def _rows_of_heads(name: str, t, dtype):
-    """Checks rows of [heads][d] dense elements; returns the rows' distance in elements."""
+    """Checks rows of [heads][d] dense elements; returns the shape and the rows' distance in elements."""
     if not t.is_cuda or t.dim() != 3 or t.dtype != dtype:
         raise ValueError(f"{name} must be a CUDA tensor [rows][heads][d] of q's dtype")
-    (_, h, d), (row, head, one) = t.shape, t.stride()
+    n, h, d = shape = t.shape
+    row, head, one = t.stride()
     if one != 1 or (h > 1 and head != d):
         raise ValueError(f"{name} must be dense within each row")
-    return row if t.shape[0] > 1 else h * d
+    return shape, row if n > 1 else h * d
 
 
-def _table32(name: str, t, n: int):
+def _table32(name: str, t, n: int) -> int:
+    """Checks an int32 [n] table; returns its address."""
     import torch
 
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.shape != (n,):
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.shape != (n,):
         raise ValueError(f"{name} must be int32 [{n}] on the device")
+    return t.data_ptr()
 
 
-def _dense(name: str, t, shape, dtype):
-    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+def _dense(name: str, t, shape, dtype) -> int:
+    """Checks a contiguous tensor; returns its address."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+    return t.data_ptr()
 
 
 def rope_table(max_pos: int, rotary: int, base: float = 10000.0, stretch: float = 1.0, trained: int = 0,
@@ -596,35 +604,37 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     """
     import torch
 
+    dtype = q.dtype
     dt = _dtype16(q, "q")
-    sq, sk = _rows_of_heads("q", q, q.dtype), _rows_of_heads("k", k, q.dtype)
-    (T, Hq, d), Hk = q.shape, k.shape[1]
-    if k.shape[0] != T or k.shape[2] != d:
+    (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
+    k_shape, sk = _rows_of_heads("k", k, dtype)
+    Hk = k_shape[1]
+    if k_shape != (T, Hk, d):
         raise ValueError("k must have q's rows and head size")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _dense(name, w, (d,), torch.float32)
-    rotary = max_pos = 0
-    if (positions is None) != (table is None):
-        raise ValueError("positions and table go together")
-    if table is not None:
+    qw = kw = tab = pos = rotary = max_pos = 0
+    if q_weight is not None:
+        qw = _dense("q_weight", q_weight, (d,), torch.float32)
+    if k_weight is not None:
+        kw = _dense("k_weight", k_weight, (d,), torch.float32)
+    if table is not None and positions is not None:
         if table.dim() != 2:
             raise ValueError("table must be [max_pos][rotary]")
-        max_pos, rotary = table.shape
-        _dense("table", table, (max_pos, rotary), torch.float32)
-        _table32("positions", positions, T)
+        max_pos, rotary = shape = table.shape
+        tab = _dense("table", table, shape, torch.float32)
+        pos = _table32("positions", positions, T)
+    elif table is not None or positions is not None:
+        raise ValueError("positions and table go together")
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     if out is None:
-        q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-        k_out = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device)
+        q_out, k_out = q.new_empty((T, Hq, d)), k.new_empty(k_shape)
     else:
         q_out, k_out = out
-        _dense("out[0]", q_out, (T, Hq, d), q.dtype)
-        _dense("out[1]", k_out, (T, Hk, d), q.dtype)
-    st = load().kda_head_norm_rope(_ptr(q), sq, _ptr(k), sk, _ptr(q_weight), _ptr(k_weight), _ptr(table), max_pos,
-                                   _ptr(positions), _ptr(q_out), _ptr(k_out), T, Hq, Hk, d, rotary,
-                                   ROPE_LAYOUTS[layout], int(norm), eps, dt, _handle(stream, q.device))
+        _dense("out[0]", q_out, (T, Hq, d), dtype)
+        _dense("out[1]", k_out, k_shape, dtype)
+    st = load().kda_head_norm_rope(q.data_ptr(), sq, k.data_ptr(), sk, qw, kw, tab, max_pos, pos, q_out.data_ptr(),
+                                   k_out.data_ptr(), T, Hq, Hk, d, rotary, ROPE_LAYOUTS[layout], 1 if norm else 0, eps,
+                                   dt, _handle(stream, q.device))
     if st != KDA_OK:
         raise KdaError(st, "kda_head_norm_rope")
     return q_out, k_out
@@ -632,26 +642,26 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
 
 def _window_args(q, k, v, kv_pool, slots, N, out):
     """The checks that the two window-attention calls share; returns what both pass on."""
-    import torch
-
+    dtype = q.dtype
     dt = _dtype16(q, "q")
-    strides = _rows_of_heads("q", q, q.dtype), _rows_of_heads("k", k, q.dtype), _rows_of_heads("v", v, q.dtype)
-    (T, Hq, d), Hk = q.shape, k.shape[1]
-    if k.shape[0] != T or k.shape[2] != d or v.shape != k.shape:
+    (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
+    k_shape, sk = _rows_of_heads("k", k, dtype)
+    v_shape, sv = _rows_of_heads("v", v, dtype)
+    Hk = k_shape[1]
+    if k_shape != (T, Hk, d) or v_shape != k_shape:
         raise ValueError("k and v must have q's rows and head size, and the same heads")
-    num_slots = rows = 0
+    num_slots = rows = pool = 0
     if kv_pool is not None:
         if kv_pool.dim() != 5:
             raise ValueError("kv_pool must be [num_slots][2][Hk][rows][d]")
-        num_slots, rows = kv_pool.shape[0], kv_pool.shape[3]
-        _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), q.dtype)
-    if slots is not None:
-        _table32("slots", slots, N)
+        num_slots, _, _, rows, _ = kv_pool.shape
+        pool = _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), dtype)
+    ids = 0 if slots is None else _table32("slots", slots, N)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        out = q.new_empty((T, Hq, d))
     else:
-        _dense("out", out, (T, Hq, d), q.dtype)
-    return dt, strides, T, Hq, Hk, d, num_slots, rows, out
+        _dense("out", out, (T, Hq, d), dtype)
+    return dt, (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv), ids, (pool, num_slots, rows), out, T, Hq, Hk, d
 
 
 def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=None, slots=None, starts=None,
@@ -665,13 +675,11 @@ def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=Non
     [T][Hq][d] (rows of padded sequences keep what ``out`` held).
     """
     N = int(cu_seqlens.shape[0]) - 1
-    dt, (sq, sk, sv), T, Hq, Hk, d, num_slots, rows, out = _window_args(q, k, v, kv_pool, slots, N, out)
-    _table32("cu_seqlens", cu_seqlens, N + 1)
-    if starts is not None:
-        _table32("starts", starts, N)
-    st = load().kda_window_prefill(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(cu_seqlens), _ptr(starts), _ptr(slots),
-                                   _ptr(kv_pool), num_slots, rows, _ptr(out), N, T, Hq, Hk, d, window, sinks,
-                                   d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
+    dt, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out)
+    cu = _table32("cu_seqlens", cu_seqlens, N + 1)
+    st = load().kda_window_prefill(*qkv, cu, 0 if starts is None else _table32("starts", starts, N), ids, *pool,
+                                   out.data_ptr(), N, T, Hq, Hk, d, window, sinks, d ** -0.5 if scale is None else scale,
+                                   dt, _handle(stream, q.device))
     if st != KDA_OK:
         raise KdaError(st, "kda_window_prefill")
     return out
@@ -684,11 +692,9 @@ def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slot
     kv_pool in place.  Returns out [N][Hq][d] (rows of padded sequences, slot -1, keep what ``out`` held).
     """
     N = q.shape[0]
-    dt, (sq, sk, sv), _, Hq, Hk, d, num_slots, rows, out = _window_args(q, k, v, kv_pool, slots, N, out)
-    _table32("positions", positions, N)
-    st = load().kda_window_decode(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(positions), _ptr(slots), _ptr(kv_pool),
-                                  num_slots, rows, _ptr(out), N, Hq, Hk, d, window, sinks,
-                                  d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
+    dt, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out)
+    st = load().kda_window_decode(*qkv, _table32("positions", positions, N), ids, *pool, out.data_ptr(), N, Hq, Hk, d,
+                                  window, sinks, d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
     if st != KDA_OK:
         raise KdaError(st, "kda_window_decode")
     return out
@@ -696,7 +702,7 @@ def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slot
 
 def _pools(pools):
     """A host array of (base, entry_bytes) pairs, the number of slots and the device of a list of pool tensors."""
-    n = int(pools[0].shape[0])
+    n = pools[0].shape[0]
     flat = []
     for p in pools:
         if not p.is_cuda or not p.is_contiguous() or p.dim() < 2 or p.shape[0] != n:
@@ -712,10 +718,8 @@ def slots_copy(pools, src, dst, stream=None) -> None:
     """
     array, n, device = _pools(pools)
     M = int(src.shape[0])
-    _table32("src", src, M)
-    _table32("dst", dst, M)
-    st = load().kda_slots_copy(ctypes.addressof(array), len(array) // 2, n, _ptr(src), _ptr(dst), M,
-                               _handle(stream, device))
+    st = load().kda_slots_copy(ctypes.addressof(array), len(pools), n, _table32("src", src, M), _table32("dst", dst, M),
+                               M, _handle(stream, device))
     if st != KDA_OK:
         raise KdaError(st, "kda_slots_copy")
 
@@ -725,13 +729,11 @@ def slots_compact(pools, slots, new_slots=None, stream=None):
     with m live entries, ids from m on take the free ids below m, both in ascending order.  slots: [N] int32 on the
     device.  Returns new_slots [N] int32, where each went (-1 stays).
     """
-    import torch
-
     array, n, device = _pools(pools)
     N = int(slots.shape[0])
     _table32("slots", slots, N)
     if new_slots is None:
-        new_slots = torch.empty_like(slots)
+        new_slots = slots.new_empty((N,))
     else:
         _table32("new_slots", new_slots, N)
     st = load().kda_slots_compact(ctypes.addressof(array), len(array) // 2, n, _ptr(slots), _ptr(new_slots), N,

@@ -193,11 +193,12 @@ int error_word_address(int **out)
     return st;
 }
 
-int device_facts(int *num_sms, int **err_word)
+int device_facts(int *device, int *num_sms, int **err_word)
 {
     DevInfo *d = nullptr;
     const int st = device_info(&d);
     if (st == KDA_OK) {
+        *device = (int)(d - g_dev);
         *num_sms = d->num_sms;
         *err_word = d->err;
     }

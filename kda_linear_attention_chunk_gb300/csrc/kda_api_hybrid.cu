@@ -10,6 +10,8 @@
 
 namespace {
 
+static_assert(kda::kMaxPools == KDA_MAX_POOLS && kda::kMaxPoolSlots == KDA_MAX_POOL_SLOTS, "the header's limits");
+
 constexpr int64_t kMaxBytes = (int64_t)1 << 40;   // a tensor's span; keeps every product below in 64 bits
 
 struct Span {
@@ -141,8 +143,8 @@ int kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
         overlap(oq, ok))
         return KDA_ERR_ALIAS;
     kda::NormRopeArgs a;
-    int sms;
-    if ((st = kda::device_facts(&sms, &a.err_word)) != KDA_OK) return st;
+    int device, sms;
+    if ((st = kda::device_facts(&device, &sms, &a.err_word)) != KDA_OK) return st;
     if (T == 0) return KDA_OK;
     a.q = q; a.k = k; a.q_stride = q_stride; a.k_stride = k_stride;
     a.q_weight = q_weight; a.k_weight = k_weight; a.table = table; a.positions = positions;
@@ -168,7 +170,7 @@ int kda_window_prefill(const void *q, int64_t q_stride, const void *k, int64_t k
     a.stream = (cudaStream_t)stream;
     int st = check_window(a, T, dtype);
     if (st != KDA_OK) return st;
-    if ((st = kda::device_facts(&a.num_sms, &a.err_word)) != KDA_OK) return st;
+    if ((st = kda::device_facts(&a.device, &a.num_sms, &a.err_word)) != KDA_OK) return st;
     if (T == 0) return KDA_OK;
     return status_of(kda::launch_window_prefill(a));
 }
@@ -189,7 +191,7 @@ int kda_window_decode(const void *q, int64_t q_stride, const void *k, int64_t k_
     int st = check_window(a, N, dtype);
     if (st != KDA_OK) return st;
     if ((int64_t)N * Hq > 0x3fffffff) return KDA_ERR_SHAPE;
-    if ((st = kda::device_facts(&a.num_sms, &a.err_word)) != KDA_OK) return st;
+    if ((st = kda::device_facts(&a.device, &a.num_sms, &a.err_word)) != KDA_OK) return st;
     return status_of(kda::launch_window_decode(a));
 }
 
@@ -205,7 +207,7 @@ int kda_slots_copy(const kda_pool *pools, int num_pools, int num_slots, const in
     if (in_pools(a.pools, num_slots, span(src, (int64_t)M * 4)) ||
         in_pools(a.pools, num_slots, span(dst, (int64_t)M * 4)))
         return KDA_ERR_ALIAS;
-    if ((st = kda::device_facts(&a.num_sms, &a.err_word)) != KDA_OK) return st;
+    if ((st = kda::device_facts(&a.device, &a.num_sms, &a.err_word)) != KDA_OK) return st;
     a.src = src; a.dst = dst; a.new_slots = nullptr; a.M = M; a.num_slots = num_slots;
     a.stream = (cudaStream_t)stream;
     return status_of(kda::launch_slots_copy(a));
@@ -222,7 +224,7 @@ int kda_slots_compact(const kda_pool *pools, int num_pools, int num_slots, const
     if (misaligned(slots, 4) || misaligned(new_slots, 4)) return KDA_ERR_ALIGN;
     const Span si = span(slots, (int64_t)N * 4), so = span(new_slots, (int64_t)N * 4);
     if (overlap(si, so) || in_pools(a.pools, num_slots, si) || in_pools(a.pools, num_slots, so)) return KDA_ERR_ALIAS;
-    if ((st = kda::device_facts(&a.num_sms, &a.err_word)) != KDA_OK) return st;
+    if ((st = kda::device_facts(&a.device, &a.num_sms, &a.err_word)) != KDA_OK) return st;
     a.src = slots; a.dst = new_slots; a.new_slots = new_slots; a.M = N; a.num_slots = num_slots;
     a.stream = (cudaStream_t)stream;
     return status_of(kda::launch_slots_compact(a));

@@ -7,15 +7,29 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kda {
 
 // A position or context length outside its range (clamped): the bit of the
 // sticky device error word that only these kernels set.
 constexpr int kErrBadPosition = 64;
 
-// kda_api.cu: SM count and error word of the current device (checked to be an
-// sm_103 device); returns a kda_status
-int device_facts(int *num_sms, int **err_word);
+// kda_api.cu: ordinal (below 64), SM count and error word of the current device
+// (checked to be an sm_103 device); returns a kda_status
+int device_facts(int *device, int *num_sms, int **err_word);
+
+// Runs `prepare` (a kernel's attributes) once for each device; a failure is
+// returned and tried again by the next call.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> &done, int device, F prepare)
+{
+    const uint64_t bit = (uint64_t)1 << device;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = prepare();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // per-head RMS norm and rotation of q and k
 struct NormRopeArgs {
@@ -45,7 +59,7 @@ struct WindowArgs {
     int N, T, Hq, Hk, d, num_slots, pool_rows, window, sinks;
     float scale;
     bool f16;
-    int num_sms;
+    int device, num_sms;
     cudaStream_t stream;
     int *err_word;
 };
@@ -53,7 +67,7 @@ cudaError_t launch_window_prefill(const WindowArgs &a);
 cudaError_t launch_window_decode(const WindowArgs &a);   // T unused; starts = the tokens' positions
 
 // moves of slot entries in several pools at once
-constexpr int kMaxPools = 128;
+constexpr int kMaxPools = 128, kMaxPoolSlots = 524288;
 struct SlotPools {
     void *base[kMaxPools];
     int64_t entry_bytes[kMaxPools];
@@ -64,7 +78,7 @@ struct SlotMoveArgs {
     const int32_t *src, *dst;        // [M]
     int32_t *new_slots;              // compaction: written from src by the plan kernel, then used as dst
     int M, num_slots;
-    int num_sms;
+    int device, num_sms;
     cudaStream_t stream;
     int *err_word;
 };

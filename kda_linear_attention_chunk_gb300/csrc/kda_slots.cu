@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ 
 // live ids before each of its words, and from both the rank of an id among the
 // high ones (>= m) and the free id below m of the same rank.
 constexpr int kPlanThreads = 1024;
+constexpr int kMaxPlanBytes = kMaxPoolSlots / 32 * 8;
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t *slots, int32_t *new_slots, int N, int num_slots, int *err)
@@ -162,12 +163,13 @@ cudaError_t launch_slots_copy(const SlotMoveArgs &a) { return move(a); }
 cudaError_t launch_slots_compact(const SlotMoveArgs &a)
 {
     const size_t smem = (size_t)((a.num_slots + 31) / 32) * 2 * sizeof(uint32_t);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = once_per_device(ready, a.device, []() {
+        return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPlanBytes);
+    });
+    if (e != cudaSuccess) return e;
     plan_kernel<<<1, kPlanThreads, smem, a.stream>>>(a.src, a.new_slots, a.M, a.num_slots, a.err_word);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     return e == cudaSuccess ? move(a) : e;
 }
 

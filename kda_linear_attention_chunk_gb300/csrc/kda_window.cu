@@ -902,11 +902,16 @@ cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
                        kBox, 1))
         return cudaErrorInvalidValue;
     const int smem = Layout<E, D>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = once_per_device(ready, a.device, [&]() {
+        cudaFuncAttributes built;
+        cudaError_t r = cudaFuncGetAttributes(&built, window_prefill_kernel<E, D>);
+        if (r == cudaSuccess && built.numRegs != kRegs) r = cudaErrorInvalidConfiguration;
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(window_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return r;
+    });
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes built;
-    if ((e = cudaFuncGetAttributes(&built, window_prefill_kernel<E, D>)) != cudaSuccess) return e;
-    if (built.numRegs != kRegs) return cudaErrorInvalidConfiguration;
     window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.pool) return e;

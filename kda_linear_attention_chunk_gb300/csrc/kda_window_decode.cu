@@ -328,7 +328,10 @@ cudaError_t launch(const WindowArgs &a, const DecodeWinParams &p)
     int ranks = 1;
     while (ranks < 8 && units * ranks * 2 <= a.num_sms && ranks * kWarps < steps) ranks *= 2;
     const int smem = sizeof(DecodeSmem<D>);
-    cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = once_per_device(ready, a.device, [&]() {
+        return cudaFuncSetAttribute(window_decode_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * ranks));
