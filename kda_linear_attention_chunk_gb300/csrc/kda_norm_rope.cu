@@ -6,7 +6,7 @@
 // over the pairs (y[i], y[i + r/2]) or (y[2i], y[2i+1]), i < r/2, in fp32 with one
 // rounding at the end.  The pass reads and writes each 16-bit element once, so
 // HBM bounds it.  d/8 lanes hold one head (16 bytes each); a warp takes one token
-// and kUnroll groups of heads, issues all their loads at once, and reads its 8
+// and kUnroll groups of heads, issues all their loads at once, and reads its four
 // cosines and sines of the table once for all of them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,26 +54,36 @@ template <> struct Pair<__half> {
     }
 };
 
-template <typename E>
-__device__ __forceinline__ void up8(const uint4 &r, float (&x)[8])
+// The lane's eight elements as pairs (a[i], b[i]) that turn together.  HALF: a are
+// four consecutive elements and b those half the rotary width further on, so no
+// lane needs another's; INTERLEAVED, and behind the rotary width: eight consecutive.
+template <typename E, bool HALF>
+__device__ __forceinline__ void unpack(const uint2 (&r)[2], float (&a)[4], float (&b)[4])
 {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 p = Pair<E>::up(w[i]);
-        x[2 * i] = p.x;
-        x[2 * i + 1] = p.y;
+    const float2 w0 = Pair<E>::up(r[0].x), w1 = Pair<E>::up(r[0].y), w2 = Pair<E>::up(r[1].x), w3 = Pair<E>::up(r[1].y);
+    if (HALF) {
+        a[0] = w0.x; a[1] = w0.y; a[2] = w1.x; a[3] = w1.y;
+        b[0] = w2.x; b[1] = w2.y; b[2] = w3.x; b[3] = w3.y;
+    } else {
+        a[0] = w0.x; b[0] = w0.y; a[1] = w1.x; b[1] = w1.y;
+        a[2] = w2.x; b[2] = w2.y; a[3] = w3.x; b[3] = w3.y;
     }
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[8])
+template <typename E, bool HALF>
+__device__ __forceinline__ void pack(const float (&a)[4], const float (&b)[4], uint2 (&r)[2])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    if (HALF) {
+        r[0] = make_uint2(Pair<E>::down(a[0], a[1]), Pair<E>::down(a[2], a[3]));
+        r[1] = make_uint2(Pair<E>::down(b[0], b[1]), Pair<E>::down(b[2], b[3]));
+    } else {
+        r[0] = make_uint2(Pair<E>::down(a[0], b[0]), Pair<E>::down(a[1], b[1]));
+        r[1] = make_uint2(Pair<E>::down(a[2], b[2]), Pair<E>::down(a[3], b[3]));
+    }
 }
 
-template <typename E, int D, bool HALF>
+// FULL: every element turns (rotary = D)
+template <typename E, int D, bool HALF, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32)
 norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
@@ -87,90 +97,109 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p)
     if (which) chunk -= p.chunks[0];
     const int c = lane % kLanes, heads = p.heads[which];
     const int head0 = chunk * kPer * kUnroll + lane / kLanes;
+    const int half = FULL ? D / 2 : p.rotary / 2;
+    const bool turns = FULL || 4 * c < half;             // this lane's pairs
+    // elements ea .. ea + 3 and eb .. eb + 3 of a head
+    const int ea = HALF && turns ? 4 * c : 8 * c, eb = HALF && turns ? 4 * c + half : 8 * c + 4;
 
-    const uint16_t *x = p.x[which] + t * p.stride[which] + 8 * c;
-    uint4 raw[kUnroll];
+    const uint16_t *x = p.x[which] + t * p.stride[which];
+    uint2 raw[kUnroll][2];
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
         const int h = head0 + u * kPer;
-        raw[u] = h < heads ? __ldcs(reinterpret_cast<const uint4 *>(x + (int64_t)h * D)) : make_uint4(0, 0, 0, 0);
-    }
-    float w[8], wp[8], cs[8], sn[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) w[i] = wp[i] = 1.f;
-    const int half = p.rotary / 2;
-    const bool turns = 8 * c < p.rotary, first = 8 * c < half;
-    const int shift = turns ? (first ? half / 8 : -(half / 8)) : 0;   // the lane that holds the pairs' other elements
-    if (p.weight[which]) {
-        load8(p.weight[which] + 8 * c, w);
-        if (HALF) load8(p.weight[which] + 8 * (c + shift), wp);
-    }
-    if (p.rotary) {
-        int pos = __ldg(p.positions + t);
-        if (pos < 0 || pos >= p.max_pos) {
-            if (lane == 0) atomicOr(p.err, kErrBadPosition);
-            pos = pos < 0 ? 0 : p.max_pos - 1;
-        }
-        if (turns) {
-            const float *row = p.table + (int64_t)pos * p.rotary;
+        const uint16_t *at = x + (int64_t)h * D;
+        if (h < heads) {
             if (HALF) {
-                load8(row + 8 * c - (first ? 0 : half), cs);
-                load8(row + 8 * c + (first ? half : 0), sn);
-                if (first)
-#pragma unroll
-                    for (int i = 0; i < 8; i++) sn[i] = -sn[i];
+                raw[u][0] = __ldcs(reinterpret_cast<const uint2 *>(at + ea));
+                raw[u][1] = __ldcs(reinterpret_cast<const uint2 *>(at + eb));
             } else {
-                const float4 a = __ldg(reinterpret_cast<const float4 *>(row + 4 * c));
-                const float4 b = __ldg(reinterpret_cast<const float4 *>(row + half + 4 * c));
-                cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
-                sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
+                const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(at + ea));
+                raw[u][0] = make_uint2(r.x, r.y);
+                raw[u][1] = make_uint2(r.z, r.w);
             }
+        } else {
+            raw[u][0] = raw[u][1] = make_uint2(0, 0);
         }
     }
-    uint16_t *y = p.y[which] + (t * heads) * D + 8 * c;
+    // a' = rs (a ac - b bs),  b' = rs (b bc + a as): weights and angles are folded once
+    // for the warp's heads
+    float ac[4], as[4], bc[4], bs[4];
+    {
+        float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (turns && half) {
+            int pos = __ldg(p.positions + t);
+            if (pos < 0 || pos >= p.max_pos) {
+                if (lane == 0) atomicOr(p.err, kErrBadPosition);
+                pos = pos < 0 ? 0 : p.max_pos - 1;
+            }
+            const float *row = p.table + (int64_t)pos * 2 * half + 4 * c;
+            cs = __ldg(reinterpret_cast<const float4 *>(row));
+            sn = __ldg(reinterpret_cast<const float4 *>(row + half));
+        }
+        float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+        if (p.weight[which]) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(p.weight[which] + ea));
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(p.weight[which] + eb));
+            if (HALF) {
+                wa[0] = v.x; wa[1] = v.y; wa[2] = v.z; wa[3] = v.w;
+                wb[0] = w.x; wb[1] = w.y; wb[2] = w.z; wb[3] = w.w;
+            } else {
+                wa[0] = v.x; wb[0] = v.y; wa[1] = v.z; wb[1] = v.w;
+                wa[2] = w.x; wb[2] = w.y; wa[3] = w.z; wb[3] = w.w;
+            }
+        }
+        const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            ac[i] = wa[i] * cv[i];
+            as[i] = wa[i] * sv[i];
+            bc[i] = wb[i] * cv[i];
+            bs[i] = wb[i] * sv[i];
+        }
+    }
+    uint16_t *y = p.y[which] + t * heads * D;
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
         const int h = head0 + u * kPer;
-        float v[8];
-        up8<E>(raw[u], v);
-        float rs = 1.f;
+        float a[4], b[4];
+        unpack<E, HALF>(raw[u], a, b);
         if (p.norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) ss = fmaf(v[i], v[i], ss);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            rs = rsqrtf(ss * (1.f / D) + p.eps);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = v[i] * rs * w[i];
-        if (HALF) {
-            uint4 other;
-            other.x = __shfl_sync(0xffffffffu, raw[u].x, lane + shift);
-            other.y = __shfl_sync(0xffffffffu, raw[u].y, lane + shift);
-            other.z = __shfl_sync(0xffffffffu, raw[u].z, lane + shift);
-            other.w = __shfl_sync(0xffffffffu, raw[u].w, lane + shift);
-            if (turns) {
-                float o[8];
-                up8<E>(other, o);
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = v[i] * cs[i] + (o[i] * rs * wp[i]) * sn[i];
-            }
-        } else if (turns) {
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const float a = v[2 * i], b = v[2 * i + 1];
-                v[2 * i] = a * cs[i] - b * sn[i];
-                v[2 * i + 1] = b * cs[i] + a * sn[i];
+                s0 = fmaf(a[i], a[i], s0);
+                s1 = fmaf(b[i], b[i], s1);
+            }
+            float ss = s0 + s1;
+#pragma unroll
+            for (int k = kLanes / 2; k > 0; k /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+            const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                a[i] *= rs;
+                b[i] *= rs;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float v = a[i], w = b[i];
+            a[i] = v * ac[i];
+            b[i] = w * bc[i];
+            if (turns) {                                 // 0 times an infinity would not be 0
+                a[i] = fmaf(-w, bs[i], a[i]);
+                b[i] = fmaf(v, as[i], b[i]);
             }
         }
         if (h < heads) {
-            uint4 r;
-            r.x = Pair<E>::down(v[0], v[1]);
-            r.y = Pair<E>::down(v[2], v[3]);
-            r.z = Pair<E>::down(v[4], v[5]);
-            r.w = Pair<E>::down(v[6], v[7]);
-            *reinterpret_cast<uint4 *>(y + (int64_t)h * D) = r;
+            uint2 r[2];
+            pack<E, HALF>(a, b, r);
+            uint16_t *at = y + (int64_t)h * D;
+            if (HALF) {
+                __stcs(reinterpret_cast<uint2 *>(at + ea), r[0]);
+                __stcs(reinterpret_cast<uint2 *>(at + eb), r[1]);
+            } else {
+                __stcs(reinterpret_cast<uint4 *>(at + ea), make_uint4(r[0].x, r[0].y, r[1].x, r[1].y));
+            }
         }
     }
 }
@@ -180,10 +209,10 @@ cudaError_t launch(const NormRopeArgs &a, const NormRopeParams &p)
 {
     const int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps * (p.chunks[0] + p.chunks[1]);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (a.layout == 0)
-        norm_rope_kernel<E, D, true><<<(unsigned)blocks, kWarps * 32, 0, a.stream>>>(p);
-    else
-        norm_rope_kernel<E, D, false><<<(unsigned)blocks, kWarps * 32, 0, a.stream>>>(p);
+    const bool full = a.rotary == D;
+    auto *kernel = a.layout == 0 ? (full ? norm_rope_kernel<E, D, true, true> : norm_rope_kernel<E, D, true, false>)
+                                 : (full ? norm_rope_kernel<E, D, false, true> : norm_rope_kernel<E, D, false, false>);
+    kernel<<<(unsigned)blocks, kWarps * 32, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
 
