@@ -598,8 +598,8 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     """Per-head RMS norm and rotation of q and k in one pass, on torch CUDA tensors.
 
     q: [T][Hq][d], k: [T][Hk][d], bfloat16 or float16, d 64 or 128, dense within a row (rows may be slices of a fused
-    projection); q_weight, k_weight: [d] float32 or None; positions: [T] int32 and table: [max_pos][rotary] float32
-    (rope_table), or both None (no rotation); layout "half" or "interleaved".  ``norm`` False rotates only.  Returns
+    projection); q_weight, k_weight: [d] float32 or None; table: [max_pos][rotary] float32 (rope_table) with positions: [T]
+    int32, or None (no rotation); layout "half" or "interleaved".  ``norm`` False rotates only.  Returns
     (q, k), dense; ``out`` may name them (in place where the inputs are dense).
     """
     import torch
@@ -616,14 +616,14 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
         qw = _dense("q_weight", q_weight, (d,), torch.float32)
     if k_weight is not None:
         kw = _dense("k_weight", k_weight, (d,), torch.float32)
-    if table is not None and positions is not None:
+    if table is not None:
+        if positions is None:
+            raise ValueError("a table needs positions")
         if table.dim() != 2:
             raise ValueError("table must be [max_pos][rotary]")
         max_pos, rotary = shape = table.shape
         tab = _dense("table", table, shape, torch.float32)
         pos = _table32("positions", positions, T)
-    elif table is not None or positions is not None:
-        raise ValueError("positions and table go together")
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     if out is None:

@@ -6,18 +6,19 @@
 // Each cached row is read once for all G heads (2 x 2 d bytes against 4 G d
 // operations), so HBM bounds it as long as enough loads are in flight.
 //
-// A CTA of eight warps takes (sequence, key head, up to 16 query heads); a
+// A CTA of four warps takes (sequence, key head, up to 16 query heads); a
 // cluster of CTAs shares one such unit where there are too few units to fill the
-// SMs.  The list of visible rows is dealt to all warps in steps of 16 keys.  The
-// heads are the 16 rows of the warp MMA: S = Q K^T, then O += P V with a running
-// maximum and sum per warp.  Both products take their operands straight from
-// global memory into registers:  the order of the summed index is free, so a
-// lane loads 16 contiguous bytes of a key row and uses them as the operands of
-// two MMAs (q is held in the same order); of the value rows it loads 16 bytes of
-// two neighbouring keys and interleaves them, which permutes only the output
-// columns.  Warps, then CTAs of a cluster (through distributed shared memory),
-// join their (maximum, sum, O) at the end.  The new token's rows are taken from
-// the call's arguments by everyone, so nobody reads the cache row being written.
+// SMs.  The list of visible rows is dealt to all warps in steps of 16 keys, which
+// each warp copies ahead (cp.async) into a ring of kStages steps of its own: the
+// eight warps of an SM keep 128 KB on their way, several times what the latency of
+// HBM asks for.  The heads are the 16 rows of the warp MMA: S = Q K^T, then O += P V with a
+// running maximum and sum per warp.  The order of the summed index is free, so a
+// lane reads 16 contiguous bytes of a key row and uses them as the operands of two
+// MMAs (q is held in the same order); of the value rows it reads 16 bytes of two
+// neighbouring keys and interleaves them, which permutes only the output columns.
+// Warps, then CTAs of a cluster (through distributed shared memory), join their
+// (maximum, sum, O) at the end.  The new token's rows are taken from the call's
+// arguments by everyone, so nobody reads the cache row being written.
 #include <cooperative_groups.h>
 #include <stdint.h>
 
@@ -28,9 +29,32 @@ namespace cg = cooperative_groups;
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 2;  // finer shares of an SM than one CTA of eight warps: 163 us instead of 174 (64 x 8 units)
 constexpr int kHeads = 16;      // query heads of a CTA: the rows of the MMA
 constexpr int kStep = 16;       // keys of a warp at a time
+constexpr int kStages = 3;      // steps in a warp's ring
+
+// 16 bytes from global to shared memory, asynchronously
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 shared16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// Place of 16-byte piece c of row r in a step's tile: the pieces that eight lanes
+// read together (of a key tile four pieces of rows 2i and 2i + 1; of a value tile
+// pieces 2i and 2i + 1 of four rows of one parity) lie in different banks.
+template <int D> __device__ __forceinline__ uint32_t place(int r, int c)
+{
+    return r * (D * 2) + ((c ^ ((r & 6) ^ ((r & 1) << 2))) << 4);
+}
 
 struct DecodeWinParams {
     const uint16_t *q, *k, *v;
@@ -71,7 +95,7 @@ template <int D> struct DecodeSmem {
 };
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 window_decode_kernel(const __grid_constant__ DecodeWinParams p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -138,44 +162,54 @@ window_decode_kernel(const __grid_constant__ DecodeWinParams p)
         for (int j = 0; j < 8; j++) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    uint4 kr[2][D / 32], vr[4][D / 64];
-    auto load_k = [&](int i0) {
+    // this warp's ring; a stage is 16 key rows, then 16 value rows
+    constexpr int kTile = kStep * D * 2;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem_raw) + warp * kStages * 2 * kTile;
+    constexpr int kPieces = D / 8, kRows = 32 / kPieces;   // 16-byte pieces of a row, rows that the warp copies at once
+    const int piece = lane % kPieces;
+    auto fetch = [&](int i0, int stage) {
+        const uint32_t to = ring_at + stage * 2 * kTile;
+        // rows of the ring that follow one another, as most do
+        const int64_t r0 = row_of(i0);
+        const bool run = i0 >= ns && i0 + kStep < count && r0 >= (int64_t)p.sinks * D &&
+                         r0 + (kStep - 1) * D < (int64_t)p.pool_rows * D;
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int64_t r = row_of(i0 + 8 * j + g);
-            const uint16_t *src = (r < 0 ? kn : kc + r) + 8 * c;
-#pragma unroll
-            for (int kk = 0; kk < D / 32; kk++) kr[j][kk] = *reinterpret_cast<const uint4 *>(src + 32 * kk);
-        }
-    };
-    auto load_v = [&](int i0) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int64_t r = row_of(i0 + 2 * c + (j & 1) + 8 * (j >> 1));
-            const uint16_t *src = (r < 0 ? vn : vc + r) + 8 * g;
-#pragma unroll
-            for (int hh = 0; hh < D / 64; hh++) vr[j][hh] = *reinterpret_cast<const uint4 *>(src + 64 * hh);
+        for (int j = 0; j < kStep / kRows; j++) {
+            const int k = j * kRows + lane / kPieces;
+            const int64_t r = run ? r0 + k * D : row_of(i0 + k);
+            copy16(to + place<D>(k, piece), (r < 0 ? kn : kc + r) + 8 * piece);
+            copy16(to + kTile + place<D>(k, piece), (r < 0 ? vn : vc + r) + 8 * piece);
         }
     };
     const int stride = ranks * kWarps * kStep;
-    int i0 = (rank * kWarps + warp) * kStep;
-    if (i0 < count) {
-        load_k(i0);
-        load_v(i0);
+    const int begin = (rank * kWarps + warp) * kStep;
+#pragma unroll
+    for (int s = 0; s < kStages - 1; s++) {
+        if (begin + s * stride < count) fetch(begin + s * stride, s);
+        copy_commit();
     }
-    for (; i0 < count; i0 += stride) {
+    int stage = 0;
+    for (int i0 = begin; i0 < count; i0 += stride) {
+        {
+            const int ahead = i0 + (kStages - 1) * stride;
+            if (ahead < count) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+            copy_commit();
+        }
+        copy_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t kt = ring_at + stage * 2 * kTile, vt = kt + kTile;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         float s[2][4];
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < D / 32; kk++) {
-                mma16816<E>(s[j], qa[kk].x, qb[kk].x, qa[kk].y, qb[kk].y, kr[j][kk].x, kr[j][kk].y);
-                mma16816<E>(s[j], qa[kk].z, qb[kk].z, qa[kk].w, qb[kk].w, kr[j][kk].z, kr[j][kk].w);
+                const uint4 kr = shared16(kt + place<D>(8 * j + g, 4 * kk + c));
+                mma16816<E>(s[j], qa[kk].x, qb[kk].x, qa[kk].y, qb[kk].y, kr.x, kr.y);
+                mma16816<E>(s[j], qa[kk].z, qb[kk].z, qa[kk].w, qb[kk].w, kr.z, kr.w);
             }
         }
-        const int next = i0 + stride;
-        if (next < count) load_k(next);
         if (i0 + kStep > count) {
 #pragma unroll
             for (int j = 0; j < 2; j++)
@@ -224,16 +258,21 @@ window_decode_kernel(const __grid_constant__ DecodeWinParams p)
         const uint32_t p2 = Half2<E>::pack(s[1][0], s[1][1]), p3 = Half2<E>::pack(s[1][2], s[1][3]);
 #pragma unroll
         for (int hh = 0; hh < D / 64; hh++) {
+            const uint4 v0 = shared16(vt + place<D>(2 * c, 8 * hh + g)), v1 = shared16(vt + place<D>(2 * c + 1, 8 * hh + g));
+            const uint4 v2 = shared16(vt + place<D>(2 * c + 8, 8 * hh + g)), v3 = shared16(vt + place<D>(2 * c + 9, 8 * hh + g));
+            const uint32_t r0[4] = {v0.x, v0.y, v0.z, v0.w}, r1[4] = {v1.x, v1.y, v1.z, v1.w};
+            const uint32_t r2[4] = {v2.x, v2.y, v2.z, v2.w}, r3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-                const uint32_t *r0 = &vr[0][hh].x, *r1 = &vr[1][hh].x, *r2 = &vr[2][hh].x, *r3 = &vr[3][hh].x;
                 mma16816<E>(o[hh][j], p0, p1, p2, p3, __byte_perm(r0[j / 2], r1[j / 2], sel),
                             __byte_perm(r2[j / 2], r3[j / 2], sel));
             }
         }
-        if (next < count) load_v(next);
+        __syncwarp();                // the stage may be filled again
     }
+    copy_wait<0>();
+    __syncthreads();                 // the rings become the join's buffers
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -326,8 +365,9 @@ cudaError_t launch(const WindowArgs &a, const DecodeWinParams &p)
     int64_t steps = ((int64_t)p.window + p.sinks + kStep - 1) / kStep;   // at most, of one unit
     if (steps > (p.pool_rows + kStep - 1) / kStep) steps = (p.pool_rows + kStep - 1) / kStep;
     int ranks = 1;
-    while (ranks < 8 && units * ranks * 2 <= a.num_sms && ranks * kWarps < steps) ranks *= 2;
-    const int smem = sizeof(DecodeSmem<D>);
+    while (ranks < 8 && units * ranks * 2 <= kCtasPerSm * a.num_sms && ranks * kWarps < steps) ranks *= 2;
+    constexpr int kRing = kWarps * kStages * 2 * kStep * D * 2, kJoin = sizeof(DecodeSmem<D>);
+    constexpr int smem = kRing > kJoin ? kRing : kJoin;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, a.device, [&]() {
         return cudaFuncSetAttribute(window_decode_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -51,6 +51,14 @@ def test_rotation_alone_and_norm_without_weights(layout):
     check(b, k, kw, None, pos, layout, 0.25, True, "bf16")
 
 
+def test_positions_without_a_table_do_not_turn():
+    q, k, qw, kw, pos, _ = draw(6, 4, 2, 64, "fp16", 0, seed=4)
+    a, b = kda.head_norm_rope(q, k, qw, kw, positions=pos, table=None)
+    check(a, q, qw, None, pos, "half", 1e-6, True, "fp16")
+    with pytest.raises(ValueError):
+        kda.head_norm_rope(q, k, qw, kw, table=kda.rope_table(500, 16))
+
+
 def test_in_place_equals_out_of_place():
     t = torch()
     q, k, qw, kw, pos, table = draw(77, 12, 4, 128, "bf16", 128, seed=5, fused=False)
