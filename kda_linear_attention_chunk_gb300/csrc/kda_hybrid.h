@@ -1,5 +1,5 @@
 // kda_hybrid.h -- launch interface of the kernels around a hybrid stack's
-// softmax layers (kda_norm_rope.cu, kda_window.cu, kda_window_decode.cu,
+// softmax layers (kda_norm_rope.cu, kda_window.cu, kda_window_rows.cu,
 // kda_slots.cu) for the C ABI (kda_api_hybrid.cu).  Not installed; the public
 // interface is include/kda.h.
 #pragma once

@@ -38,19 +38,6 @@ namespace {
 
 using namespace sm100;
 
-struct PrefillParams {
-    const uint16_t *k, *v;           // the call's rows (for the cache kernel)
-    int64_t k_stride, v_stride;
-    const int32_t *cu, *starts, *slots;
-    uint16_t *pool, *out;
-    int N, T, Hq, Hk, num_slots, pool_rows, window, sinks;
-    int G, tile_tokens;              // query heads per key head; tokens of a query tile
-    int inv_G;                       // ceil(2^16 / G): r / G = r inv_G >> 16 for r < 128
-    int items;                       // numbers of items, at least as many as there are
-    float scale_log2;
-    int *err;
-};
-
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is rounded up to
@@ -176,71 +163,8 @@ __device__ __forceinline__ void loaded(uint32_t (&a)[32], uint32_t (&b)[32], uin
     for (int i = 0; i < 32; i++) asm volatile("" : "+r"(a[i]), "+r"(b[i]), "+r"(c[i]), "+r"(d[i]));
 }
 
-// The spans of `span` rows of a packed batch are numbered so that sequence n has the
-// numbers from cu[n] / span + n on: at least as many as it has spans, without a
-// pass over the table.  A sequence's facts:
-struct Sequence {
-    int cu0, cu1, start, slot;       // its two table entries, context length and slot, as they are
-    int part;                        // the number's place among the sequence's spans (may be past its rows)
-};
-
-// The last sequence whose numbers start at or before `number`, by a converged warp:
-// 32 probes at a time, the last of which bring the facts along.
-__device__ __forceinline__ Sequence sequence_of(const PrefillParams &p, int span, int number, int lane)
-{
-    int a = 0, n = p.N;              // the answer is in [a, a + n)
-    while (n > 32) {
-        const int step = (n + 31) / 32, at = a + lane * step;
-        const bool le = lane * step < n && p.cu[at] / span + at <= number;
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, le || lane == 0));
-        n = min(step, n - last * step);
-        a += last * step;
-    }
-    const int at = a + min(lane, n - 1);
-    Sequence s;
-    s.cu0 = p.cu[at];
-    s.cu1 = p.cu[at + 1];
-    s.start = p.starts ? p.starts[at] : 0;
-    s.slot = p.slots ? p.slots[at] : at;
-    s.part = number - (s.cu0 / span + at);
-    const int who = 31 - __clz(__ballot_sync(0xffffffffu, (lane < n && s.part >= 0) || lane == 0));
-    s.cu0 = __shfl_sync(0xffffffffu, s.cu0, who);
-    s.cu1 = __shfl_sync(0xffffffffu, s.cu1, who);
-    s.start = __shfl_sync(0xffffffffu, s.start, who);
-    s.slot = __shfl_sync(0xffffffffu, s.slot, who);
-    s.part = __shfl_sync(0xffffffffu, s.part, who);
-    return s;
-}
-
-// The rows that number `number` stands for, all checked; `reports`: whether this
-// warp tells of entries out of range.
-struct Rows {
-    int bos, len, start, entry;      // the sequence's first row, rows, context length, cache entry
-    int from, n;                     // the span's first row within the sequence, and its rows (0: none)
-};
-__device__ __forceinline__ Rows rows_of(const PrefillParams &p, int span, int number, int lane, bool reports)
-{
-    const Sequence s = sequence_of(p, span, number, lane);
-    reports = reports && lane == 0 && s.part == 0;
-    Rows r;
-    r.bos = clamp_row(s.cu0, p.T, reports ? p.err : nullptr);
-    r.len = max(0, clamp_row(s.cu1, p.T, reports ? p.err : nullptr) - r.bos);
-    const int most = 0x7fffffff - r.len;
-    r.start = min(max(s.start, 0), most);
-    if (r.start != s.start && reports) atomicOr(p.err, kErrBadPosition);
-    r.entry = s.slot;
-    if (p.slots && (s.slot < 0 || s.slot >= p.num_slots)) {
-        if (s.slot != -1 && reports) atomicOr(p.err, kErrBadSlot);
-        r.entry = -1;
-    }
-    const int64_t from = (int64_t)s.part * span;
-    r.n = s.part < 0 || from >= r.len || r.entry < 0 ? 0 : (int)min((int64_t)span, r.len - from);
-    r.from = r.n ? (int)from : 0;
-    return r;
-}
-
 // runs of consecutive rows that hold the positions [a, b) of the sequence
-__device__ __forceinline__ void add_runs(Item &c, const PrefillParams &p, int bos, int start, int a, int b)
+__device__ __forceinline__ void add_runs(Item &c, const WindowParams &p, int bos, int start, int a, int b)
 {
     auto add = [&](int cached, int row, int pos, int len) {
         if (len > 0) c.runs[c.nruns++] = {cached, row, pos, len};
@@ -341,7 +265,7 @@ struct Maps {
 
 // What every role knows.
 struct Ctx {
-    const PrefillParams &p;
+    const WindowParams &p;
     Ctl &c;
     Bars bars;
     uint8_t *smem;                   // 1024-byte aligned
@@ -365,7 +289,7 @@ struct Ctx {
 // other round in reverse order, so that late ones, which have most keys, are dealt
 // evenly) and writes it to `item`; the warp's lanes agree on what is returned.
 // False: there is none.
-__device__ __forceinline__ bool find_item(const PrefillParams &p, int &round, Item &item, int lane)
+__device__ __forceinline__ bool find_item(const WindowParams &p, int &round, Item &item, int lane)
 {
     const int span = 2 * p.tile_tokens;
     for (;; round++) {
@@ -401,7 +325,7 @@ template <typename E, int D>
 __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
 {
     using L = Layout<E, D>;
-    const PrefillParams &p = x.p;
+    const WindowParams &p = x.p;
     const uint32_t sq = x.base, skv = x.base + 2 * L::kTile;
     int it = 0, round = 0, item = 0, qs[2] = {0, 0};     // tiles and query tiles loaded, items written
     bool ok = true, more = true;
@@ -482,7 +406,7 @@ template <typename E, int D>
 __device__ __forceinline__ void product_role(const Ctx &x, int which)
 {
     using L = Layout<E, D>;
-    const PrefillParams &p = x.p;
+    const WindowParams &p = x.p;
     const int q = __shfl_sync(0xffffffffu, which, 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
     const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q;
@@ -605,7 +529,7 @@ template <typename E, int D>
 __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
 {
     using L = Layout<E, D>;
-    const PrefillParams &p = x.p;
+    const WindowParams &p = x.p;
     const int q = warp >> 2, row = 32 * (warp & 3) + x.lane, lane = x.lane;
     const int token = row * p.inv_G >> 16;               // row / G
     const uint32_t lanes = x.tmem + ((uint32_t)(warp & 3) << 21);
@@ -769,7 +693,7 @@ template <typename E, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mpool,
-                      const __grid_constant__ PrefillParams p)
+                      const __grid_constant__ WindowParams p)
 {
     using L = Layout<E, D>;
     extern __shared__ uint8_t smem_raw[];
@@ -833,7 +757,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 constexpr int kCommitRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant__ PrefillParams p)
+__global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant__ WindowParams p)
 {
     const int lane = threadIdx.x & 31;
     const Rows r = rows_of(p, kCommitRows, blockIdx.x, lane, false);
@@ -889,8 +813,21 @@ bool make_map(CUtensorMap *m, const void *base, bool f16, int d, int64_t n1, int
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the call has so few query rows a sequence and key head (on average) that
+// the warp-MMA kernel, which takes 16 to 64 of them at a time, is faster than tiles
+// of 128: up to 32, and up to 256 where so few items leave most SMs without a tile
+// (the other kernel spreads each over eight CTAs).  Measured (us, warp-MMA / tiles;
+// G = 4, d = 128): 64 sequences, window 1024: 16 rows 65 / 90, 32 rows 85 / 91, 64
+// rows 139 / 106; one sequence, window 4096: 32 rows 26 / 64, 256 rows 57 / 66, 512
+// rows 67 / 67; 16 fresh sequences: 64 rows 23 / 23, 256 rows 34 / 23.
+bool few_rows(const WindowParams &p, int num_sms)
+{
+    const int64_t rows = (int64_t)p.T * p.G;
+    return rows <= (int64_t)32 * p.N || (rows <= (int64_t)256 * p.N && p.items * 8 <= num_sms);
+}
+
 template <typename E, int D>
-cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
+cudaError_t launch_tiles(const WindowArgs &a, const WindowParams &p)
 {
     CUtensorMap mq, mk, mv, mpool;
     if (!make_map(&mq, a.q, a.f16, D, a.Hq, D, a.T, a.q_stride, p.G, p.tile_tokens) ||
@@ -913,7 +850,13 @@ cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
     });
     if (e != cudaSuccess) return e;
     window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
-    e = cudaGetLastError();
+    return cudaGetLastError();
+}
+
+template <typename E, int D>
+cudaError_t launch(const WindowArgs &a, const WindowParams &p)
+{
+    cudaError_t e = few_rows(p, a.num_sms) ? launch_window_rows(a) : launch_tiles<E, D>(a, p);
     if (e != cudaSuccess || !a.pool) return e;
     ring_commit_kernel<D><<<p.T / kCommitRows + p.N, 256, 0, a.stream>>>(p);
     return cudaGetLastError();
@@ -923,21 +866,12 @@ cudaError_t launch(const WindowArgs &a, const PrefillParams &p)
 
 cudaError_t launch_window_prefill(const WindowArgs &a)
 {
-    PrefillParams p;
-    p.k = (const uint16_t *)a.k; p.v = (const uint16_t *)a.v;
-    p.k_stride = a.k_stride; p.v_stride = a.v_stride;
-    p.cu = a.cu_seqlens; p.starts = a.starts; p.slots = a.slots;
-    p.pool = (uint16_t *)a.pool; p.out = (uint16_t *)a.out;
-    p.N = a.N; p.T = a.T; p.Hq = a.Hq; p.Hk = a.Hk; p.num_slots = a.num_slots; p.pool_rows = a.pool_rows;
-    p.window = a.window; p.sinks = a.sinks;
-    p.G = a.Hq / a.Hk;
+    WindowParams p = window_params(a);
     p.tile_tokens = 128 / p.G;
     p.inv_G = (65536 + p.G - 1) / p.G;
     const int64_t items = ((int64_t)a.T / (2 * p.tile_tokens) + a.N) * a.Hk;
     if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
     p.items = (int)items;
-    p.scale_log2 = a.scale * kLog2e;
-    p.err = a.err_word;
     if (a.d == 128) return a.f16 ? launch<__half, 128>(a, p) : launch<__nv_bfloat16, 128>(a, p);
     return a.f16 ? launch<__half, 64>(a, p) : launch<__nv_bfloat16, 64>(a, p);
 }

@@ -38,6 +38,83 @@ __device__ __forceinline__ int ring_row(int p, int sinks, int rows)
     return p < sinks ? p : sinks + (p - sinks) % (rows - sinks);
 }
 
+struct WindowParams {
+    const uint16_t *q, *k, *v;       // the call's rows
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu, *starts, *slots;   // starts: context lengths (decode: the tokens' positions)
+    uint16_t *pool, *out;
+    int N, T, Hq, Hk, num_slots, pool_rows, window, sinks;
+    int G, tile_tokens;              // query heads per key head; tokens of a query tile
+    int inv_G;                       // ceil(2^16 / G): r / G = r inv_G >> 16 for r < 128
+    int items;                       // numbers of items, at least as many as there are
+    int groups;                      // groups of up to 16 query heads per key head (warp-MMA kernel)
+    float scale_log2;
+    int *err;
+};
+
+// The spans of `span` rows of a packed batch are numbered so that sequence n has the
+// numbers from cu[n] / span + n on: at least as many as it has spans, without a
+// pass over the table.  A sequence's facts:
+struct Sequence {
+    int cu0, cu1, start, slot;       // its two table entries, context length and slot, as they are
+    int part;                        // the number's place among the sequence's spans (may be past its rows)
+};
+
+// The last sequence whose numbers start at or before `number`, by a converged warp:
+// 32 probes at a time, the last of which bring the facts along.
+__device__ __forceinline__ Sequence sequence_of(const WindowParams &p, int span, int number, int lane)
+{
+    int a = 0, n = p.N;              // the answer is in [a, a + n)
+    while (n > 32) {
+        const int step = (n + 31) / 32, at = a + lane * step;
+        const bool le = lane * step < n && p.cu[at] / span + at <= number;
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, le || lane == 0));
+        n = min(step, n - last * step);
+        a += last * step;
+    }
+    const int at = a + min(lane, n - 1);
+    Sequence s;
+    s.cu0 = p.cu[at];
+    s.cu1 = p.cu[at + 1];
+    s.start = p.starts ? p.starts[at] : 0;
+    s.slot = p.slots ? p.slots[at] : at;
+    s.part = number - (s.cu0 / span + at);
+    const int who = 31 - __clz(__ballot_sync(0xffffffffu, (lane < n && s.part >= 0) || lane == 0));
+    s.cu0 = __shfl_sync(0xffffffffu, s.cu0, who);
+    s.cu1 = __shfl_sync(0xffffffffu, s.cu1, who);
+    s.start = __shfl_sync(0xffffffffu, s.start, who);
+    s.slot = __shfl_sync(0xffffffffu, s.slot, who);
+    s.part = __shfl_sync(0xffffffffu, s.part, who);
+    return s;
+}
+
+// The rows that number `number` stands for, all checked; `reports`: whether this
+// warp tells of entries out of range.
+struct Rows {
+    int bos, len, start, entry;      // the sequence's first row, rows, context length, cache entry
+    int from, n;                     // the span's first row within the sequence, and its rows (0: none)
+};
+__device__ __forceinline__ Rows rows_of(const WindowParams &p, int span, int number, int lane, bool reports)
+{
+    const Sequence s = sequence_of(p, span, number, lane);
+    reports = reports && lane == 0 && s.part == 0;
+    Rows r;
+    r.bos = clamp_row(s.cu0, p.T, reports ? p.err : nullptr);
+    r.len = max(0, clamp_row(s.cu1, p.T, reports ? p.err : nullptr) - r.bos);
+    const int most = 0x7fffffff - r.len;
+    r.start = min(max(s.start, 0), most);
+    if (r.start != s.start && reports) atomicOr(p.err, kErrBadPosition);
+    r.entry = s.slot;
+    if (p.slots && (s.slot < 0 || s.slot >= p.num_slots)) {
+        if (s.slot != -1 && reports) atomicOr(p.err, kErrBadSlot);
+        r.entry = -1;
+    }
+    const int64_t from = (int64_t)s.part * span;
+    r.n = s.part < 0 || from >= r.len || r.entry < 0 ? 0 : (int)min((int64_t)span, r.len - from);
+    r.from = r.n ? (int)from : 0;
+    return r;
+}
+
 template <typename E> struct Half2;
 template <> struct Half2<__nv_bfloat16> {
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
@@ -58,5 +135,24 @@ template <> struct Half2<__half> {
     }
     static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 };
+
+inline WindowParams window_params(const WindowArgs &a)
+{
+    WindowParams p = {};
+    p.q = (const uint16_t *)a.q; p.k = (const uint16_t *)a.k; p.v = (const uint16_t *)a.v;
+    p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
+    p.cu = a.cu_seqlens; p.starts = a.starts; p.slots = a.slots;
+    p.pool = (uint16_t *)a.pool; p.out = (uint16_t *)a.out;
+    p.N = a.N; p.T = a.T; p.Hq = a.Hq; p.Hk = a.Hk; p.num_slots = a.num_slots; p.pool_rows = a.pool_rows;
+    p.window = a.window; p.sinks = a.sinks;
+    p.G = a.Hq / a.Hk;
+    p.scale_log2 = a.scale * kLog2e;
+    p.err = a.err_word;
+    return p;
+}
+
+// The warp-MMA kernel for few rows a sequence (kda_window_rows.cu), without the
+// writing of the cache.
+cudaError_t launch_window_rows(const WindowArgs &a);
 
 }  // namespace kda

@@ -127,7 +127,7 @@ class Batch:
         return out
 
 
-HEADS = [(1, 1), (2, 2), (6, 2), (5, 1), (8, 1), (14, 2), (16, 1), (40, 2)]
+HEADS = [(1, 1), (2, 2), (6, 2), (5, 1), (8, 1), (14, 2), (16, 1), (40, 2), (48, 1), (128, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -136,6 +136,24 @@ HEADS = [(1, 1), (2, 2), (6, 2), (5, 1), (8, 1), (14, 2), (16, 1), (40, 2)]
 def test_prefill_heads_and_types(Hq, Hk, d, dtype):
     b = Batch([0, 30, 3], Hq, Hk, d, window=11, sinks=2, dtype=dtype, seed=Hq)
     b.prefill([37, 1, 20])
+
+
+# (sequences, rows of each) with few rows a sequence, where the warp-MMA kernel runs, and with more, where the
+# tensor-core tiles do: rows x query heads per key head at most 32 a sequence, or up to 256 of a single sequence
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 1), (10, 2), (16, 1), (20, 1), (33, 1), (64, 1), (100, 1), (128, 1)])
+@pytest.mark.parametrize("N,L", [(40, 1), (40, 2), (7, 5), (1, 3), (1, 8), (1, 70), (5, 40), (3, 300)])
+def test_prefill_from_few_rows_to_many(N, L, Hq, Hk, d):
+    """Both kernels and every sharing of keys between warps, over contexts around the window and the ring's wrap."""
+    b = Batch([(37 * i + 5) % 90 for i in range(N)], Hq, Hk, d, window=24, sinks=3, dtype="bf16", seed=N + Hq)
+    b.prefill([L + (i % 3 == 1) - (i % 4 == 2) for i in range(N)], check_rows=[0, 1, 2, 4, 7, 8, 31, 39, 64, 127, 128, 299])
+
+
+@pytest.mark.parametrize("lens", [[1] * 60 + [700], [0] * 50 + [90, 0, 3], [2] * 3 + [500] + [0] * 70])
+def test_prefill_mixed_lengths_under_one_rule(lens):
+    """The kernel is chosen by the average: long sequences among many short ones."""
+    b = Batch([20 + 3 * i for i in range(len(lens))], 8, 2, 64, window=40, sinks=2, dtype="bf16", seed=len(lens))
+    b.prefill(lens, check_rows=[0, 1, 3, 15, 16, 63, 64, 130, 499, 699])
 
 
 @pytest.mark.parametrize("window,sinks,extra", [(1, 0, 0), (1, 3, 0), (2, 0, 5), (16, 16, 0), (17, 1, 3), (63, 0, 1),
@@ -180,6 +198,7 @@ def test_prefill_padded_and_bad_slots():
     t = torch()
     b = Batch([10, 20, 30, 0], 4, 2, 128, window=9, sinks=2, dtype="bf16", seed=5)
     b.prefill([12, 40, 3, 8], padded=(1,))
+    b.prefill([120, 140, 300, 8], padded=(2,))
     kda.device_error(reset=True)
     q, k, v = b.new_rows(9)
     ids = b.ids()
@@ -213,32 +232,34 @@ def test_prefill_bad_sequence_table_stays_in_bounds():
     assert kda.device_error(reset=True) == kda.ERR_BAD_SEQLENS
 
 
-def test_masked_keys_never_reach_an_output():
+@pytest.mark.parametrize("T", [80, 400])
+def test_masked_keys_never_reach_an_output(T):
     """Keys that are infinite, NaN or of the type's lowest value change only the rows that see them; rows that see
     them would give NaN."""
     t = torch()
     for bad in (float("inf"), float("-inf"), float("nan"), t.finfo(t.bfloat16).min):
         b = Batch([0], 4, 2, 128, window=6, sinks=0, dtype="bf16", seed=8)
-        q, k, v = b.new_rows(80, fused=False)
-        clean = kda.window_prefill(q, k, v, b.int32([0, 80]), 6)
+        q, k, v = b.new_rows(T, fused=False)
+        clean = kda.window_prefill(q, k, v, b.int32([0, T]), 6)
         k2 = k.clone()
         k2[3] = bad
         k2[40] = bad
-        got = kda.window_prefill(q, k2, v, b.int32([0, 80]), 6)
-        seen = [r for r in range(80) if 3 <= r < 9 or 40 <= r < 46]
-        rest = [r for r in range(80) if r not in seen]
+        got = kda.window_prefill(q, k2, v, b.int32([0, T]), 6)
+        seen = [r for r in range(T) if 3 <= r < 9 or 40 <= r < 46]
+        rest = [r for r in range(T) if r not in seen]
         assert t.equal(got[rest], clean[rest])
 
 
-def test_values_of_other_sequences_never_reach_an_output():
+@pytest.mark.parametrize("a,b_,c", [(19, 40, 61), (5, 12, 20), (300, 511, 700)])
+def test_values_of_other_sequences_never_reach_an_output(a, b_, c):
     t = torch()
     b = Batch([0, 0, 0], 4, 2, 64, window=20, sinks=3, dtype="bf16", seed=9)
-    q, k, v = b.new_rows(61, fused=False)
-    cu = b.int32([0, 19, 40, 61])
+    q, k, v = b.new_rows(c, fused=False)
+    cu = b.int32([0, a, b_, c])
     clean = kda.window_prefill(q, k, v, cu, 20, sinks=3)
-    k[19:40], v[19:40] = float("nan"), float("nan")
+    k[a:b_], v[a:b_] = float("nan"), float("nan")
     got = kda.window_prefill(q, k, v, cu, 20, sinks=3)
-    assert t.equal(got[:19], clean[:19]) and t.equal(got[40:], clean[40:])
+    assert t.equal(got[:a], clean[:a]) and t.equal(got[b_:], clean[b_:])
 
 
 def test_large_scores_and_lowest_values():
