@@ -40,7 +40,8 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;           // keys of a tile
-constexpr int kBox = 32;             // rows of a TMA box: what a ragged tile is rounded up to
+constexpr int kBox = 16;             // rows of a TMA box: what a run is rounded up to
+constexpr int kBigBox = 64;          // rows of one where a run has as many
 constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
 constexpr int kMaxRuns = 6;
 constexpr int kBars = 3 * kStages + 22;
@@ -188,33 +189,59 @@ __device__ __forceinline__ void add_runs(Item &c, const WindowParams &p, int bos
     add(0, bos + from - start, from, b - from);
 }
 
-// walks the tiles of the runs
+// A piece of a key tile: `take` consecutive rows in its columns from `col` on.
+struct Piece {
+    int cached, row, pos, take, col;
+};
+
+// Walks the tiles of an item's runs.  A tile is filled with runs one after the other,
+// each from a multiple of 16 columns on, up to 128 columns.
 struct Tiles {
     const Item &c;
-    int run = 0, off = 0;
-    int cached, row, pos, count;
+    int run = 0, off = 0;            // where the next tile starts
+    int run0 = 0, off0 = 0;          // where this one does
+    int keys;                        // columns, a multiple of 16
+    int lo, hi, low;                 // lowest and highest position, lowest that is no sink
+    bool complete;                   // no column without a key
     __device__ explicit Tiles(const Item &item) : c(item) {}
-    __device__ bool next()
+    // the piece that starts at (r, o), column `col`; moves on to the next
+    __device__ Piece piece(int &r, int &o, int &col) const
+    {
+        const Run &x = c.runs[r];
+        const Piece s = {x.cached, x.row + o, x.pos + o, min(kKeys - col, x.len - o), col};
+        o += s.take;
+        if (o >= x.len) {
+            r++;
+            o = 0;
+        }
+        col += (s.take + 15) & ~15;
+        return s;
+    }
+    __device__ bool next(int sinks)
     {
         if (run >= c.nruns) return false;
-        const Run &r = c.runs[run];
-        cached = r.cached;
-        row = r.row + off;
-        pos = r.pos + off;
-        count = min(kKeys, r.len - off);
-        off += count;
-        if (off >= r.len) {
-            run++;
-            off = 0;
-        }
+        run0 = run;
+        off0 = off;
+        keys = 0;
+        lo = low = 0x7fffffff;
+        hi = -1;
+        complete = true;
+        do {
+            const Piece s = piece(run, off, keys);
+            const int end = s.pos + s.take - 1;
+            lo = min(lo, s.pos);
+            hi = max(hi, end);
+            if (end >= sinks) low = min(low, max(s.pos, sinks));
+            if (s.take & 15) complete = false;
+        } while (keys < kKeys && run < c.nruns);
         return true;
     }
 };
 
-// whether any of the positions [first, last] sees any key of the tile
+// whether any of the positions [first, last] sees any key of the tile (or may)
 __device__ __forceinline__ bool sees(const Tiles &t, int first, int last, int window, int sinks)
 {
-    return first <= last && t.pos <= last && (t.pos + t.count - 1 > first - window || t.pos < sinks);
+    return first <= last && t.lo <= last && (t.hi > first - window || t.lo < sinks);
 }
 
 // positions of an item's query tile q
@@ -259,8 +286,9 @@ struct Bars {
 };
 constexpr int kItemReaders = 8 + 2 + 1;   // softmax warps, product warps, patch warp
 
+// Tensor maps; k, v and pool: boxes of kBox rows, then of kBigBox.
 struct Maps {
-    const CUtensorMap *q, *k, *v, *pool;
+    CUtensorMap q, k[2], v[2], pool[2];
 };
 
 // What every role knows.
@@ -345,31 +373,37 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         const int entry_head = __shfl_sync(0xffffffffu, now.entry, 0) * 2 * p.Hk + hk;
         bool queries = false;
         Tiles t(now);
-        while (ok && __shfl_sync(0xffffffffu, t.next(), 0)) {
-            const int boxes = __shfl_sync(0xffffffffu, (t.count + kBox - 1) / kBox, 0);
-            const int row = __shfl_sync(0xffffffffu, t.row, 0);
-            const bool cached = __shfl_sync(0xffffffffu, t.cached, 0);
+        while (ok && __shfl_sync(0xffffffffu, t.next(p.sinks), 0)) {
+            const int keys = __shfl_sync(0xffffffffu, t.keys, 0);
 #pragma unroll
             for (int kv = 0; kv < 2; kv++) {
                 const int s = it % kStages;
                 if (ok && it >= kStages) ok = x.wait(x.bars.empty(s), it / kStages - 1);
                 if (!ok) break;
-                if (elect_one()) {
-                    const uint32_t bar = x.bars.full(s), to = skv + s * L::kTile;
-                    mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kBox * 128 * (D / 64)));
-                    if (cached) {
-                        for (int b = 0; b < boxes; b++)
+                const uint32_t bar = x.bars.full(s), to = skv + s * L::kTile;
+                if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(keys * 128 * (D / 64)));
+                __syncwarp();
+                for (int r = t.run0, o = t.off0, col = 0; col < keys;) {
+                    const Piece piece = t.piece(r, o, col);
+                    const int take = __shfl_sync(0xffffffffu, piece.take, 0), at = __shfl_sync(0xffffffffu, piece.col, 0);
+                    const int row = __shfl_sync(0xffffffffu, piece.row, 0);
+                    const bool cached = __shfl_sync(0xffffffffu, piece.cached, 0);
+                    if (elect_one()) {
+                        const CUtensorMap *const of = cached ? maps.pool : kv ? maps.v : maps.k;
+                        const int c1 = cached ? row : hk, c2 = cached ? entry_head + kv * p.Hk : row;
+                        int b = 0;
+                        for (; b + kBigBox <= take; b += kBigBox)
 #pragma unroll
                             for (int h = 0; h < D / 64; h++)
-                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), maps.pool, 64 * h, row + b * kBox,
-                                            entry_head + kv * p.Hk, bar);
-                    } else {
-                        for (int b = 0; b < boxes; b++)
+                                tma_load_3d(to + h * L::kHalf + (at + b) * 128, of + 1, 64 * h, c1 + (cached ? b : 0),
+                                            c2 + (cached ? 0 : b), bar);
+                        for (; b < take; b += kBox)
 #pragma unroll
                             for (int h = 0; h < D / 64; h++)
-                                tma_load_3d(to + h * L::kHalf + b * (kBox * 128), kv ? maps.v : maps.k, 64 * h, hk,
-                                            row + b * kBox, bar);
+                                tma_load_3d(to + h * L::kHalf + (at + b) * 128, of, 64 * h, c1 + (cached ? b : 0),
+                                            c2 + (cached ? 0 : b), bar);
                     }
+                    __syncwarp();
                 }
                 it++;
                 if (queries) continue;
@@ -381,7 +415,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                         mbar_arrive_expect_tx(x.bars.q_full(q), (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64)));
 #pragma unroll
                         for (int h = 0; h < D / 64; h++)
-                            tma_load_3d(sq + q * L::kTile + h * L::kHalf, maps.q, 64 * h, hk * p.G,
+                            tma_load_3d(sq + q * L::kTile + h * L::kHalf, &maps.q, 64 * h, hk * p.G,
                                         t0 + q * p.tile_tokens, x.bars.q_full(q));
                     }
                     if (ok) qs[q]++;
@@ -422,28 +456,28 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
         const bool both = tokens > p.tile_tokens, any = __shfl_sync(0xffffffffu, rows.tokens > 0, 0);
         int done = 0;                                    // products P V of this item
         Tiles t(now);
-        bool have = __shfl_sync(0xffffffffu, t.next(), 0);
+        bool have = __shfl_sync(0xffffffffu, t.next(p.sinks), 0);
         bool sees_now = __shfl_sync(0xffffffffu, sees(t, rows.first, rows.last, p.window, p.sinks), 0);
-        int count = __shfl_sync(0xffffffffu, t.count, 0);
+        int keys = __shfl_sync(0xffffffffu, t.keys, 0);
         ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), mine));
         if (elect_one()) {
             if (ok && sees_now) {
-                mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc((count + 15) & ~15, 0, L::kF16));
+                mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc(keys, 0, L::kF16));
                 mma_commit(x.bars.s_full(q));
             }
             mma_commit(x.bars.empty(it % kStages));
         }
         it++;
         while (have && ok) {
-            const int sv = it % kStages, steps = (count + 15) / 16;   // this tile's values
+            const int sv = it % kStages, steps = keys / 16;       // this tile's values
             const bool saw = sees_now;
             ok = x.wait(x.bars.values(sv), it / kStages);
             it++;
             const int sk = it % kStages;                 // the next tile's keys
-            have = __shfl_sync(0xffffffffu, t.next(), 0);
+            have = __shfl_sync(0xffffffffu, t.next(p.sinks), 0);
             if (have) {
                 sees_now = __shfl_sync(0xffffffffu, sees(t, rows.first, rows.last, p.window, p.sinks), 0);
-                count = __shfl_sync(0xffffffffu, t.count, 0);
+                keys = __shfl_sync(0xffffffffu, t.keys, 0);
                 ok = ok && x.wait(x.bars.full(sk), it / kStages);
                 it++;
             } else if (any && elect_one()) {
@@ -468,7 +502,7 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
             }
             if (elect_one()) {
                 if (ok && have && sees_now) {
-                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc((count + 15) & ~15, 0, L::kF16));
+                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc(keys, 0, L::kF16));
                     mma_commit(x.bars.s_full(q));
                 }
                 if (both) mbar_arrive(x.bars.turn(!q));
@@ -490,28 +524,33 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
 }
 
 // ---- zeros behind ragged runs ------------------------------------------------------
-// Value rows past a run hold anything, and 0 x NaN is NaN: the rows that the last 16
-// keys of its tile are rounded up to become zeros.  Every value tile passes through
+// Value rows past a run hold anything, and 0 x NaN is NaN: the rows that a run is
+// rounded up to become zeros.  Every value tile passes through
 // here.
 template <typename E, int D>
 __device__ __forceinline__ void patch_role(const Ctx &x)
 {
     using L = Layout<E, D>;
+    const WindowParams &p = x.p;
     bool ok = true;
     for (int item = 0, it = 1; ok; item++) {
         const Item &now = x.c.items[item & 1];
         ok = x.wait(x.bars.item_full(item & 1), item / 2);
         if (!ok || now.tokens == 0) break;
         Tiles t(now);
-        for (; ok && t.next(); it += 2) {
+        for (; ok && t.next(p.sinks); it += 2) {
             const int s = it % kStages;
             ok = x.wait(x.bars.full(s), it / kStages);
             if (!ok) break;
-            if (t.count & 15) {
-                for (int e = x.lane; e < (16 - (t.count & 15)) * (D / 8); e += 32) {
-                    const int r = t.count + e / (D / 8), v = e % (D / 8);
-                    *reinterpret_cast<uint4 *>(x.smem + (2 + s) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
-                        make_uint4(0, 0, 0, 0);
+            if (!t.complete) {
+                for (int r = t.run0, o = t.off0, col = 0; col < t.keys;) {
+                    const Piece piece = t.piece(r, o, col);
+                    const int from = piece.col + piece.take;
+                    for (int e = x.lane; e < (col - from) * (D / 8); e += 32) {
+                        const int at = from + e / (D / 8), v = e % (D / 8);
+                        *reinterpret_cast<uint4 *>(x.smem + (2 + s) * L::kTile + (v / 8) * L::kHalf + at * 128 + (v % 8) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
                 }
                 fence_proxy_async_smem();
             }
@@ -549,11 +588,10 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         const int pos = rows.first + token, t0 = now.t0 + q * p.tile_tokens, hk = now.hk;
         float m = -INFINITY, sum = 0.f;
         Tiles t(now);
-        while (rows.tokens && t.next()) {
+        while (rows.tokens && t.next(p.sinks)) {
             if (!sees(t, rows.first, rows.last, p.window, p.sinks)) continue;
             // every key of the tile visible to every row of the warp: no test per key
-            const bool whole = t.count == kKeys && t.pos + kKeys - 1 <= lo_row &&
-                               (t.pos > hi_row - p.window || t.pos + kKeys <= p.sinks);
+            const bool whole = t.complete && t.keys == kKeys && t.hi <= lo_row && t.low > hi_row - p.window;
             ok = mbar_wait(x.bars.s_full(q), it & 1, x.abort);
             if (!ok) break;
             it++;
@@ -568,18 +606,24 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             uint32_t s[4][32];
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                if (32 * i < t.count) tmem_ld32(ts + 32 * i, s[i]);
+                if (32 * i < t.keys) tmem_ld32(ts + 32 * i, s[i]);
             loaded(s[0], s[1], s[2], s[3]);
             if (!whole) {
-                const int hi = min(pos - t.pos, t.count - 1);        // last visible column
-                const int lo = max(pos - p.window, -1) - t.pos;      // columns up to here are behind the window
-                const int sk = p.sinks - t.pos;                      // unless they are sinks
+                uint32_t seen[4] = {0, 0, 0, 0};         // visible columns
+                for (int r = t.run0, o = t.off0, col = 0; col < t.keys;) {
+                    const Piece s = t.piece(r, o, col);
+                    const int end = s.col + min(s.take, pos - s.pos + 1);            // columns at or before the row
+                    const int old = s.col + max(pos - p.window, -1) - s.pos + 1;     // columns behind the window,
+                    const int sink = s.col + p.sinks - s.pos;                        // but for the sinks
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        seen[i] |= below(end - 32 * i) & ~below(s.col - 32 * i) & ~(below(old - 32 * i) & ~below(sink - 32 * i));
+                }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const uint32_t seen = below(hi + 1 - 32 * i) & ~(below(lo + 1 - 32 * i) & ~below(sk - 32 * i));
 #pragma unroll
                     for (int j = 0; j < 32; j++)
-                        if (!(seen & (1u << j))) s[i][j] = 0xff800000u;   // -inf
+                        if (!(seen[i] & (1u << j))) s[i][j] = 0xff800000u;   // -inf
                 }
             }
             float mx[4];
@@ -618,7 +662,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(x.bars.p_half(q));
                 }
-                if (32 * i < t.count) {
+                if (32 * i < t.keys) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
@@ -691,9 +735,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
 
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mpool,
-                      const __grid_constant__ WindowParams p)
+window_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowParams p)
 {
     using L = Layout<E, D>;
     extern __shared__ uint8_t smem_raw[];
@@ -723,10 +765,12 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             mbar_init(bars.item_empty(q), kItemReaders);
         }
         mbar_fence_init();
-        tma_prefetch_desc(&mq);
-        tma_prefetch_desc(&mk);
-        tma_prefetch_desc(&mv);
-        tma_prefetch_desc(&mpool);
+        tma_prefetch_desc(&maps.q);
+        for (int i = 0; i < 2; i++) {
+            tma_prefetch_desc(&maps.k[i]);
+            tma_prefetch_desc(&maps.v[i]);
+            tma_prefetch_desc(&maps.pool[i]);
+        }
     }
     if (warp == 9) {
         tmem_alloc(smem_u32(&c.tmem), 512);
@@ -738,7 +782,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const Ctx x{p, c, bars, smem, base, c.tmem, lane, &c.abort};
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (warp == 8) load_role<E, D>(x, Maps{&mq, &mk, &mv, &mpool});
+        if (warp == 8) load_role<E, D>(x, maps);
         else if (warp == 10) patch_role<E, D>(x);
         else product_role<E, D>(x, warp == 11);
     } else {
@@ -829,15 +873,17 @@ bool few_rows(const WindowParams &p, int num_sms)
 template <typename E, int D>
 cudaError_t launch_tiles(const WindowArgs &a, const WindowParams &p)
 {
-    CUtensorMap mq, mk, mv, mpool;
-    if (!make_map(&mq, a.q, a.f16, D, a.Hq, D, a.T, a.q_stride, p.G, p.tile_tokens) ||
-        !make_map(&mk, a.k, a.f16, D, a.Hk, D, a.T, a.k_stride, 1, kBox) ||
-        !make_map(&mv, a.v, a.f16, D, a.Hk, D, a.T, a.v_stride, 1, kBox))
-        return cudaErrorInvalidValue;
-    if (!a.pool) mpool = mk;         // never used: no position is before the call's
-    else if (!make_map(&mpool, a.pool, a.f16, D, a.pool_rows, D, (int64_t)a.num_slots * 2 * a.Hk, (int64_t)a.pool_rows * D,
-                       kBox, 1))
-        return cudaErrorInvalidValue;
+    Maps maps;
+    bool ok = make_map(&maps.q, a.q, a.f16, D, a.Hq, D, a.T, a.q_stride, p.G, p.tile_tokens);
+    for (int i = 0; i < 2 && ok; i++) {
+        const int box = i ? kBigBox : kBox;
+        ok = make_map(&maps.k[i], a.k, a.f16, D, a.Hk, D, a.T, a.k_stride, 1, box) &&
+             make_map(&maps.v[i], a.v, a.f16, D, a.Hk, D, a.T, a.v_stride, 1, box);
+        if (!a.pool) maps.pool[i] = maps.k[i];           // never used: no position is before the call's
+        else ok = ok && make_map(&maps.pool[i], a.pool, a.f16, D, a.pool_rows, D, (int64_t)a.num_slots * 2 * a.Hk,
+                                 (int64_t)a.pool_rows * D, box, 1);
+    }
+    if (!ok) return cudaErrorInvalidValue;
     const int smem = Layout<E, D>::kSmem;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, a.device, [&]() {
@@ -849,7 +895,7 @@ cudaError_t launch_tiles(const WindowArgs &a, const WindowParams &p)
         return r;
     });
     if (e != cudaSuccess) return e;
-    window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(mq, mk, mv, mpool, p);
+    window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(maps, p);
     return cudaGetLastError();
 }
 
