@@ -779,6 +779,7 @@ window_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_go_on();
     const Ctx x{p, c, bars, smem, base, c.tmem, lane, &c.abort};
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -806,9 +807,15 @@ __global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant_
     const int lane = threadIdx.x & 31;
     const Rows r = rows_of(p, kCommitRows, blockIdx.x, lane, false);
     const int i = r.from + (threadIdx.x >> 5);           // this warp's row of the sequence
+    // The attention kernel may still be running, and reads the cached rows of sequences
+    // that have some; nobody leaves before it is done.
+    if (r.start != 0 || i >= r.from + r.n) grid_wait();
     if (i >= r.from + r.n) return;
     const int pos = r.start + i, ring = p.pool_rows - p.sinks;
-    if (pos >= p.sinks && r.len - i > ring) return;      // a later row of the call takes its place
+    if (pos >= p.sinks && r.len - i > ring) {            // a later row of the call takes its place
+        grid_wait();
+        return;
+    }
     const uint16_t *k = p.k + (r.bos + i) * p.k_stride, *v = p.v + (r.bos + i) * p.v_stride;
     uint16_t *to = p.pool + (int64_t)r.entry * 2 * p.Hk * p.pool_rows * D + (int64_t)ring_row(pos, p.sinks, p.pool_rows) * D;
     const int64_t head = (int64_t)p.pool_rows * D;
@@ -826,6 +833,7 @@ __global__ void __launch_bounds__(256) ring_commit_kernel(const __grid_constant_
             if (e < n) *reinterpret_cast<uint4 *>(to + h * head + at) = x[j];
         }
     }
+    grid_wait();
 }
 
 // The driver's tensor-map encoder, looked up once.
@@ -904,8 +912,18 @@ cudaError_t launch(const WindowArgs &a, const WindowParams &p)
 {
     cudaError_t e = few_rows(p, a.num_sms) ? launch_window_rows(a) : launch_tiles<E, D>(a, p);
     if (e != cudaSuccess || !a.pool) return e;
-    ring_commit_kernel<D><<<p.T / kCommitRows + p.N, 256, 0, a.stream>>>(p);
-    return cudaGetLastError();
+    // its CTAs start where those of the attention kernel have ended
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.T / kCommitRows + p.N));
+    cfg.blockDim = dim3(256);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, ring_commit_kernel<D>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace

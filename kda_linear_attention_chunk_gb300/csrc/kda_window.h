@@ -21,6 +21,11 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Programmatic dependent launch: the next kernel of the stream may start where this
+// one leaves room; and in that kernel, waiting for the end of the one before.
+__device__ __forceinline__ void grid_go_on() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // the pool entry of sequence n: -1 for a padded one; an id out of range is
 // reported (by the caller that `reports`) and skipped
 __device__ __forceinline__ int entry_of(const int32_t *slots, int n, int num_slots, int *err, bool reports)

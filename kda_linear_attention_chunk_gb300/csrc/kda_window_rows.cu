@@ -105,6 +105,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int part = warp / SHARE, sub = warp % SHARE;   // which keys, which rows
 
+    if (MANY) grid_go_on();
     int unit = blockIdx.x / ranks;
     const int group = unit % p.groups;
     unit /= p.groups;
