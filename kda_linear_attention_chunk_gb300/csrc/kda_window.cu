@@ -226,6 +226,7 @@ struct Tiles {
         lo = low = 0x7fffffff;
         hi = -1;
         complete = true;
+#pragma unroll 1
         do {
             const Piece s = piece(run, off, keys);
             const int end = s.pos + s.take - 1;
@@ -375,7 +376,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         Tiles t(now);
         while (ok && __shfl_sync(0xffffffffu, t.next(p.sinks), 0)) {
             const int keys = __shfl_sync(0xffffffffu, t.keys, 0);
-#pragma unroll
+#pragma unroll 1
             for (int kv = 0; kv < 2; kv++) {
                 const int s = it % kStages;
                 if (ok && it >= kStages) ok = x.wait(x.bars.empty(s), it / kStages - 1);
@@ -383,6 +384,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                 const uint32_t bar = x.bars.full(s), to = skv + s * L::kTile;
                 if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(keys * 128 * (D / 64)));
                 __syncwarp();
+#pragma unroll 1
                 for (int r = t.run0, o = t.off0, col = 0; col < keys;) {
                     const Piece piece = t.piece(r, o, col);
                     const int take = __shfl_sync(0xffffffffu, piece.take, 0), at = __shfl_sync(0xffffffffu, piece.col, 0);
@@ -392,13 +394,15 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                         const CUtensorMap *const of = cached ? maps.pool : kv ? maps.v : maps.k;
                         const int c1 = cached ? row : hk, c2 = cached ? entry_head + kv * p.Hk : row;
                         int b = 0;
+#pragma unroll 1
                         for (; b + kBigBox <= take; b += kBigBox)
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < D / 64; h++)
                                 tma_load_3d(to + h * L::kHalf + (at + b) * 128, of + 1, 64 * h, c1 + (cached ? b : 0),
                                             c2 + (cached ? 0 : b), bar);
+#pragma unroll 1
                         for (; b < take; b += kBox)
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < D / 64; h++)
                                 tma_load_3d(to + h * L::kHalf + (at + b) * 128, of, 64 * h, c1 + (cached ? b : 0),
                                             c2 + (cached ? 0 : b), bar);
@@ -408,6 +412,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                 it++;
                 if (queries) continue;
                 queries = true;                          // after the first keys, which need not wait for their room
+#pragma unroll 1
                 for (int q = 0; q < nq && ok; q++) {
                     if (qs[q]) ok = x.wait(x.bars.q_empty(q), qs[q] - 1);
                     if (ok && elect_one()) {
@@ -425,8 +430,10 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
     }
     if (!ok && x.lane == 0) x.give_up();
     // nothing may still be on its way into shared memory when the CTA ends
+#pragma unroll 1
     for (int q = 0; q < 2; q++)
         if (qs[q]) mbar_wait_drain(x.bars.q_full(q), (qs[q] - 1) & 1);
+#pragma unroll 1
     for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(x.bars.full(i % kStages), (i / kStages) & 1);
 }
 
@@ -543,9 +550,11 @@ __device__ __forceinline__ void patch_role(const Ctx &x)
             ok = x.wait(x.bars.full(s), it / kStages);
             if (!ok) break;
             if (!t.complete) {
+#pragma unroll 1
                 for (int r = t.run0, o = t.off0, col = 0; col < t.keys;) {
                     const Piece piece = t.piece(r, o, col);
                     const int from = piece.col + piece.take;
+#pragma unroll 1
                     for (int e = x.lane; e < (col - from) * (D / 8); e += 32) {
                         const int at = from + e / (D / 8), v = e % (D / 8);
                         *reinterpret_cast<uint4 *>(x.smem + (2 + s) * L::kTile + (v / 8) * L::kHalf + at * 128 + (v % 8) * 16) =
@@ -610,6 +619,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             loaded(s[0], s[1], s[2], s[3]);
             if (!whole) {
                 uint32_t seen[4] = {0, 0, 0, 0};         // visible columns
+#pragma unroll 1
                 for (int r = t.run0, o = t.off0, col = 0; col < t.keys;) {
                     const Piece s = t.piece(r, o, col);
                     const int end = s.col + min(s.take, pos - s.pos + 1);            // columns at or before the row
