@@ -44,7 +44,7 @@ constexpr int kBox = 16;             // rows of a TMA box: what a run is rounded
 constexpr int kBigBox = 64;          // rows of one where a run has as many
 constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
 constexpr int kMaxRuns = 6;
-constexpr int kBars = 3 * kStages + 22;
+constexpr int kBars = 3 * kStages + 23;
 constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
@@ -59,7 +59,7 @@ struct Run {
 };
 
 // One item of work: two query tiles of one key head.
-struct Item {
+struct alignas(16) Item {
     Run runs[kMaxRuns];
     int nruns;
     int tokens;                      // rows of the item; 0: there are no more items
@@ -69,6 +69,7 @@ struct Item {
 
 struct Ctl {
     Item items[2];
+    uint4 claim;                     // the answer to a claim (16-byte aligned by what precedes it)
     int abort;
     uint32_t tmem;
     uint64_t bars[kBars];
@@ -282,6 +283,7 @@ struct Bars {
     __device__ uint32_t o_free(int q) const { return at + 8 * (3 * kStages + 12 + q); }   // O read
     __device__ uint32_t turn(int q) const { return at + 8 * (3 * kStages + 14 + q); }
     __device__ uint32_t drained(int q) const { return at + 8 * (3 * kStages + 16 + q); }
+    __device__ uint32_t claimed() const { return at + 8 * (3 * kStages + 22); }     // a claim is answered
     __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kStages + 18 + i); }
     __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kStages + 20 + i); }
 };
@@ -314,18 +316,50 @@ struct Ctx {
     }
 };
 
-// Finds the CTA's next item from number `at` on (numbers go up by gridDim.x, every
-// other round in reverse order, so that late ones, which have most keys, are dealt
-// evenly) and writes it to `item`; the warp's lanes agree on what is returned.
-// False: there is none.
-__device__ __forceinline__ bool find_item(const WindowParams &p, int &round, Item &item, int lane)
+// The grid has a CTA for each number of an item.  A CTA on an SM, done with its own,
+// takes over that of one that has not started yet (cluster launch control), so items
+// of any length are dealt evenly without a counter in memory.  Late positions, which
+// have most keys, come first.
+__device__ __forceinline__ void claim_cta(uint32_t answer, uint32_t bar)
 {
-    const int span = 2 * p.tile_tokens;
-    for (;; round++) {
-        const int64_t at = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if ((int64_t)round * gridDim.x >= p.items) return false;
-        if (at >= p.items) continue;
-        const int number = p.items - 1 - (int)at, slot = number / p.Hk, hk = number - slot * p.Hk;
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+                 "r"(bar) : "memory");
+}
+// the number of the CTA that was taken over, -1 if none is left
+__device__ __forceinline__ int claimed_cta(uint32_t answer)
+{
+    int cta;
+    asm volatile("{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%1];\n"
+                 " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n mov.b32 %0, -1;\n"
+                 " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n}" : "=r"(cta) : "r"(answer) : "memory");
+    return cta;
+}
+
+// Writes the CTA's next item to `item`; `claims`: how many were made (0: its own comes
+// first).  The lanes of the converged warp agree on what is returned: 1 found, 0 none
+// left, -1 a wait gave up.
+__device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item)
+{
+    const WindowParams &p = x.p;
+    const int span = 2 * p.tile_tokens, lane = x.lane;
+    const uint32_t answer = smem_u32(&x.c.claim);
+    for (bool own = claims == 0;; own = false) {
+        int at = blockIdx.x;
+        if (!own) {
+            if (elect_one()) claim_cta(answer, x.bars.claimed());
+            __syncwarp();
+            if (!x.wait(x.bars.claimed(), claims - 1)) {
+                mbar_wait_drain(x.bars.claimed(), (claims - 1) & 1);
+                return -1;
+            }
+            at = __shfl_sync(0xffffffffu, claimed_cta(answer), 0);
+            fence_proxy_async_smem();                    // the next answer is written behind this read
+            __syncwarp();
+        }
+        claims++;
+        if (at < 0) return 0;
+        const int number = p.items - 1 - at, slot = number / p.Hk, hk = number - slot * p.Hk;
         const Rows r = rows_of(p, span, slot, lane, hk == 0);
         if (!r.n) continue;          // past the sequence's rows, or padded
         if (lane == 0) {
@@ -344,8 +378,7 @@ __device__ __forceinline__ bool find_item(const WindowParams &p, int &round, Ite
             }
         }
         __syncwarp();
-        round++;
-        return true;
+        return 1;
     }
 }
 
@@ -356,13 +389,16 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
     using L = Layout<E, D>;
     const WindowParams &p = x.p;
     const uint32_t sq = x.base, skv = x.base + 2 * L::kTile;
-    int it = 0, round = 0, item = 0, qs[2] = {0, 0};     // tiles and query tiles loaded, items written
+    int it = 0, claims = 0, item = 0, qs[2] = {0, 0};    // tiles and query tiles loaded, items written
     bool ok = true, more = true;
     while (ok && more) {
         Item &now = x.c.items[item & 1];
         if (item >= 2) ok = x.wait(x.bars.item_empty(item & 1), item / 2 - 1);
         if (!ok) break;
-        more = find_item(p, round, now, x.lane);
+        const int found = find_item(x, claims, now);
+        ok = found >= 0;
+        more = found > 0;
+        if (!ok) break;
         if (x.lane == 0) {
             if (!more) now.tokens = 0;
             mbar_arrive(x.bars.item_full(item & 1));
@@ -774,6 +810,7 @@ window_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__
             mbar_init(bars.item_full(q), 1);
             mbar_init(bars.item_empty(q), kItemReaders);
         }
+        mbar_init(bars.claimed(), 1);
         mbar_fence_init();
         tma_prefetch_desc(&maps.q);
         for (int i = 0; i < 2; i++) {
@@ -913,7 +950,7 @@ cudaError_t launch_tiles(const WindowArgs &a, const WindowParams &p)
         return r;
     });
     if (e != cudaSuccess) return e;
-    window_prefill_kernel<E, D><<<p.items < a.num_sms ? p.items : a.num_sms, kThreads, smem, a.stream>>>(maps, p);
+    window_prefill_kernel<E, D><<<p.items, kThreads, smem, a.stream>>>(maps, p);
     return cudaGetLastError();
 }
 
