@@ -9,6 +9,7 @@
 
 #include "kda_common.cuh"
 #include "kda_hybrid.h"
+#include "kda_pdl.cuh"
 
 namespace kda {
 namespace {
@@ -27,6 +28,7 @@ struct MoveParams {
 
 __global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ MoveParams p)
 {
+    grid_wait();                                      // for the plan, where there is one
     const int64_t items = p.pieces * p.M;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         int64_t piece = item / p.M;
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t *slots, int32_t *new_slots, int N, int num_slots, int *err)
 {
     extern __shared__ uint32_t sm[];
+    grid_go_on();
     const int words = (num_slots + 31) / 32, tid = threadIdx.x;
     uint32_t *map = sm, *before = sm + words;     // before[w]: live ids in words < w
     __shared__ uint32_t part[kPlanThreads / 32];
@@ -144,7 +147,8 @@ plan_kernel(const int32_t *slots, int32_t *new_slots, int N, int num_slots, int 
     }
 }
 
-cudaError_t move(const SlotMoveArgs &a)
+// planned: behind the plan kernel, whose end its CTAs, already there, wait for
+cudaError_t move(const SlotMoveArgs &a, bool planned)
 {
     MoveParams p;
     p.pools = a.pools;
@@ -152,13 +156,22 @@ cudaError_t move(const SlotMoveArgs &a)
     p.pieces = 0;
     for (int i = 0; i < a.pools.n; i++) p.pieces += (a.pools.entry_bytes[i] + kPiece - 1) / kPiece;
     const int64_t items = p.pieces * a.M, most = (int64_t)a.num_sms * 64;
-    move_kernel<<<(unsigned)(items < most ? items : most), kThreads, 0, a.stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = planned;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, move_kernel, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
-cudaError_t launch_slots_copy(const SlotMoveArgs &a) { return move(a); }
+cudaError_t launch_slots_copy(const SlotMoveArgs &a) { return move(a, false); }
 
 cudaError_t launch_slots_compact(const SlotMoveArgs &a)
 {
@@ -170,7 +183,7 @@ cudaError_t launch_slots_compact(const SlotMoveArgs &a)
     if (e != cudaSuccess) return e;
     plan_kernel<<<1, kPlanThreads, smem, a.stream>>>(a.src, a.new_slots, a.M, a.num_slots, a.err_word);
     e = cudaGetLastError();
-    return e == cudaSuccess ? move(a) : e;
+    return e == cudaSuccess ? move(a, true) : e;
 }
 
 }  // namespace kda

@@ -8,6 +8,7 @@
 
 #include "kda_common.cuh"
 #include "kda_hybrid.h"
+#include "kda_pdl.cuh"
 
 namespace kda {
 
@@ -20,11 +21,6 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// Programmatic dependent launch: the next kernel of the stream may start where this
-// one leaves room; and in that kernel, waiting for the end of the one before.
-__device__ __forceinline__ void grid_go_on() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // the pool entry of sequence n: -1 for a padded one; an id out of range is
 // reported (by the caller that `reports`) and skipped
