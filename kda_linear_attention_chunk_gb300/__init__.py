@@ -627,7 +627,8 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     if out is None:
-        q_out, k_out = q.new_empty((T, Hq, d)), k.new_empty(k_shape)
+        q_out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
+        k_out = torch.empty(k_shape, dtype=dtype, device=q.device)
     else:
         q_out, k_out = out
         _dense("out[0]", q_out, (T, Hq, d), dtype)
@@ -642,6 +643,8 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
 
 def _window_args(q, k, v, kv_pool, slots, N, out):
     """The checks that the two window-attention calls share; returns what both pass on."""
+    import torch
+
     dtype = q.dtype
     dt = _dtype16(q, "q")
     (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
@@ -658,7 +661,7 @@ def _window_args(q, k, v, kv_pool, slots, N, out):
         pool = _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), dtype)
     ids = 0 if slots is None else _table32("slots", slots, N)
     if out is None:
-        out = q.new_empty((T, Hq, d))
+        out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
     else:
         _dense("out", out, (T, Hq, d), dtype)
     return dt, (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv), ids, (pool, num_slots, rows), out, T, Hq, Hk, d
@@ -729,11 +732,13 @@ def slots_compact(pools, slots, new_slots=None, stream=None):
     with m live entries, ids from m on take the free ids below m, both in ascending order.  slots: [N] int32 on the
     device.  Returns new_slots [N] int32, where each went (-1 stays).
     """
+    import torch
+
     array, n, device = _pools(pools)
     N = int(slots.shape[0])
     _table32("slots", slots, N)
     if new_slots is None:
-        new_slots = slots.new_empty((N,))
+        new_slots = torch.empty((N,), dtype=torch.int32, device=device)
     else:
         _table32("new_slots", new_slots, N)
     st = load().kda_slots_compact(ctypes.addressof(array), len(array) // 2, n, _ptr(slots), _ptr(new_slots), N,

@@ -33,6 +33,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 2;  // finer shares of an SM than one CTA of eight warps: 163 us instead of 174 (64 x 8 units)
 constexpr int kRows = 16;       // query rows of a warp: the rows of the MMA
+constexpr int kMaxRanks = 8;    // CTAs of a cluster
 constexpr int kStep = 16;       // keys at a time
 constexpr int kTiles = kStep / 8;   // score tiles of a step
 constexpr int kStages = 3;      // steps in a ring, for each warp that shares it
@@ -128,9 +129,9 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         tokens = r.n;
     } else {
         t0 = bos = unit / p.Hk;
+        start = p.starts[t0];
         entry = entry_of(p.slots, t0, p.num_slots, p.err, reports && lane == 0);
         if (entry < 0) return;
-        start = p.starts[t0];
         if (start < 0) {
             if (reports && lane == 0) atomicOr(p.err, kErrBadPosition);
             start = 0;
@@ -395,17 +396,32 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         const int r = e / kQuads, d4 = e % kQuads;
         float *ms = &sm.m[r / kRows][r % kRows], *ls = &sm.l[r / kRows][r % kRows];
         float4 *os = reinterpret_cast<float4 *>(sm.o[r / kRows][r % kRows]) + d4;
-        float m = -INFINITY, l = 0.f;
-        for (int k = 0; k < ranks; k++) m = fmaxf(m, *cluster.map_shared_rank(ms, k));
+        // all the ranks' parts are on their way together: a read of another CTA takes some
+        // hundred nanoseconds
+        float mk[kMaxRanks], lk[kMaxRanks], m = -INFINITY, l = 0.f;
+        float4 ok[kMaxRanks];
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; k++) {
+            mk[k] = -INFINITY;
+            lk[k] = 0.f;
+            ok[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < ranks) {
+                mk[k] = *cluster.map_shared_rank(ms, k);
+                lk[k] = *cluster.map_shared_rank(ls, k);
+                ok[k] = *cluster.map_shared_rank(os, k);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; k++) m = fmaxf(m, mk[k]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < ranks; k++) {
-            const float f = m == -INFINITY ? 0.f : ex2((*cluster.map_shared_rank(ms, k) - m) * p.scale_log2);
-            const float4 x = *cluster.map_shared_rank(os, k);
-            l += *cluster.map_shared_rank(ls, k) * f;
-            acc.x += x.x * f;
-            acc.y += x.y * f;
-            acc.z += x.z * f;
-            acc.w += x.w * f;
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; k++) {
+            const float f = mk[k] == -INFINITY ? 0.f : ex2((mk[k] - m) * p.scale_log2);
+            l += lk[k] * f;
+            acc.x += ok[k].x * f;
+            acc.y += ok[k].y * f;
+            acc.z += ok[k].z * f;
+            acc.w += ok[k].w * f;
         }
         const float inv = 1.f / l;
         uint2 r2;
@@ -427,7 +443,7 @@ cudaError_t launch(const WindowArgs &a, WindowParams p)
     int64_t steps = (int64_t)p.window + p.sinks + p.tile_tokens - 1, held = (int64_t)(p.pool ? p.pool_rows : 0) + p.T;
     steps = ((steps < held ? steps : held) + kStep - 1) / kStep;
     int ranks = 1;
-    while (ranks < 8 && units * ranks * 2 <= kCtasPerSm * a.num_sms && ranks * (kWarps / SHARE) < steps) ranks *= 2;
+    while (ranks < kMaxRanks && units * ranks * 2 <= kCtasPerSm * a.num_sms && ranks * (kWarps / SHARE) < steps) ranks *= 2;
     if (units * ranks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int kRings = kWarps * kStages * 2 * kStep * D * 2, kJoin = sizeof(JoinSmem<D>);
     constexpr int smem = kRings > kJoin ? kRings : kJoin;
