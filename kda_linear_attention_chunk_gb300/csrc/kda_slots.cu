@@ -2,7 +2,7 @@
 // at once: pure data movement, bound by HBM.
 //
 // The work is cut into pieces of kPiece bytes of one entry; a CTA copies one
-// piece with eight 16-byte loads in flight per thread.  Pieces are ordered with
+// piece with four 16-byte loads in flight per thread.  Pieces are ordered with
 // the moves innermost, so the forks of one source read each of its pieces
 // together (from L2 after the first).
 #include <stdint.h>
@@ -15,8 +15,8 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 8;                              // 16-byte vectors per thread and piece
-constexpr int64_t kPiece = kThreads * kVecs * 16;     // 32 KB
+constexpr int kVecs = 4;                              // 16-byte vectors per thread and piece
+constexpr int64_t kPiece = kThreads * kVecs * 16;     // 16 KB
 
 struct MoveParams {
     SlotPools pools;
