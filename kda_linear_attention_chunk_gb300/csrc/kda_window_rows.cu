@@ -146,7 +146,8 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
     const int ring = p.pool_rows - p.sinks, wrap0 = max(lo, p.sinks);
     const int ring0 = p.pool ? (wrap0 - p.sinks) % ring : 0;
     const int64_t head_rows = (int64_t)p.pool_rows * D;
-    uint16_t *kc = p.pool ? p.pool + ((int64_t)entry * 2 * p.Hk + hk) * head_rows : nullptr, *vc = kc + p.Hk * head_rows;
+    uint16_t *kc = p.pool ? p.pool + ((int64_t)entry * 2 * p.Hk + hk) * head_rows : nullptr;
+    const int64_t v_behind = p.Hk * head_rows;           // from a key row to its value row
     const uint16_t *kn = p.k + bos * p.k_stride + hk * D, *vn = p.v + bos * p.v_stride + hk * D;
     // row in the cache of list item i (which is there)
     auto cache_row = [&](int i) {
@@ -159,7 +160,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         const int64_t at = (int64_t)ring_row(first, p.sinks, p.pool_rows) * D;
         const int e = (threadIdx.x & (D / 8 - 1)) * 8;
         if (threadIdx.x < D / 8) *reinterpret_cast<uint4 *>(kc + at + e) = *reinterpret_cast<const uint4 *>(kn + e);
-        else *reinterpret_cast<uint4 *>(vc + at + e) = *reinterpret_cast<const uint4 *>(vn + e);
+        else *reinterpret_cast<uint4 *>(kc + v_behind + at + e) = *reinterpret_cast<const uint4 *>(vn + e);
     }
 
     // q in the order of the key loads: rows g and g + 8, elements 32 kk + 8c .. + 7
@@ -194,23 +195,33 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         const int x0 = lo + i0 - ns;                     // position of the first, from item ns on
         const bool old = i0 >= ns && x0 >= p.sinks && x0 <= start - kStep;
         const int r0 = old ? cache_row(i0) : 0;
-        const bool run = old && r0 + kStep <= p.pool_rows;
+        if (old && r0 + kStep <= p.pool_rows) {
+            const int k0 = sub * kAtOnce + lane / kPieces;
+            const uint16_t *ks = kc + (int64_t)(r0 + k0) * D + 8 * piece, *vs = ks + v_behind;
 #pragma unroll
-        for (int j = 0; j < kStep / kAtOnce / SHARE; j++) {
-            const int k = (j * SHARE + sub) * kAtOnce + lane / kPieces;
-            const uint16_t *ks, *vs;
-            const int i = min(i0 + k, count - 1);        // past the end: any row of the list will do
-            const int x = i < ns ? i : lo + i - ns;
-            if (run || x < start) {
-                const int64_t r = (int64_t)(run ? r0 + k : cache_row(i)) * D;
-                ks = kc + r;
-                vs = vc + r;
-            } else {
-                ks = kn + (x - start) * p.k_stride;
-                vs = vn + (x - start) * p.v_stride;
+            for (int j = 0; j < kStep / kAtOnce / SHARE; j++) {
+                const int k = j * SHARE * kAtOnce;
+                const uint32_t at = to + place<D>(k0 + k, piece);
+                copy16(at, ks + k * D);
+                copy16(at + kTile, vs + k * D);
             }
-            copy16(to + place<D>(k, piece), ks + 8 * piece);
-            copy16(to + kTile + place<D>(k, piece), vs + 8 * piece);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kStep / kAtOnce / SHARE; j++) {
+                const int k = (j * SHARE + sub) * kAtOnce + lane / kPieces;
+                const uint16_t *ks, *vs;
+                const int i = min(i0 + k, count - 1);    // past the end: any row of the list will do
+                const int x = i < ns ? i : lo + i - ns;
+                if (x < start) {
+                    ks = kc + (int64_t)cache_row(i) * D;
+                    vs = ks + v_behind;
+                } else {
+                    ks = kn + (x - start) * p.k_stride;
+                    vs = vn + (x - start) * p.v_stride;
+                }
+                copy16(to + place<D>(k, piece), ks + 8 * piece);
+                copy16(to + kTile + place<D>(k, piece), vs + 8 * piece);
+            }
         }
     };
     const int stride = ranks * kParts * kStep;
