@@ -15,8 +15,7 @@
 // rows are the 16 rows of the warp MMA: S = Q K^T, then O += P V with a running
 // maximum and sum per warp.  The order of the summed index is free, so a lane reads
 // 16 contiguous bytes of a key row and uses them as the operands of two MMAs (q is
-// held in the same order); of the value rows it reads 16 bytes of two neighbouring
-// keys and interleaves them, which permutes only the output columns.  Warps, then
+// held in the same order); the value rows come transposed by ldmatrix.  Warps, then
 // CTAs of a cluster (through distributed shared memory), join their (maximum, sum,
 // O) at the end.  In decode the new token's rows are taken from the call's arguments
 // by everyone, so nobody reads the cache row being written.
@@ -55,12 +54,21 @@ __device__ __forceinline__ uint4 shared16(uint32_t at)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
-// Place of 16-byte piece c of row r in a step's tile: the pieces that eight lanes
-// read together (of a key tile four pieces of rows 2i and 2i + 1; of a value tile
-// pieces 2i and 2i + 1 of four rows of one parity) lie in different banks.
-template <int D> __device__ __forceinline__ uint32_t place(int r, int c)
+// Place of 16-byte piece c of row r in a step's tile of keys: the pieces that eight
+// lanes read together (four of rows 2i and 2i + 1) lie in different banks; and of
+// values, where they are one piece of eight rows.
+template <int D> __device__ __forceinline__ uint32_t place_key(int r, int c)
 {
-    return r * (D * 2) + ((c ^ ((r & 6) ^ ((r & 1) << 2))) << 4);
+    return r * (D * 2) + ((c ^ ((r & 1) << 2)) << 4);
+}
+template <int D> __device__ __forceinline__ uint32_t place_value(int r, int c) { return r * (D * 2) + ((c ^ (r & 7)) << 4); }
+
+// Four 8 x 8 matrices of 16-bit elements, transposed; lane 8 i + j points at row j of
+// the i-th.
+__device__ __forceinline__ void load_matrices_t(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
 template <typename E>
@@ -86,7 +94,7 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uin
 // shared memory of a CTA: every warp's O, then maxima and sums; after the warps
 // are joined, those of the CTA's 16 SHARE rows in the first SHARE parts
 template <int D> struct JoinSmem {
-    float o[kWarps][kRows][D];
+    float o[kWarps][kRows][D + 8];   // rows 8 banks apart
     float m[kWarps][kRows], l[kWarps][kRows];
 };
 
@@ -176,11 +184,9 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         qb[kk] = row_b < rows ? *reinterpret_cast<const uint4 *>(qpb + 32 * kk) : make_uint4(0, 0, 0, 0);
     }
 
-    float o[D / 64][8][4];
+    float o[D / 8][4];               // tiles of 8 columns
 #pragma unroll
-    for (int i = 0; i < D / 64; i++)
-#pragma unroll
-        for (int j = 0; j < 8; j++) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+    for (int j = 0; j < D / 8; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     // the ring of these keys; a stage is 16 key rows, then 16 value rows, each copied by
@@ -201,9 +207,8 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
 #pragma unroll
             for (int j = 0; j < kStep / kAtOnce / SHARE; j++) {
                 const int k = j * SHARE * kAtOnce;
-                const uint32_t at = to + place<D>(k0 + k, piece);
-                copy16(at, ks + k * D);
-                copy16(at + kTile, vs + k * D);
+                copy16(to + place_key<D>(k0 + k, piece), ks + k * D);
+                copy16(to + kTile + place_value<D>(k0 + k, piece), vs + k * D);
             }
         } else {
 #pragma unroll 1
@@ -219,8 +224,8 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
                     ks = kn + (x - start) * p.k_stride;
                     vs = vn + (x - start) * p.v_stride;
                 }
-                copy16(to + place<D>(k, piece), ks + 8 * piece);
-                copy16(to + kTile + place<D>(k, piece), vs + 8 * piece);
+                copy16(to + place_key<D>(k, piece), ks + 8 * piece);
+                copy16(to + kTile + place_value<D>(k, piece), vs + 8 * piece);
             }
         }
     };
@@ -248,7 +253,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
             s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < D / 32; kk++) {
-                const uint4 kr = shared16(kt + place<D>(8 * j + g, 4 * kk + c));
+                const uint4 kr = shared16(kt + place_key<D>(8 * j + g, 4 * kk + c));
                 mma16816<E>(s[j], qa[kk].x, qb[kk].x, qa[kk].y, qb[kk].y, kr.x, kr.y);
                 mma16816<E>(s[j], qa[kk].z, qb[kk].z, qa[kk].w, qb[kk].w, kr.z, kr.w);
             }
@@ -295,14 +300,12 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
             l0 *= f0;
             l1 *= f1;
 #pragma unroll
-            for (int i = 0; i < D / 64; i++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    o[i][j][0] *= f0;
-                    o[i][j][1] *= f0;
-                    o[i][j][2] *= f1;
-                    o[i][j][3] *= f1;
-                }
+            for (int j = 0; j < D / 8; j++) {
+                o[j][0] *= f0;
+                o[j][1] *= f0;
+                o[j][2] *= f1;
+                o[j][3] *= f1;
+            }
             m0 = a;
             m1 = b;
         }
@@ -322,19 +325,13 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
             const float(&x)[4] = s[2 * k], (&y)[4] = s[2 * k + 1];
             const uint32_t p0 = Half2<E>::pack(x[0], x[1]), p1 = Half2<E>::pack(x[2], x[3]);
             const uint32_t p2 = Half2<E>::pack(y[0], y[1]), p3 = Half2<E>::pack(y[2], y[3]);
+            const int r = 16 * k + (lane & 15);
 #pragma unroll
-            for (int hh = 0; hh < D / 64; hh++) {
-                const int r = 16 * k + 2 * c;
-                const uint4 v0 = shared16(vt + place<D>(r, 8 * hh + g)), v1 = shared16(vt + place<D>(r + 1, 8 * hh + g));
-                const uint4 v2 = shared16(vt + place<D>(r + 8, 8 * hh + g)), v3 = shared16(vt + place<D>(r + 9, 8 * hh + g));
-                const uint32_t r0[4] = {v0.x, v0.y, v0.z, v0.w}, r1[4] = {v1.x, v1.y, v1.z, v1.w};
-                const uint32_t r2[4] = {v2.x, v2.y, v2.z, v2.w}, r3[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-                    mma16816<E>(o[hh][j], p0, p1, p2, p3, __byte_perm(r0[j / 2], r1[j / 2], sel),
-                                __byte_perm(r2[j / 2], r3[j / 2], sel));
-                }
+            for (int j = 0; j < D / 8; j += 2) {
+                uint32_t b[4];
+                load_matrices_t(vt + place_value<D>(r, j + (lane >> 4)), b);
+                mma16816<E>(o[j], p0, p1, p2, p3, b[0], b[1]);
+                mma16816<E>(o[j + 1], p0, p1, p2, p3, b[2], b[3]);
             }
         }
     }
@@ -350,20 +347,11 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         sm.l[warp][g] = l0;
         sm.l[warp][g + 8] = l1;
     }
-    // column 2c (+1) of the tile (hh, j) is element 64 hh + 16 c (+ 8) + j
 #pragma unroll
-    for (int hh = 0; hh < D / 64; hh++)
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-#pragma unroll
-            for (int q = 0; q < 2; q++) {
-                float *to = &sm.o[warp][g + 8 * e][64 * hh + 16 * c + 8 * q];
-                float4 x, y;
-                x.x = o[hh][0][2 * e + q]; x.y = o[hh][1][2 * e + q]; x.z = o[hh][2][2 * e + q]; x.w = o[hh][3][2 * e + q];
-                y.x = o[hh][4][2 * e + q]; y.y = o[hh][5][2 * e + q]; y.z = o[hh][6][2 * e + q]; y.w = o[hh][7][2 * e + q];
-                reinterpret_cast<float4 *>(to)[0] = x;
-                reinterpret_cast<float4 *>(to)[1] = y;
-            }
+    for (int j = 0; j < D / 8; j++) {
+        *reinterpret_cast<float2 *>(&sm.o[warp][g][8 * j + 2 * c]) = make_float2(o[j][0], o[j][1]);
+        *reinterpret_cast<float2 *>(&sm.o[warp][g + 8][8 * j + 2 * c]) = make_float2(o[j][2], o[j][3]);
+    }
     __syncthreads();
     // join the warps of different keys: the CTA's maxima, sums and O into the first SHARE
     // parts (each element is read and written by one thread; the factors are read
