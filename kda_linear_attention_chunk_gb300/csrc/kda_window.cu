@@ -33,6 +33,13 @@
 #include "kda_sm100.cuh"
 #include "kda_window.h"
 
+// Poll limit of the softmax's wait for scores.  A test build of the library sets it to
+// zero: the wait then gives up at once although its MMAs complete, which takes every
+// CTA through the wind-down.
+#ifndef KDA_WAIT_LIMIT_SCORES
+#define KDA_WAIT_LIMIT_SCORES (1u << 18)
+#endif
+
 namespace kda {
 namespace {
 
@@ -637,7 +644,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             if (!sees(t, rows.first, rows.last, p.window, p.sinks)) continue;
             // every key of the tile visible to every row of the warp: no test per key
             const bool whole = t.complete && t.keys == kKeys && t.hi <= lo_row && t.low > hi_row - p.window;
-            ok = mbar_wait(x.bars.s_full(q), it & 1, x.abort);
+            ok = mbar_wait(x.bars.s_full(q), it & 1, x.abort, KDA_WAIT_LIMIT_SCORES);
             if (!ok) break;
             it++;
             if (dead) {                                  // whatever is there will do as these rows' P
@@ -916,9 +923,9 @@ bool make_map(CUtensorMap *m, const void *base, bool f16, int d, int64_t n1, int
 // the warp-MMA kernel, which takes 16 to 64 of them at a time, is faster than tiles
 // of 128: up to 32, and up to 256 where so few items leave most SMs without a tile
 // (the other kernel spreads each over eight CTAs).  Measured (us, warp-MMA / tiles;
-// G = 4, d = 128): 64 sequences, window 1024: 16 rows 65 / 90, 32 rows 85 / 91, 64
-// rows 139 / 106; one sequence, window 4096: 32 rows 26 / 64, 256 rows 57 / 66, 512
-// rows 67 / 67; 16 fresh sequences: 64 rows 23 / 23, 256 rows 34 / 23.
+// G = 4, d = 128): 64 sequences, window 1024: 16 rows 58 / 77, 32 rows 72 / 80, 64
+// rows 121 / 81; one sequence, window 4096: 32 rows 21 / 56, 256 rows 48 / 63; 16
+// fresh sequences: 64 rows 22 / 20, 256 rows 31 / 19.
 bool few_rows(const WindowParams &p, int num_sms)
 {
     const int64_t rows = (int64_t)p.T * p.G;
