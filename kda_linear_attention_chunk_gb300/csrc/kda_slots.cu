@@ -4,7 +4,8 @@
 // The work is cut into pieces of kPiece bytes of one entry; a CTA copies one
 // piece with four 16-byte loads in flight per thread.  Pieces are ordered with
 // the moves innermost, so the forks of one source read each of its pieces
-// together (from L2 after the first).
+// together (from L2 after the first).  16 forks of 12.7 MB each take 41.7 us on a GB300,
+// 6.1 TB/s of algorithmic bytes (32 KB pieces 43.5 us).
 #include <stdint.h>
 
 #include "kda_common.cuh"

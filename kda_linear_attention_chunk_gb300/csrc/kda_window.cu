@@ -1,17 +1,17 @@
 // kda_window.cu -- window attention of packed new tokens over the ring cache and
-// themselves (prefill, and the verification of drafts), on the tensor cores.
+// themselves (prefill), on the tensor cores.
 //
 // For the query at position p:  o = sum_j softmax_j(scale q . k_j) v_j  over the
 // positions j <= p with j > p - window or j < sinks.  Keys of positions before
 // the call's come from the cache, the others from the call's rows.
 //
-// A CTA takes two tiles of up to 128 query rows of one key head: the G query
-// heads that share it for floor(128 / G) consecutive tokens each, so that each
-// key and value tile serves G heads and a tile spans few positions (little of
-// the window's edges is computed and masked away).  The visible positions are a
-// few runs of consecutive rows (sinks, the ring before and after its wrap, the
-// call's rows), cut into tiles of up to 128 keys.  Per tile and query tile, with
-// S, P and O in TMEM:
+// An item of work is two tiles of up to 128 query rows of one key head: the G query
+// heads that share it for floor(128 / G) consecutive tokens each, so that each key
+// and value tile serves G heads and a tile spans few positions (little of the
+// window's edges is computed and masked away).  The visible positions are a few
+// runs of consecutive rows (sinks, the ring before and after its wrap, the call's
+// rows); they fill tiles of 128 keys, each run from a multiple of 16 on.  Per key
+// and query tile, with S, P and O in TMEM:
 //
 //     S = Q K^T            (tcgen05.mma, both operands in shared memory)
 //     P = 2^(c S - c m)    one thread per query row: 128 scores in registers
@@ -23,9 +23,17 @@
 // division makes the result independent of m), so O is rarely rescaled, and the
 // threads that own the rows do it themselves.
 //
-// Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 the TMA
-// loads (a ring of five key / value tiles), warp 9 the MMAs, warp 10 the zeros
-// behind ragged value tiles (11 completes the warpgroup).  A second kernel then writes the rows that the cache keeps.
+// Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 finds items and
+// loads (a ring of four key and value tiles), warps 9 and 11 the MMAs of the two
+// query tiles, warp 10 the zeros behind ragged runs of values.  A second kernel then
+// writes the rows that the cache keeps.
+//
+// On a GB300, 32 query heads on 8 key heads of 128: 8192 rows in the middle of a
+// context, window 4096, 0.39-0.41 ms (1.34-1.41 PFLOP/s); 32,768 rows at once
+// 1.36-1.44 ms; 16 prompts in 8192 rows, window 1024, 84 us.  With long windows the
+// chain of one query tile bounds it (scores, softmax, P V, the next scores: 2750 cycles
+// a key tile, 2050 of them the tensor core's work for both query tiles); with short
+// ones what an item costs beside its tiles.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <stdint.h>
