@@ -450,6 +450,8 @@ int kda_short_conv(const uint16_t *xq, const uint16_t *xk, const uint16_t *xv,
  *             context is plain causal attention.
  *  Heads      Hq query heads share Hk key heads in order: query head h reads
  *             key head h / (Hq / Hk); Hq a multiple of Hk, at most 128 times it.
+ *  Capture    every call can be captured into a CUDA graph, after one call of its
+ *             kind (dtype, d) outside of a capture, which sets the kernels up.
  */
 typedef enum { KDA_BF16 = 0, KDA_F16 = 1 } kda_dtype;
 typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
@@ -509,7 +511,7 @@ int kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
  *   kv_pool     the ring cache, read and updated in place, or NULL: nothing is
  *               cached before or after (starts and slots must then be NULL).
  *   out         [T][Hq][d]; every row of an unpadded sequence is written.
- *   scale       > 0, finite.
+ *   scale       > 0, at most 1e37.
  * A masked key never reaches an output, whatever its score.  A value row that
  * is not finite reaches, besides the rows that see it, rows of the same
  * sequence in the same tile (up to 128 keys by 256 query rows); it reaches no

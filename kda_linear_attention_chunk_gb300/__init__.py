@@ -641,9 +641,12 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     return q_out, k_out
 
 
-def _window_args(q, k, v, kv_pool, slots, N, out):
+def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks):
     """The checks that the two window-attention calls share; returns what both pass on."""
     import torch
+
+    if not 0 < window <= 0x7fffffff or not 0 <= sinks <= 0x7fffffff:
+        raise ValueError("window and sinks must be 32-bit numbers, window >= 1, sinks >= 0")
 
     dtype = q.dtype
     dt = _dtype16(q, "q")
@@ -678,7 +681,7 @@ def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=Non
     [T][Hq][d] (rows of padded sequences keep what ``out`` held).
     """
     N = int(cu_seqlens.shape[0]) - 1
-    dt, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out)
+    dt, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks)
     cu = _table32("cu_seqlens", cu_seqlens, N + 1)
     st = load().kda_window_prefill(*qkv, cu, 0 if starts is None else _table32("starts", starts, N), ids, *pool,
                                    out.data_ptr(), N, T, Hq, Hk, d, window, sinks, d ** -0.5 if scale is None else scale,
@@ -695,7 +698,7 @@ def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slot
     kv_pool in place.  Returns out [N][Hq][d] (rows of padded sequences, slot -1, keep what ``out`` held).
     """
     N = q.shape[0]
-    dt, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out)
+    dt, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks)
     st = load().kda_window_decode(*qkv, _table32("positions", positions, N), ids, *pool, out.data_ptr(), N, Hq, Hk, d,
                                   window, sinks, d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
     if st != KDA_OK:
@@ -705,6 +708,8 @@ def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slot
 
 def _pools(pools):
     """A host array of (base, entry_bytes) pairs, the number of slots and the device of a list of pool tensors."""
+    if not pools:
+        raise ValueError("at least one pool is needed")
     n = pools[0].shape[0]
     flat = []
     for p in pools:

@@ -46,7 +46,7 @@ int check_window(const kda::WindowArgs &a, int rows, int dtype)
     int st = check_heads(a.Hq, a.Hk, a.d, dtype);
     if (st != KDA_OK) return st;
     if (a.Hq % a.Hk || a.window < 1 || a.sinks < 0) return KDA_ERR_SHAPE;
-    if (!(a.scale > 0.f && a.scale <= 3.0e38f)) return KDA_ERR_SHAPE;   // also rejects NaN
+    if (!(a.scale > 0.f && a.scale <= 1.0e37f)) return KDA_ERR_SHAPE;   // also rejects NaN
     if (a.Hq / a.Hk > 128) return KDA_ERR_UNSUPPORTED;
     const int64_t wq = (int64_t)a.Hq * a.d, wk = (int64_t)a.Hk * a.d;
     const int64_t strides[] = {a.q_stride, a.k_stride, a.v_stride};
@@ -172,6 +172,10 @@ int kda_window_prefill(const void *q, int64_t q_stride, const void *k, int64_t k
     if (st != KDA_OK) return st;
     if ((st = kda::device_facts(&a.device, &a.num_sms, &a.err_word)) != KDA_OK) return st;
     if (T == 0) return KDA_OK;
+    if (!kv_pool) {              // every position is below T: neither needs to be larger
+        if (a.window > T) a.window = T;
+        if (a.sinks > T) a.sinks = T;
+    }
     return status_of(kda::launch_window_prefill(a));
 }
 

@@ -81,7 +81,7 @@ def test_window_refusals(kda_lib, call):
         assert call(**{name: 0}) == kda.KDA_ERR_NULL, name
     for bad in (dict(N=0), dict(Hq=0), dict(Hk=0), dict(Hk=3), dict(Hq=1), dict(window=0), dict(sinks=-1), dict(window=17),
                 dict(sinks=5), dict(rows=19), dict(window=0x7fffffff, sinks=0x7fffffff), dict(num_slots=0),
-                dict(slots=0, num_slots=1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
+                dict(slots=0, num_slots=1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=2e37),
                 dict(scale=float("nan")), dict(q_stride=512), dict(v_stride=8), dict(num_slots=0x7fffffff)):
         assert call(**bad) == kda.KDA_ERR_SHAPE, bad
     for bad in (dict(d=96), dict(d=32), dict(dtype=2), dict(dtype=-1), dict(Hq=129, Hk=1, q_stride=129 * 128)):
@@ -161,6 +161,9 @@ def test_wrappers_refuse_wrong_tensors():
     for call in (lambda: kda.head_norm_rope(x, x), lambda: kda.head_norm_rope(x.float(), x.float()),
                  lambda: kda.window_prefill(x, x, x, i, 16), lambda: kda.window_decode(x, x, x, i, pool, 16),
                  lambda: kda.slots_copy([pool], i, i), lambda: kda.slots_compact([pool], i),
+                 lambda: kda.slots_copy([], i, i), lambda: kda.slots_compact([], i),
+                 lambda: kda.window_prefill(x, x, x, i, 1 << 32), lambda: kda.window_prefill(x, x, x, i, 4, sinks=1 << 31),
+                 lambda: kda.window_decode(x, x, x, i, pool, 0),
                  lambda: kda.rope_table(0, 16), lambda: kda.rope_table(8, 15), lambda: kda.rope_table(8, 16, base=0.5),
                  lambda: kda.rope_table(8, 16, stretch=0.5)):
         with pytest.raises(ValueError):

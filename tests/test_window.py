@@ -194,6 +194,65 @@ def test_prefill_wider_window_than_any_context_is_causal_attention():
     small.prefill([300], cached=False, qkv=(q, k, v))
 
 
+def test_prefill_sinks_and_window_beyond_everything():
+    """Without a cache neither is bounded by one; both at the largest number are causal attention."""
+    t = torch()
+    for T in (40, 500):
+        b = Batch([0], 4, 2, 64, window=T, sinks=0, dtype="bf16", seed=T)
+        q, k, v = b.new_rows(T)
+        want = kda.window_prefill(q, k, v, b.int32([0, T]), T)
+        for window, sinks in ((0x7fffffff, 0x7fffffff), (1, 0x7fffffff), (3, T)):
+            assert t.equal(kda.window_prefill(q, k, v, b.int32([0, T]), window, sinks=sinks), want)
+
+
+@pytest.mark.parametrize("L", [1, 10])
+def test_prefill_many_sequences(L):
+    """More sequences than one round of probes tells apart, some empty, for both kernels."""
+    rng = np.random.default_rng(L)
+    lens = [int(x) for x in rng.integers(0, 2 * L + 1, 1200)]
+    b = Batch([int(x) for x in rng.integers(0, 12, 1200)], 4, 1, 64, window=9, sinks=1, dtype="bf16", seed=L)
+    b.prefill(lens, padded=(3, 700), check_rows=[0, L, 2 * L - 1])
+
+
+def test_offsets_beyond_32_bits():
+    """Rows, outputs and cache entries whose offsets pass 2^31 elements: rows at the end against the same rows alone."""
+    t = torch()
+    T, H, d = (1 << 31) // 2048 + 700, 16, 128
+    free = t.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    qkv = t.empty(T, H + 2, d, dtype=t.bfloat16, device="cuda").normal_()
+    q, k, v = qkv[:, :H], qkv[:, H:H + 1], qkv[:, H + 1:]
+    cu = t.tensor([0, T], dtype=t.int32, device="cuda")
+    out = kda.window_prefill(q, k, v, cu, 50)
+    tail = kda.window_prefill(q[-300:], k[-300:], v[-300:], t.tensor([0, 300], dtype=t.int32, device="cuda"), 50)
+    # as far as the reduction's order goes: the tiles of the two calls start at different rows
+    assert (out[-250:].float() - tail[-250:].float()).abs().max() <= 2.0 ** -5
+    a, b = kda.head_norm_rope(q, k, positions=t.zeros(T, dtype=t.int32, device="cuda"), table=kda.rope_table(1, d))
+    x, y = kda.head_norm_rope(q[-9:], k[-9:], positions=t.zeros(9, dtype=t.int32, device="cuda"), table=kda.rope_table(1, d))
+    assert t.equal(a[-9:], x) and t.equal(b[-9:], y)
+    del out, a, b
+    rows, slots = 140000, 64                       # 64 x 2 x 140000 x 128 elements
+    pool = t.zeros(slots, 2, 1, rows, d, dtype=t.bfloat16, device="cuda")
+    assert pool.numel() > 1 << 31
+    small = t.empty(1, 2, 1, rows, d, dtype=t.bfloat16, device="cuda").normal_()
+    pool[slots - 1] = small[0]
+    ids, start = t.tensor([slots - 1], dtype=t.int32, device="cuda"), t.tensor([200000], dtype=t.int32, device="cuda")
+    for L in (1, 2, 300):
+        cu = t.tensor([0, L], dtype=t.int32, device="cuda")
+        p, s = pool, small.clone()
+        got = kda.window_prefill(q[:L], k[:L], v[:L], cu, rows - 4, sinks=4, kv_pool=p, slots=ids, starts=start)
+        want = kda.window_prefill(q[:L], k[:L], v[:L], cu, rows - 4, sinks=4, kv_pool=s, starts=start)
+        assert t.equal(got, want) and t.equal(p[slots - 1], s[0])
+        pool[slots - 1] = small[0]
+    got = kda.window_decode(q[:1], k[:1], v[:1], start, pool, rows - 4, sinks=4, slots=ids)
+    s = small.clone()
+    assert t.equal(got, kda.window_decode(q[:1], k[:1], v[:1], start, s, rows - 4, sinks=4))
+    assert t.equal(pool[slots - 1], s[0])
+    kda.slots_copy([pool], ids, t.tensor([3], dtype=t.int32, device="cuda"))
+    assert t.equal(pool[3], pool[slots - 1])
+
+
 def test_prefill_padded_and_bad_slots():
     t = torch()
     b = Batch([10, 20, 30, 0], 4, 2, 128, window=9, sinks=2, dtype="bf16", seed=5)
