@@ -36,6 +36,7 @@ KDA_ROPE_HALF, KDA_ROPE_INTERLEAVED = 0, 1
 KDA_MAX_POOLS, KDA_MAX_POOL_SLOTS = 128, 524288
 
 _lib = None
+_torch_module = None
 
 
 class KdaError(RuntimeError):
@@ -512,22 +513,30 @@ def decode_conv(xq, xk, xv, conv_weight, conv_pool, g, beta, state_pool, conv_sl
 ROPE_LAYOUTS = {"half": KDA_ROPE_HALF, "interleaved": KDA_ROPE_INTERLEAVED}
 
 
+def _torch():
+    """The torch module, imported by the first call that needs it (a later import statement looks it up anew, and a call
+    on small tensors is all host time)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
 def _handle(stream, device) -> int:
     """The stream's handle; without one, torch's current stream of the device (its raw handle: building a Stream object
     for it would cost as much as the rest of a call)."""
     if stream is None:
-        import torch
-
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype16(t, name: str) -> int:
-    import torch
-
-    if t.dtype == torch.bfloat16:
+    torch = _torch()
+    if t.dtype is torch.bfloat16:
         return KDA_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return KDA_F16
     raise ValueError(f"{name} must be bfloat16 or float16")
 
@@ -545,9 +554,7 @@ def _rows_of_heads(name: str, t, dtype):
 
 def _table32(name: str, t, n: int) -> int:
     """Checks an int32 [n] table; returns its address."""
-    import torch
-
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.shape != (n,):
+    if t.dtype is not _torch().int32 or not t.is_cuda or not t.is_contiguous() or t.shape != (n,):
         raise ValueError(f"{name} must be int32 [{n}] on the device")
     return t.data_ptr()
 
@@ -602,8 +609,7 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     int32, or None (no rotation); layout "half" or "interleaved".  ``norm`` False rotates only.  Returns
     (q, k), dense; ``out`` may name them (in place where the inputs are dense).
     """
-    import torch
-
+    torch = _torch()
     dtype = q.dtype
     dt = _dtype16(q, "q")
     (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
@@ -643,11 +649,9 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
 
 def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks):
     """The checks that the two window-attention calls share; returns what both pass on."""
-    import torch
-
     if not 0 < window <= 0x7fffffff or not 0 <= sinks <= 0x7fffffff:
         raise ValueError("window and sinks must be 32-bit numbers, window >= 1, sinks >= 0")
-
+    torch = _torch()
     dtype = q.dtype
     dt = _dtype16(q, "q")
     (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
