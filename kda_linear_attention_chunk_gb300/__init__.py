@@ -532,6 +532,20 @@ def _handle(stream, device) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(shape, dtype, device, stream):
+    """An output of a call on ``stream``.  Its memory has to be free on that stream, whatever torch's current stream still
+    does with blocks it has given back; and it is not given back before the current stream, where it will be used, is
+    done with it."""
+    torch = _torch()
+    if stream is None or _handle(stream, device) == _handle(None, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_handle(stream, device), device=device)):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def _dtype16(t, name: str) -> int:
     torch = _torch()
     if t.dtype is torch.bfloat16:
@@ -633,8 +647,8 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     if out is None:
-        q_out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
-        k_out = torch.empty(k_shape, dtype=dtype, device=q.device)
+        q_out = _new((T, Hq, d), dtype, q.device, stream)
+        k_out = _new(k_shape, dtype, q.device, stream)
     else:
         q_out, k_out = out
         _dense("out[0]", q_out, (T, Hq, d), dtype)
@@ -647,11 +661,10 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     return q_out, k_out
 
 
-def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks):
+def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks, stream):
     """The checks that the two window-attention calls share; returns what both pass on."""
     if not 0 < window <= 0x7fffffff or not 0 <= sinks <= 0x7fffffff:
         raise ValueError("window and sinks must be 32-bit numbers, window >= 1, sinks >= 0")
-    torch = _torch()
     dtype = q.dtype
     dt = _dtype16(q, "q")
     (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
@@ -668,7 +681,7 @@ def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks):
         pool = _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), dtype)
     ids = 0 if slots is None else _table32("slots", slots, N)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
+        out = _new((T, Hq, d), dtype, q.device, stream)
     else:
         _dense("out", out, (T, Hq, d), dtype)
     return dt, (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv), ids, (pool, num_slots, rows), out, T, Hq, Hk, d
@@ -685,7 +698,8 @@ def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=Non
     [T][Hq][d] (rows of padded sequences keep what ``out`` held).
     """
     N = int(cu_seqlens.shape[0]) - 1
-    dt, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks)
+    dt, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks,
+                                                             stream)
     cu = _table32("cu_seqlens", cu_seqlens, N + 1)
     st = load().kda_window_prefill(*qkv, cu, 0 if starts is None else _table32("starts", starts, N), ids, *pool,
                                    out.data_ptr(), N, T, Hq, Hk, d, window, sinks, d ** -0.5 if scale is None else scale,
@@ -702,7 +716,8 @@ def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slot
     kv_pool in place.  Returns out [N][Hq][d] (rows of padded sequences, slot -1, keep what ``out`` held).
     """
     N = q.shape[0]
-    dt, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks)
+    dt, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks,
+                                                             stream)
     st = load().kda_window_decode(*qkv, _table32("positions", positions, N), ids, *pool, out.data_ptr(), N, Hq, Hk, d,
                                   window, sinks, d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
     if st != KDA_OK:
@@ -741,13 +756,11 @@ def slots_compact(pools, slots, new_slots=None, stream=None):
     with m live entries, ids from m on take the free ids below m, both in ascending order.  slots: [N] int32 on the
     device.  Returns new_slots [N] int32, where each went (-1 stays).
     """
-    import torch
-
     array, n, device = _pools(pools)
     N = int(slots.shape[0])
     _table32("slots", slots, N)
     if new_slots is None:
-        new_slots = torch.empty((N,), dtype=torch.int32, device=device)
+        new_slots = _new((N,), _torch().int32, device, stream)
     else:
         _table32("new_slots", new_slots, N)
     st = load().kda_slots_compact(ctypes.addressof(array), len(array) // 2, n, _ptr(slots), _ptr(new_slots), N,

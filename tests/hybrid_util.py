@@ -89,3 +89,24 @@ def worst(got, ref, bound):
     """Largest |got - ref| / bound: <= 1 passes; NaN anywhere fails."""
     x = np.abs(got - ref) / bound
     return float(x.max()) if x.size and not np.isnan(x).any() else (math.inf if x.size else 0.0)
+
+
+def beside_pending_work(call, shape, dtype):
+    """call(stream) on a stream of its own while the current one still has writes before it into blocks of the given
+    size that were handed back: the outputs must not lie in one of those."""
+    import torch
+
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(512)]
+    blocks[0].fill_(0)                             # loads the kernel: later that would wait for the sleep
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(60_000_000)                  # some 30 ms
+    for b in blocks:
+        b.fill_(7)
+    del b, blocks[::2]                             # holes of just that size
+    got = call(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    return got

@@ -4,7 +4,7 @@ import pytest
 
 import kda_linear_attention_chunk_gb300 as kda
 from gpu_util import torch
-from hybrid_util import f64, norm_rope, torch_dtype, worst
+from hybrid_util import beside_pending_work, f64, norm_rope, torch_dtype, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -103,6 +103,14 @@ def test_no_rows_and_another_stream():
     with t.cuda.stream(s):
         got = kda.head_norm_rope(q, k, qw, kw, pos, table)
     s.synchronize()
+    assert t.equal(got[0], want[0]) and t.equal(got[1], want[1])
+
+
+def test_outputs_on_a_given_stream():
+    t = torch()
+    q, k, qw, kw, pos, table = draw(300, 8, 8, 64, "bf16", 64, seed=18)
+    want = kda.head_norm_rope(q, k, qw, kw, pos, table)
+    got = beside_pending_work(lambda s: kda.head_norm_rope(q, k, qw, kw, pos, table, stream=s), (300, 8, 64), t.bfloat16)
     assert t.equal(got[0], want[0]) and t.equal(got[1], want[1])
 
 

@@ -4,6 +4,7 @@ import pytest
 
 import kda_linear_attention_chunk_gb300 as kda
 from gpu_util import torch
+from hybrid_util import beside_pending_work
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +136,11 @@ def test_other_stream():
     s.synchronize()
     for p, w in zip(pools, was):
         assert t.equal(p[5].cpu(), w[1]) and t.equal(p[6].cpu(), w[2])
+
+
+def test_compact_result_on_a_given_stream():
+    t = torch()
+    pools, slots = make_pools(6, seed=14), int32([5, -1, 3])
+    kda.slots_compact(make_pools(6, seed=14), slots)
+    got = beside_pending_work(lambda s: kda.slots_compact(pools, slots, stream=s), (3,), t.int32)
+    assert got.tolist() == compacted([5, -1, 3], 6)

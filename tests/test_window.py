@@ -6,7 +6,7 @@ import pytest
 
 import kda_linear_attention_chunk_gb300 as kda
 from gpu_util import torch
-from hybrid_util import attention, f64, row_of, torch_dtype, worst
+from hybrid_util import attention, beside_pending_work, f64, row_of, torch_dtype, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -345,6 +345,17 @@ def test_prefill_empty_call_and_other_stream():
     got = kda.window_prefill(q, k, v, cu, 10, sinks=1, kv_pool=p2, slots=ids, starts=st, stream=s)
     s.synchronize()
     assert t.equal(got, want) and t.equal(p1.view(t.int16), p2.view(t.int16))
+
+
+def test_outputs_on_a_given_stream():
+    t = torch()
+    b = Batch([0] * 40, 8, 2, 128, window=40, sinks=2, dtype="bf16", seed=25)
+    q, k, v = b.new_rows(40)
+    cu, ids, st = b.int32(list(range(41))), b.ids(), b.int32(b.length)
+    for call in (lambda s: kda.window_prefill(q, k, v, cu, 40, sinks=2, kv_pool=b.pool, slots=ids, starts=st, stream=s),
+                 lambda s: kda.window_decode(q, k, v, st, b.pool, 40, sinks=2, slots=ids, stream=s)):
+        want = call(None)
+        assert t.equal(beside_pending_work(call, (40, 8, 128), t.bfloat16), want)
 
 
 def test_prefill_same_bytes_every_time():
