@@ -202,7 +202,7 @@ __device__ __forceinline__ void add_runs(Item &c, const WindowParams &p, int bos
         }
     }
     const int from = max(a, start);
-    add(0, bos + from - start, from, b - from);
+    add(0, bos + (from - start), from, b - from);
 }
 
 // A piece of a key tile: `take` consecutive rows in its columns from `col` on.
@@ -643,7 +643,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         if (!ok || now.tokens == 0) break;
         const Span rows(now, p.tile_tokens, q);
         const int lo_row = rows.first + (32 * (warp & 3) * p.inv_G >> 16);
-        const int hi_row = rows.first + ((32 * (warp & 3) + 31) * p.inv_G >> 16);
+        const int hi_row = rows.first + min((32 * (warp & 3) + 31) * p.inv_G >> 16, rows.tokens - 1);   // (no sum beyond 2^31)
         const bool dead = 32 * (warp & 3) >= rows.tokens * p.G;      // no row of this warp is one: O may be anything
         const int pos = rows.first + token, t0 = now.t0 + q * p.tile_tokens, hk = now.hk;
         float m = -INFINITY, sum = 0.f;
@@ -674,7 +674,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
                 for (int r = t.run0, o = t.off0, col = 0; col < t.keys;) {
                     const Piece s = t.piece(r, o, col);
                     const int end = s.col + min(s.take, pos - s.pos + 1);            // columns at or before the row
-                    const int old = s.col + max(pos - p.window, -1) - s.pos + 1;     // columns behind the window,
+                    const int old = s.col + (max(pos - p.window, -1) - s.pos) + 1;   // columns behind the window,
                     const int sink = s.col + p.sinks - s.pos;                        // but for the sinks
 #pragma unroll
                     for (int i = 0; i < 4; i++)

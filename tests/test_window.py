@@ -253,6 +253,32 @@ def test_offsets_beyond_32_bits():
     assert t.equal(pool[3], pool[slots - 1])
 
 
+@pytest.mark.parametrize("window", [60, 1000])
+@pytest.mark.parametrize("L", [1, 3, 50, 300, 700])
+@pytest.mark.parametrize("Hq,Hk,d", [(1, 1, 64), (5, 1, 64), (8, 2, 128)])
+def test_positions_up_to_the_largest(Hq, Hk, d, L, window):
+    """Whole turns of the ring apart, contexts give the same bytes, up to the last positions that an int32 holds."""
+    t = torch()
+    sinks, rows = 4, window + 9
+    ring, top = rows - sinks, (1 << 31) - 1 - L
+    near = ring * 3 + (top - sinks) % ring + sinks
+    b = Batch([0], Hq, Hk, d, window, sinks, "bf16", extra=5, seed=L)
+    b.pool.normal_()
+    q, k, v = b.new_rows(L)
+    cu = b.int32([0, L])
+    kda.device_error(reset=True)
+    pools = [b.pool.clone() for _ in range(2)]
+    got = [kda.window_prefill(q, k, v, cu, window, sinks=sinks, kv_pool=p, slots=b.ids(), starts=b.int32([s]))
+           for p, s in zip(pools, (near, top))]
+    assert b.pool.shape[3] == rows and t.isfinite(got[0]).all()
+    assert t.equal(*got) and t.equal(*pools)
+    for back in (0, 1):
+        got = [kda.window_decode(q[:1], k[:1], v[:1], b.int32([s + L - back]), p, window, sinks=sinks, slots=b.ids())
+               for p, s in zip(pools, (near, top))]
+        assert t.equal(*got) and t.equal(*pools)
+    assert kda.device_error() == 0
+
+
 def test_prefill_padded_and_bad_slots():
     t = torch()
     b = Batch([10, 20, 30, 0], 4, 2, 128, window=9, sinks=2, dtype="bf16", seed=5)
