@@ -312,13 +312,15 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
             m0 = a;
             m1 = b;
         }
-        const float z0 = m0 == -INFINITY ? 0.f : m0 * p.scale_log2, z1 = m1 == -INFINITY ? 0.f : m1 * p.scale_log2;
+        // the difference first: rounded products with the scale would not cancel where a
+        // maximum changes or two are joined (by 2^-24 of their size, which has no bound)
+        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
         for (int j = 0; j < kTiles; j++) {
-            s[j][0] = ex2(fmaf(s[j][0], p.scale_log2, -z0));
-            s[j][1] = ex2(fmaf(s[j][1], p.scale_log2, -z0));
-            s[j][2] = ex2(fmaf(s[j][2], p.scale_log2, -z1));
-            s[j][3] = ex2(fmaf(s[j][3], p.scale_log2, -z1));
+            s[j][0] = ex2((s[j][0] - z0) * p.scale_log2);
+            s[j][1] = ex2((s[j][1] - z0) * p.scale_log2);
+            s[j][2] = ex2((s[j][2] - z1) * p.scale_log2);
+            s[j][3] = ex2((s[j][3] - z1) * p.scale_log2);
             l0 += s[j][0] + s[j][1];
             l1 += s[j][2] + s[j][3];
         }
