@@ -729,12 +729,12 @@ def _pools(pools):
     """A host array of (base, entry_bytes) pairs, the number of slots and the device of a list of pool tensors."""
     if not pools:
         raise ValueError("at least one pool is needed")
-    n = pools[0].shape[0]
+    n = pools[0].shape[0] if pools[0].dim() else 0
     flat = []
     for p in pools:
-        if not p.is_cuda or not p.is_contiguous() or p.dim() < 2 or p.shape[0] != n:
+        if not p.is_cuda or not p.is_contiguous() or p.dim() < 2 or p.shape[0] != n or not p.numel():
             raise ValueError("every pool must be a contiguous CUDA tensor [num_slots][...] of the same num_slots")
-        flat += (p.data_ptr(), p.stride(0) * p.element_size())
+        flat += (p.data_ptr(), p.numel() // n * p.element_size())   # (the stride of an axis of one may be anything)
     return (ctypes.c_int64 * len(flat))(*flat), n, pools[0].device
 
 
