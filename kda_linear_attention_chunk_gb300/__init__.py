@@ -539,8 +539,10 @@ def _new(shape, dtype, device, stream):
     torch = _torch()
     if stream is None or _handle(stream, device) == _handle(None, device):
         return torch.empty(shape, dtype=dtype, device=device)
-    current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_handle(stream, device), device=device)):
+    current, handle = torch.cuda.current_stream(device), _handle(stream, device)
+    # the default stream's handles (0, and 1 by name) are none that ExternalStream takes
+    given = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(given):
         out = torch.empty(shape, dtype=dtype, device=device)
     out.record_stream(current)
     return out
