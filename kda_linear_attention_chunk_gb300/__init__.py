@@ -524,11 +524,28 @@ def _torch():
     return _torch_module
 
 
+def _current_device() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
+def _device_of(name: str, t) -> int:
+    """The index of the device of a call's first tensor.  The library launches on the current device with the addresses
+    that it gets, so it has to be that one, and the other tensors and the stream have to be the device's too."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if at != _current_device():
+        raise ValueError(f"{name} lies on cuda:{at}, which is not the current device")
+    return at
+
+
 def _handle(stream, device) -> int:
     """The stream's handle; without one, torch's current stream of the device (its raw handle: building a Stream object
     for it would cost as much as the rest of a call)."""
     if stream is None:
         return _torch()._C._cuda_getCurrentRawStream(device.index)
+    if getattr(stream, "device_index", device.index) != device.index:
+        raise ValueError(f"the stream is not one of {device}")
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -557,10 +574,10 @@ def _dtype16(t, name: str) -> int:
     raise ValueError(f"{name} must be bfloat16 or float16")
 
 
-def _rows_of_heads(name: str, t, dtype):
-    """Checks rows of [heads][d] dense elements; returns the shape and the rows' distance in elements."""
-    if not t.is_cuda or t.dim() != 3 or t.dtype != dtype:
-        raise ValueError(f"{name} must be a CUDA tensor [rows][heads][d] of q's dtype")
+def _rows_of_heads(name: str, t, dtype, at: int):
+    """Checks rows of [heads][d] dense elements on device ``at``; returns the shape and the rows' distance in elements."""
+    if t.get_device() != at or t.dim() != 3 or t.dtype != dtype:
+        raise ValueError(f"{name} must be a tensor [rows][heads][d] of q's dtype and device")
     n, h, d = shape = t.shape
     row, head, one = t.stride()
     if one != 1 or (h > 1 and head != d):
@@ -568,17 +585,17 @@ def _rows_of_heads(name: str, t, dtype):
     return shape, row if n > 1 else h * d
 
 
-def _table32(name: str, t, n: int) -> int:
-    """Checks an int32 [n] table; returns its address."""
-    if t.dtype is not _torch().int32 or not t.is_cuda or not t.is_contiguous() or t.shape != (n,):
+def _table32(name: str, t, n: int, at: int) -> int:
+    """Checks an int32 [n] table on device ``at``; returns its address."""
+    if t.dtype is not _torch().int32 or t.get_device() != at or not t.is_contiguous() or t.shape != (n,):
         raise ValueError(f"{name} must be int32 [{n}] on the device")
     return t.data_ptr()
 
 
-def _dense(name: str, t, shape, dtype) -> int:
-    """Checks a contiguous tensor; returns its address."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+def _dense(name: str, t, shape, dtype, at: int) -> int:
+    """Checks a contiguous tensor on device ``at``; returns its address."""
+    if t.dtype != dtype or t.get_device() != at or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous tensor {list(shape)} of {dtype} on the device")
     return t.data_ptr()
 
 
@@ -627,25 +644,25 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
     """
     torch = _torch()
     dtype = q.dtype
-    dt = _dtype16(q, "q")
-    (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
-    k_shape, sk = _rows_of_heads("k", k, dtype)
+    dt, at = _dtype16(q, "q"), _device_of("q", q)
+    (T, Hq, d), sq = _rows_of_heads("q", q, dtype, at)
+    k_shape, sk = _rows_of_heads("k", k, dtype, at)
     Hk = k_shape[1]
     if k_shape != (T, Hk, d):
         raise ValueError("k must have q's rows and head size")
     qw = kw = tab = pos = rotary = max_pos = 0
     if q_weight is not None:
-        qw = _dense("q_weight", q_weight, (d,), torch.float32)
+        qw = _dense("q_weight", q_weight, (d,), torch.float32, at)
     if k_weight is not None:
-        kw = _dense("k_weight", k_weight, (d,), torch.float32)
+        kw = _dense("k_weight", k_weight, (d,), torch.float32, at)
     if table is not None:
         if positions is None:
             raise ValueError("a table needs positions")
         if table.dim() != 2:
             raise ValueError("table must be [max_pos][rotary]")
         max_pos, rotary = shape = table.shape
-        tab = _dense("table", table, shape, torch.float32)
-        pos = _table32("positions", positions, T)
+        tab = _dense("table", table, shape, torch.float32, at)
+        pos = _table32("positions", positions, T, at)
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     if out is None:
@@ -653,8 +670,8 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=Non
         k_out = _new(k_shape, dtype, q.device, stream)
     else:
         q_out, k_out = out
-        _dense("out[0]", q_out, (T, Hq, d), dtype)
-        _dense("out[1]", k_out, k_shape, dtype)
+        _dense("out[0]", q_out, (T, Hq, d), dtype, at)
+        _dense("out[1]", k_out, k_shape, dtype, at)
     st = load().kda_head_norm_rope(q.data_ptr(), sq, k.data_ptr(), sk, qw, kw, tab, max_pos, pos, q_out.data_ptr(),
                                    k_out.data_ptr(), T, Hq, Hk, d, rotary, ROPE_LAYOUTS[layout], 1 if norm else 0, eps,
                                    dt, _handle(stream, q.device))
@@ -668,10 +685,10 @@ def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks, stream):
     if not 0 < window <= 0x7fffffff or not 0 <= sinks <= 0x7fffffff:
         raise ValueError("window and sinks must be 32-bit numbers, window >= 1, sinks >= 0")
     dtype = q.dtype
-    dt = _dtype16(q, "q")
-    (T, Hq, d), sq = _rows_of_heads("q", q, dtype)
-    k_shape, sk = _rows_of_heads("k", k, dtype)
-    v_shape, sv = _rows_of_heads("v", v, dtype)
+    dt, at = _dtype16(q, "q"), _device_of("q", q)
+    (T, Hq, d), sq = _rows_of_heads("q", q, dtype, at)
+    k_shape, sk = _rows_of_heads("k", k, dtype, at)
+    v_shape, sv = _rows_of_heads("v", v, dtype, at)
     Hk = k_shape[1]
     if k_shape != (T, Hk, d) or v_shape != k_shape:
         raise ValueError("k and v must have q's rows and head size, and the same heads")
@@ -680,13 +697,13 @@ def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks, stream):
         if kv_pool.dim() != 5:
             raise ValueError("kv_pool must be [num_slots][2][Hk][rows][d]")
         num_slots, _, _, rows, _ = kv_pool.shape
-        pool = _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), dtype)
-    ids = 0 if slots is None else _table32("slots", slots, N)
+        pool = _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), dtype, at)
+    ids = 0 if slots is None else _table32("slots", slots, N, at)
     if out is None:
         out = _new((T, Hq, d), dtype, q.device, stream)
     else:
-        _dense("out", out, (T, Hq, d), dtype)
-    return dt, (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv), ids, (pool, num_slots, rows), out, T, Hq, Hk, d
+        _dense("out", out, (T, Hq, d), dtype, at)
+    return dt, at, (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv), ids, (pool, num_slots, rows), out, T, Hq, Hk, d
 
 
 def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=None, slots=None, starts=None,
@@ -700,10 +717,9 @@ def window_prefill(q, k, v, cu_seqlens, window: int, sinks: int = 0, kv_pool=Non
     [T][Hq][d] (rows of padded sequences keep what ``out`` held).
     """
     N = int(cu_seqlens.shape[0]) - 1
-    dt, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks,
-                                                             stream)
-    cu = _table32("cu_seqlens", cu_seqlens, N + 1)
-    st = load().kda_window_prefill(*qkv, cu, 0 if starts is None else _table32("starts", starts, N), ids, *pool,
+    dt, at, qkv, ids, pool, out, T, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks, stream)
+    cu = _table32("cu_seqlens", cu_seqlens, N + 1, at)
+    st = load().kda_window_prefill(*qkv, cu, 0 if starts is None else _table32("starts", starts, N, at), ids, *pool,
                                    out.data_ptr(), N, T, Hq, Hk, d, window, sinks, d ** -0.5 if scale is None else scale,
                                    dt, _handle(stream, q.device))
     if st != KDA_OK:
@@ -718,9 +734,8 @@ def window_decode(q, k, v, positions, kv_pool, window: int, sinks: int = 0, slot
     kv_pool in place.  Returns out [N][Hq][d] (rows of padded sequences, slot -1, keep what ``out`` held).
     """
     N = q.shape[0]
-    dt, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks,
-                                                             stream)
-    st = load().kda_window_decode(*qkv, _table32("positions", positions, N), ids, *pool, out.data_ptr(), N, Hq, Hk, d,
+    dt, at, qkv, ids, pool, out, _, Hq, Hk, d = _window_args(q, k, v, kv_pool, slots, N, out, window, sinks, stream)
+    st = load().kda_window_decode(*qkv, _table32("positions", positions, N, at), ids, *pool, out.data_ptr(), N, Hq, Hk, d,
                                   window, sinks, d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
     if st != KDA_OK:
         raise KdaError(st, "kda_window_decode")
@@ -731,11 +746,12 @@ def _pools(pools):
     """A host array of (base, entry_bytes) pairs, the number of slots and the device of a list of pool tensors."""
     if not pools:
         raise ValueError("at least one pool is needed")
+    at = _device_of("pools[0]", pools[0])
     n = pools[0].shape[0] if pools[0].dim() else 0
     flat = []
     for p in pools:
-        if not p.is_cuda or not p.is_contiguous() or p.dim() < 2 or p.shape[0] != n or not p.numel():
-            raise ValueError("every pool must be a contiguous CUDA tensor [num_slots][...] of the same num_slots")
+        if p.get_device() != at or not p.is_contiguous() or p.dim() < 2 or p.shape[0] != n or not p.numel():
+            raise ValueError("every pool must be a contiguous tensor [num_slots][...] of the same num_slots and device")
         flat += (p.data_ptr(), p.numel() // n * p.element_size())   # (the stride of an axis of one may be anything)
     return (ctypes.c_int64 * len(flat))(*flat), n, pools[0].device
 
@@ -746,9 +762,10 @@ def slots_copy(pools, src, dst, stream=None) -> None:
     int32 on the device (targets distinct and no other row's source).
     """
     array, n, device = _pools(pools)
+    at = device.index
     M = int(src.shape[0])
-    st = load().kda_slots_copy(ctypes.addressof(array), len(pools), n, _table32("src", src, M), _table32("dst", dst, M),
-                               M, _handle(stream, device))
+    st = load().kda_slots_copy(ctypes.addressof(array), len(pools), n, _table32("src", src, M, at),
+                               _table32("dst", dst, M, at), M, _handle(stream, device))
     if st != KDA_OK:
         raise KdaError(st, "kda_slots_copy")
 
@@ -759,12 +776,13 @@ def slots_compact(pools, slots, new_slots=None, stream=None):
     device.  Returns new_slots [N] int32, where each went (-1 stays).
     """
     array, n, device = _pools(pools)
+    at = device.index
     N = int(slots.shape[0])
-    _table32("slots", slots, N)
+    _table32("slots", slots, N, at)
     if new_slots is None:
         new_slots = _new((N,), _torch().int32, device, stream)
     else:
-        _table32("new_slots", new_slots, N)
+        _table32("new_slots", new_slots, N, at)
     st = load().kda_slots_compact(ctypes.addressof(array), len(array) // 2, n, _ptr(slots), _ptr(new_slots), N,
                                   _handle(stream, device))
     if st != KDA_OK:

@@ -35,6 +35,7 @@ class Library:
 def library(monkeypatch):
     lib = Library()
     monkeypatch.setattr(kda, "load", lambda: lib)
+    monkeypatch.setattr(kda, "_current_device", lambda: 0, raising=False)
     return lib
 
 
@@ -94,3 +95,69 @@ def test_a_single_slot_that_is_a_view_is_cleared_and_nothing_beside_it():
     kda.slots_copy([t.transpose(0, 1)], torch.tensor([-1], dtype=torch.int32, device="cuda"),
                    torch.tensor([0], dtype=torch.int32, device="cuda"))
     assert not t.any()
+
+
+def everywhere():
+    """Every call with its tensors: {name: (call(tensors), tensors)}; each runs on device 0 as it is."""
+    import torch
+    half = lambda *s: OnGpu(torch.zeros(*s, dtype=torch.bfloat16))   # noqa: E731
+    f32 = lambda *s: OnGpu(torch.zeros(*s))   # noqa: E731
+    q, k, v, pool, out = half(4, 8, 64), half(4, 2, 64), half(4, 2, 64), half(4, 2, 2, 20, 64), half(4, 8, 64)
+    rope = dict(q=q, k=k, q_weight=f32(64), k_weight=f32(64), positions=int32([0] * 4), table=f32(9, 32))
+    window = dict(q=q, k=k, v=v, kv_pool=pool, slots=int32([0] * 4), out=out)
+    return {
+        "rope": (lambda a, b, **kw: kda.head_norm_rope(out=(a, b), stream=0, **kw), dict(rope, a=half(4, 8, 64), b=half(4, 2, 64))),
+        "prefill": (lambda **kw: kda.window_prefill(window=16, stream=0, **kw),
+                    dict(window, cu_seqlens=int32([0, 1, 2, 3, 4]), starts=int32([0] * 4))),
+        "decode": (lambda **kw: kda.window_decode(window=16, stream=0, **kw), dict(window, positions=int32([0] * 4))),
+        "copy": (lambda a, b, **kw: kda.slots_copy([a, b], stream=0, **kw),
+                 dict(a=pool, b=f32(4, 8), src=int32([0]), dst=int32([1]))),
+        "compact": (lambda a, b, **kw: kda.slots_compact([a, b], stream=0, **kw),
+                    dict(a=pool, b=f32(4, 8), slots=int32([0]), new_slots=int32([0]))),
+    }
+
+
+@pytest.mark.parametrize("which", ["rope", "prefill", "decode", "copy", "compact"])
+def test_tensors_of_two_devices_are_refused(library, which):
+    call, tensors = everywhere()[which]
+    call(**tensors)
+    assert len(library.calls) == 1
+    for name, t in tensors.items():
+        with pytest.raises(ValueError):
+            call(**dict(tensors, **{name: OnGpu(t.t, 1)}))
+        with pytest.raises(ValueError):
+            call(**dict(tensors, **{name: t.t}))
+    assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("which", ["rope", "prefill", "decode", "copy", "compact"])
+def test_tensors_beside_the_current_device_are_refused(library, which):
+    """The library launches on the current device."""
+    call, tensors = everywhere()[which]
+    with pytest.raises(ValueError, match="current device"):
+        call(**{name: OnGpu(t.t, 1) for name, t in tensors.items()})
+    assert library.calls == []
+
+
+@pytest.mark.parametrize("which", ["rope", "prefill", "decode", "copy", "compact"])
+def test_a_stream_of_another_device_is_refused(library, which):
+    class Stream:
+        cuda_stream, device_index = 4096, 1
+
+    call, tensors = everywhere()[which]
+    names = {"rope": "kda_head_norm_rope", "prefill": "kda_window_prefill", "decode": "kda_window_decode",
+             "copy": "kda_slots_copy", "compact": "kda_slots_compact"}
+    fn = {"rope": kda.head_norm_rope, "prefill": kda.window_prefill, "decode": kda.window_decode, "copy": kda.slots_copy,
+          "compact": kda.slots_compact}[which]
+    kw = dict(tensors)
+    if which in ("copy", "compact"):
+        kw["pools"] = [kw.pop("a"), kw.pop("b")]
+    elif which == "rope":
+        kw["out"] = (kw.pop("a"), kw.pop("b"))
+    else:
+        kw["window"] = 16
+    with pytest.raises(ValueError):
+        fn(stream=Stream(), **kw)
+    Stream.device_index = 0
+    fn(stream=Stream(), **kw)
+    assert [c[0] for c in library.calls] == [names[which]] and library.calls[0][1][-1] == 4096
