@@ -339,10 +339,12 @@ struct Ctx {
         atomicOr(p.err, kErrWaitTimeout);
         *abort = 1;
     }
-    // a wait of the whole warp, the same answer in every lane
-    __device__ bool wait(uint32_t bar, int phase) const
+    // A wait of the whole warp, the same answer in every lane: lanes poll and see the abort
+    // flag one by one, and one that ran on without the others would meet no partner at
+    // the next instruction of the whole warp.
+    __device__ bool wait(uint32_t bar, int phase, uint32_t limit = 1u << 18) const
     {
-        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, limit)) != 0;
     }
 };
 
@@ -654,7 +656,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
     bool ok = true;
     for (int item = 0; ok; item++) {
         const Item &now = x.c.items[item & 1];
-        ok = mbar_wait(x.bars.item_full(item & 1), (item / 2) & 1, x.abort);
+        ok = x.wait(x.bars.item_full(item & 1), item / 2);
         if (!ok || now.tokens == 0) break;
         const Span rows(now, p.tile_tokens, q);
         const int lo_row = rows.first + (32 * (warp & 3) * p.inv_G >> 16);
@@ -667,16 +669,21 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             if (!sees(t, rows.first, rows.last, p.window, p.sinks)) continue;
             // every key of the tile visible to every row of the warp: no test per key
             const bool whole = t.complete && t.keys == kKeys && t.hi <= lo_row && t.low > hi_row - p.window;
-            ok = mbar_wait(x.bars.s_full(q), it & 1, x.abort, KDA_WAIT_LIMIT_SCORES);
-            if (!ok) break;
+            // Lanes may give up one by one: the vote on the maxima below is also the one on that
+            // (a vote here: 405 us for 399, 8192 rows, W 4096); a lane that gave up goes
+            // on until then with what its row of TMEM holds.
+            const bool got = mbar_wait(x.bars.s_full(q), it & 1, x.abort, KDA_WAIT_LIMIT_SCORES);
             it++;
             if (dead) {                                  // whatever is there will do as these rows' P
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
                 if (lane == 0) {
                     mbar_arrive(x.bars.p_half(q));
                     mbar_arrive(x.bars.p_ready(q));
                 }
                 continue;
             }
+            __syncwarp();
             tc_fence_after();
             uint32_t s[4][32];
 #pragma unroll
@@ -712,7 +719,9 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             const float was = slope<E>(m, c2);
             const bool behind = m != -INFINITY && (top - m) * was > kLag;
-            if (__any_sync(0xffffffffu, behind)) {
+            if (__any_sync(0xffffffffu, behind || !got)) {
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
                 // the products into O so far were complete before these scores were, and
                 // the next one waits for this warp
                 const float f = behind ? ex2(fmaf(m - top, c2, residue(top, slope<E>(top, c2)) - residue(m, was))) : 1.f;
@@ -762,7 +771,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         __syncwarp();
         if (lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
         if (!ok || !rows.tokens) continue;
-        ok = mbar_wait(x.bars.o_done(q), mine & 1, x.abort);
+        ok = x.wait(x.bars.o_done(q), mine);
         if (!ok) break;
         tc_fence_after();
         mine++;
