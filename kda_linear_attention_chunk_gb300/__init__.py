@@ -697,6 +697,8 @@ def _window_args(q, k, v, kv_pool, slots, N, out, window, sinks, stream):
         if kv_pool.dim() != 5:
             raise ValueError("kv_pool must be [num_slots][2][Hk][rows][d]")
         num_slots, _, _, rows, _ = kv_pool.shape
+        if not num_slots or not rows:            # its null address would stand for no cache
+            raise ValueError("kv_pool has no entry")
         pool = _dense("kv_pool", kv_pool, (num_slots, 2, Hk, rows, d), dtype, at)
     ids = 0 if slots is None else _table32("slots", slots, N, at)
     if out is None:

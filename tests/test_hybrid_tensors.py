@@ -161,3 +161,15 @@ def test_a_stream_of_another_device_is_refused(library, which):
     Stream.device_index = 0
     fn(stream=Stream(), **kw)
     assert [c[0] for c in library.calls] == [names[which]] and library.calls[0][1][-1] == 4096
+
+
+@pytest.mark.parametrize("shape", [(0, 2, 2, 20, 64), (4, 2, 2, 0, 64)])
+def test_a_ring_cache_without_entries_is_refused(library, shape):
+    """Its address is null, which would mean that nothing is cached."""
+    import torch
+    for which in ("prefill", "decode"):
+        call, tensors = everywhere()[which]
+        tensors = {k: t for k, t in tensors.items() if k not in ("slots", "starts")}
+        with pytest.raises(ValueError):
+            call(**dict(tensors, kv_pool=OnGpu(torch.zeros(shape, dtype=torch.bfloat16))))
+    assert library.calls == []
