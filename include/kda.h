@@ -564,6 +564,7 @@ typedef struct {
  *               rows may name one source; the targets must be distinct, and no
  *               target may be a source of another row.  An id outside
  *               [-1, num_slots) skips its row and sets bit 8.
+ *   M           at least 1 (N below too).
  *   num_slots   entries in every pool, at most KDA_MAX_POOL_SLOTS.
  * Returns a kda_status.
  */

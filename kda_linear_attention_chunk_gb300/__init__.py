@@ -761,13 +761,15 @@ def _pools(pools):
 def slots_copy(pools, src, dst, stream=None) -> None:
     """Copies slot entries in every pool of a list at once, on torch CUDA tensors: entry dst[i] becomes entry src[i],
     or zeros where src[i] is -1; dst[i] = -1 skips a row.  pools: contiguous [num_slots][...] tensors; src, dst: [M]
-    int32 on the device (targets distinct and no other row's source).
+    int32 on the device (targets distinct and no other row's source).  Without rows nothing is done.
     """
     array, n, device = _pools(pools)
     at = device.index
     M = int(src.shape[0])
-    st = load().kda_slots_copy(ctypes.addressof(array), len(pools), n, _table32("src", src, M, at),
-                               _table32("dst", dst, M, at), M, _handle(stream, device))
+    ids = _table32("src", src, M, at), _table32("dst", dst, M, at)
+    if not M:
+        return
+    st = load().kda_slots_copy(ctypes.addressof(array), len(pools), n, *ids, M, _handle(stream, device))
     if st != KDA_OK:
         raise KdaError(st, "kda_slots_copy")
 
@@ -785,6 +787,8 @@ def slots_compact(pools, slots, new_slots=None, stream=None):
         new_slots = _new((N,), _torch().int32, device, stream)
     else:
         _table32("new_slots", new_slots, N, at)
+    if not N:
+        return new_slots
     st = load().kda_slots_compact(ctypes.addressof(array), len(array) // 2, n, _ptr(slots), _ptr(new_slots), N,
                                   _handle(stream, device))
     if st != KDA_OK:

@@ -173,3 +173,28 @@ def test_a_ring_cache_without_entries_is_refused(library, shape):
         with pytest.raises(ValueError):
             call(**dict(tensors, kv_pool=OnGpu(torch.zeros(shape, dtype=torch.bfloat16))))
     assert library.calls == []
+
+
+def test_an_empty_list_of_moves_is_a_call_without_work(library):
+    """A step that forks nothing and a batch without live sequences; what is wrong with the tensors is still refused."""
+    import torch
+    pool, none = OnGpu(torch.zeros(3, 8)), int32([])
+    assert kda.slots_copy([pool], none, none, stream=0) is None
+    new = int32([])
+    assert kda.slots_compact([pool], none, new, stream=0) is new
+    assert library.calls == []
+    for call in (lambda: kda.slots_copy([pool], none, int32([0]), stream=0), lambda: kda.slots_copy([], none, none, stream=0),
+                 lambda: kda.slots_copy([pool], none, int32([], index=1), stream=0),
+                 lambda: kda.slots_compact([pool], none, int32([0]), stream=0)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.gpu
+def test_an_empty_table_compacts_to_an_empty_one():
+    import torch
+    pool = torch.ones(3, 8, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    kda.slots_copy([pool], none, none)
+    got = kda.slots_compact([pool], none)
+    assert got.shape == (0,) and got.dtype == torch.int32 and got.is_cuda and bool((pool == 1).all())
