@@ -443,15 +443,17 @@ int kda_short_conv(const uint16_t *xq, const uint16_t *xk, const uint16_t *xv,
  *             sequence (0 is its first token) is kept in row p while p < sinks,
  *             else in row sinks + (p - sinks) mod (pool_rows - sinks), which a
  *             later position takes over.  pool_rows >= sinks + window.  Rows
- *             that hold no visible position are never read (they may hold
- *             anything).
+ *             that hold no visible position reach no output (they may hold
+ *             anything), but may be read along with their neighbours, as may the
+ *             call's other rows: nothing of an entry, nor of q, k and v, may be
+ *             written while a call that names it runs.
  *  Visible    the query at position p sees the positions j <= p with
  *             j > p - window or j < sinks.  A window of at least the longest
  *             context is plain causal attention.
  *  Heads      Hq query heads share Hk key heads in order: query head h reads
  *             key head h / (Hq / Hk); Hq a multiple of Hk, at most 128 times it.
- *  Capture    every call can be captured into a CUDA graph, after one call of its
- *             kind (dtype, d) outside of a capture, which sets the kernels up.
+ *  Capture    every call can be captured into a CUDA graph, after any one call of
+ *             this library on the device outside of a capture.
  */
 typedef enum { KDA_BF16 = 0, KDA_F16 = 1 } kda_dtype;
 typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
