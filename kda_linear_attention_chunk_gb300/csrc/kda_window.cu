@@ -371,7 +371,7 @@ __device__ __forceinline__ int claimed_cta(uint32_t answer)
 // Writes the CTA's next item to `item`; `claims`: how many were made (0: its own comes
 // first).  The lanes of the converged warp agree on what is returned: 1 found, 0 none
 // left, -1 a wait gave up.
-__device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item)
+template <bool LONG> __device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item)
 {
     const WindowParams &p = x.p;
     const int span = 2 * p.tile_tokens, lane = x.lane;
@@ -392,7 +392,9 @@ __device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item)
         claims++;
         if (at < 0) return 0;
         const int number = p.items - 1 - at, slot = number / p.Hk, hk = number - slot * p.Hk;
-        const Rows r = rows_of(p, span, slot, lane, hk == 0);
+        // (the other kernel of a divided batch goes through all sequences, and reports)
+        const Rows r = LONG ? rows_in(p, sequence_of_long(p, span, slot, lane), span, lane, false)
+                            : rows_of(p, span, slot, lane, hk == 0);
         if (!r.n) continue;          // past the sequence's rows, or padded
         if (lane == 0) {
             item.nruns = 0;
@@ -415,7 +417,7 @@ __device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item)
 }
 
 // ---- items and loads ---------------------------------------------------------
-template <typename E, int D>
+template <typename E, int D, bool LONG>
 __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
 {
     using L = Layout<E, D>;
@@ -427,7 +429,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         Item &now = x.c.items[item & 1];
         if (item >= 2) ok = x.wait(x.bars.item_empty(item & 1), item / 2 - 1);
         if (!ok) break;
-        const int found = find_item(x, claims, now);
+        const int found = find_item<LONG>(x, claims, now);
         ok = found >= 0;
         more = found > 0;
         if (!ok) break;
@@ -819,12 +821,17 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
     if (!ok) x.give_up();
 }
 
-template <typename E, int D>
+// LONG: for a divided batch
+template <typename E, int D, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 window_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowParams p)
 {
     using L = Layout<E, D>;
     extern __shared__ uint8_t smem_raw[];
+    if (LONG) {                      // mostly there is nothing to do, and the other kernel wants the SMs
+        grid_go_on();
+        if (!__syncthreads_or(sees_long(p, threadIdx.x, kThreads))) return;
+    }
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));
     Ctl &c = *reinterpret_cast<Ctl *>(smem + L::kCtl);
@@ -870,7 +877,7 @@ window_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     const Ctx x{p, c, bars, smem, base, c.tmem, lane, &c.abort};
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (warp == 8) load_role<E, D>(x, maps);
+        if (warp == 8) load_role<E, D, LONG>(x, maps);
         else if (warp == 10) patch_role<E, D>(x);
         else product_role<E, D>(x, warp == 11);
     } else {
@@ -958,14 +965,26 @@ bool make_map(CUtensorMap *m, const void *base, bool f16, int d, int64_t n1, int
 // (the other kernel spreads each over eight CTAs).  Measured (us, warp-MMA / tiles;
 // G = 4, d = 128): 64 sequences, window 1024: 16 rows 58 / 77, 32 rows 72 / 80, 64
 // rows 121 / 81; one sequence, window 4096: 32 rows 21 / 56, 256 rows 48 / 63; 16
-// fresh sequences: 64 rows 22 / 20, 256 rows 31 / 19.
+// fresh sequences: 64 rows 22 / 20, 256 rows 31 / 19.  Over G = 1 to 128 and d = 64 and 128 the
+// quotient of the two is, for the 64 sequences, 0.62-0.83 at 16 rows, 0.75-1.15 at 32 and
+// 1.2-1.8 at 64; for the one sequence 0.3-0.5 at 32 rows and 0.4-1.2 at 256.
 bool few_rows(const WindowParams &p, int num_sms)
 {
     const int64_t rows = (int64_t)p.T * p.G;
     return rows <= (int64_t)32 * p.N || (rows <= (int64_t)256 * p.N && p.items * 8 <= num_sms);
 }
 
-template <typename E, int D>
+// The rule goes by the average, which says nothing of a long sequence among many short or
+// empty ones.  So where few_rows holds, a batch of kDividedRows query rows a key head or
+// more is divided (kda_window.h): the tiles take its sequences of more than kLongRows,
+// and their CTAs leave at once where there are none.  Measured (us, undivided / divided; G = 4,
+// d = 128): one sequence of 512 tokens among 63 empty ones, window 1024 74 / 34, window
+// 4096 197 / 73; 2048 tokens among 255 empty ones 270 / 61 and 715 / 132; 64 sequences of
+// eight tokens each, of which none is long, 74 / 77.  Below, division gains less (128
+// tokens among 15 empty ones, 512 rows: 34 / 34 and 85 / 73).
+constexpr int kLongRows = 256, kDividedRows = 1024;
+
+template <typename E, int D, bool LONG>
 cudaError_t launch_tiles(const WindowArgs &a, const WindowParams &p)
 {
     Maps maps;
@@ -983,21 +1002,33 @@ cudaError_t launch_tiles(const WindowArgs &a, const WindowParams &p)
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, a.device, [&]() {
         cudaFuncAttributes built;
-        cudaError_t r = cudaFuncGetAttributes(&built, window_prefill_kernel<E, D>);
+        cudaError_t r = cudaFuncGetAttributes(&built, window_prefill_kernel<E, D, LONG>);
         if (r == cudaSuccess && built.numRegs != kRegs) r = cudaErrorInvalidConfiguration;
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(window_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            r = cudaFuncSetAttribute(window_prefill_kernel<E, D, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         return r;
     });
     if (e != cudaSuccess) return e;
-    window_prefill_kernel<E, D><<<p.items, kThreads, smem, a.stream>>>(maps, p);
+    window_prefill_kernel<E, D, LONG><<<p.items, kThreads, smem, a.stream>>>(maps, p);
     return cudaGetLastError();
 }
 
 template <typename E, int D>
 cudaError_t launch(const WindowArgs &a, const WindowParams &p)
 {
-    cudaError_t e = few_rows(p, a.num_sms) ? launch_window_rows(a) : launch_tiles<E, D>(a, p);
+    cudaError_t e;
+    if (!few_rows(p, a.num_sms)) {
+        e = launch_tiles<E, D, false>(a, p);
+    } else if ((int64_t)p.T * p.G < kDividedRows) {
+        e = launch_window_rows(a, 0);
+    } else {
+        WindowParams l = p;
+        l.longer = kLongRows;
+        const int64_t most = (int64_t)p.T * p.G / (kLongRows + 1);   // long sequences that there can be
+        l.items = (int)((p.T / (2 * p.tile_tokens) + (most < p.N ? most : p.N)) * p.Hk);
+        e = launch_tiles<E, D, true>(a, l);
+        if (e == cudaSuccess) e = launch_window_rows(a, kLongRows);
+    }
     if (e != cudaSuccess || !a.pool) return e;
     // its CTAs start where those of the attention kernel have ended
     cudaLaunchConfig_t cfg = {};

@@ -48,6 +48,7 @@ struct WindowParams {
     int G, tile_tokens;              // query heads per key head; tokens of a query tile
     int inv_G;                       // ceil(2^16 / G): r / G = r inv_G >> 16 for r < 128
     int items;                       // numbers of items, at least as many as there are
+    int longer;                      // > 0: the batch is divided (divided() below)
     int groups;                      // groups of up to 16 query heads per key head (warp-MMA kernel)
     float scale_log2;
     int *err;
@@ -89,15 +90,59 @@ __device__ __forceinline__ Sequence sequence_of(const WindowParams &p, int span,
     return s;
 }
 
-// The rows that number `number` stands for, all checked; `reports`: whether this
-// warp tells of entries out of range.
+// A divided batch: the tiles take the sequences of more than `longer` query rows a key
+// head, the warp-MMA kernel the others.
+__device__ __forceinline__ bool is_long(const WindowParams &p, int len) { return p.longer && (int64_t)len * p.G > p.longer; }
+
+// Whether the block's share of the table, every `step`-th from `at` on, has a long one.
+__device__ __forceinline__ bool sees_long(const WindowParams &p, int at, int step)
+{
+    bool any = false;
+    for (int n = at; n < p.N; n += step)
+        any |= is_long(p, clamp_row(p.cu[n + 1], p.T, nullptr) - clamp_row(p.cu[n], p.T, nullptr));
+    return any;
+}
+
+// The sequence of the number-th span of the long ones alone, by a converged warp that
+// goes through the table; part -1: there are fewer spans.
+__device__ __forceinline__ Sequence sequence_of_long(const WindowParams &p, int span, int number, int lane)
+{
+    Sequence s = {0, 0, 0, 0, -1};
+    int before = 0;                  // spans in what was gone through
+    for (int base = 0; base < p.N; base += 32) {
+        const int at = min(base + lane, p.N - 1);
+        const int cu0 = p.cu[at], cu1 = p.cu[at + 1];
+        const int len = clamp_row(cu1, p.T, nullptr) - clamp_row(cu0, p.T, nullptr);
+        const int mine = base + lane < p.N && is_long(p, len) ? (len - 1) / span + 1 : 0;
+        int end = mine;              // spans up to this lane's
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += x;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + end > number);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            s.cu0 = __shfl_sync(0xffffffffu, cu0, who);
+            s.cu1 = __shfl_sync(0xffffffffu, cu1, who);
+            s.part = number - before - __shfl_sync(0xffffffffu, end - mine, who);
+            s.start = p.starts ? p.starts[base + who] : 0;
+            s.slot = p.slots ? p.slots[base + who] : base + who;
+            return s;
+        }
+        before += __shfl_sync(0xffffffffu, end, 31);
+    }
+    return s;
+}
+
+// The rows that a span stands for, all checked; `reports`: whether this warp tells of
+// entries out of range.
 struct Rows {
     int bos, len, start, entry;      // the sequence's first row, rows, context length, cache entry
     int from, n;                     // the span's first row within the sequence, and its rows (0: none)
 };
-__device__ __forceinline__ Rows rows_of(const WindowParams &p, int span, int number, int lane, bool reports)
+__device__ __forceinline__ Rows rows_in(const WindowParams &p, const Sequence &s, int span, int lane, bool reports)
 {
-    const Sequence s = sequence_of(p, span, number, lane);
     reports = reports && lane == 0 && s.part == 0;
     Rows r;
     r.bos = clamp_row(s.cu0, p.T, reports ? p.err : nullptr);
@@ -114,6 +159,10 @@ __device__ __forceinline__ Rows rows_of(const WindowParams &p, int span, int num
     r.n = s.part < 0 || from >= r.len || r.entry < 0 ? 0 : (int)min((int64_t)span, r.len - from);
     r.from = r.n ? (int)from : 0;
     return r;
+}
+__device__ __forceinline__ Rows rows_of(const WindowParams &p, int span, int number, int lane, bool reports)
+{
+    return rows_in(p, sequence_of(p, span, number, lane), span, lane, reports);
 }
 
 template <typename E> struct Half2;
@@ -153,7 +202,7 @@ inline WindowParams window_params(const WindowArgs &a)
 }
 
 // The warp-MMA kernel for few rows a sequence (kda_window_rows.cu), without the
-// writing of the cache.
-cudaError_t launch_window_rows(const WindowArgs &a);
+// writing of the cache; longer > 0: for a divided batch, behind the tiles' launch.
+cudaError_t launch_window_rows(const WindowArgs &a, int longer);
 
 }  // namespace kda

@@ -118,6 +118,11 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
     const int part = warp / SHARE, sub = warp % SHARE;   // which keys, which rows
 
     if (MANY) grid_go_on();
+    // In a divided batch this grid must not end before that of the tiles, which is why its
+    // last cluster waits for it: the cache kernel waits for this one only.
+    auto leave = [&]() {
+        if (MANY && blockIdx.x + ranks >= gridDim.x) grid_wait();
+    };
     int unit = blockIdx.x / ranks;
     const int group = unit % p.groups;
     unit /= p.groups;
@@ -131,7 +136,10 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
     int entry, t0, bos, start, first, tokens = 1;
     if (MANY) {
         const Rows r = rows_of(p, p.tile_tokens, unit / p.Hk, lane, reports);
-        if (!r.n) return;
+        if (!r.n || is_long(p, r.len)) {
+            leave();
+            return;
+        }
         entry = r.entry;
         bos = r.bos;
         start = r.start;
@@ -435,6 +443,7 @@ window_rows_kernel(const __grid_constant__ WindowParams p)
         *reinterpret_cast<uint2 *>(p.out + ((int64_t)(t0 + tok) * p.Hq + head0 + r - tok * heads) * D + 4 * d4) = r2;
     }
     if (ranks > 1) cluster.sync();      // nobody leaves while its shared memory is being read
+    leave();
 }
 
 template <typename E, int D, bool MANY, int SHARE>
@@ -461,12 +470,14 @@ cudaError_t launch(const WindowArgs &a, WindowParams p)
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.longer ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, window_rows_kernel<E, D, MANY, SHARE>, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -482,16 +493,17 @@ cudaError_t launch_shared(const WindowArgs &a, const WindowParams &p)
 }
 
 template <bool MANY>
-cudaError_t launch_rows(const WindowArgs &a)
+cudaError_t launch_rows(const WindowArgs &a, int longer)
 {
-    const WindowParams p = window_params(a);
+    WindowParams p = window_params(a);
+    p.longer = longer;
     if (a.d == 128) return a.f16 ? launch_shared<__half, 128, MANY>(a, p) : launch_shared<__nv_bfloat16, 128, MANY>(a, p);
     return a.f16 ? launch_shared<__half, 64, MANY>(a, p) : launch_shared<__nv_bfloat16, 64, MANY>(a, p);
 }
 
 }  // namespace
 
-cudaError_t launch_window_decode(const WindowArgs &a) { return launch_rows<false>(a); }
-cudaError_t launch_window_rows(const WindowArgs &a) { return launch_rows<true>(a); }
+cudaError_t launch_window_decode(const WindowArgs &a) { return launch_rows<false>(a, 0); }
+cudaError_t launch_window_rows(const WindowArgs &a, int longer) { return launch_rows<true>(a, longer); }
 
 }  // namespace kda
