@@ -374,7 +374,7 @@ __device__ __forceinline__ int claimed_cta(uint32_t answer)
 // Writes the CTA's next item to `item`; `claims`: how many were made (0: its own comes
 // first).  The lanes of the converged warp agree on what is returned: 1 found, 0 none
 // left, -1 a wait gave up.
-template <bool LONG> __device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item)
+template <bool LONG> __device__ __forceinline__ int find_item(const Ctx &x, int &claims, Item &item, const LongSpans &l)
 {
     const WindowParams &p = x.p;
     const int span = 2 * p.tile_tokens, lane = x.lane;
@@ -396,7 +396,7 @@ template <bool LONG> __device__ __forceinline__ int find_item(const Ctx &x, int 
         if (at < 0) return 0;
         const int number = p.items - 1 - at, slot = number / p.Hk, hk = number - slot * p.Hk;
         // (the other kernel of a divided batch goes through all sequences, and reports)
-        const Rows r = LONG ? rows_in(p, sequence_of_long(p, span, slot, lane), span, lane, false)
+        const Rows r = LONG ? rows_in(p, sequence_of_long(p, span, slot, lane, l), span, lane, false)
                             : rows_of(p, span, slot, lane, hk == 0);
         if (!r.n) continue;          // past the sequence's rows, or padded
         if (lane == 0) {
@@ -428,11 +428,12 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
     const uint32_t sq = x.base, skv = x.base + 2 * L::kTile;
     int it = 0, claims = 0, item = 0, qs[2] = {0, 0};    // tiles and query tiles loaded, items written
     bool ok = true, more = true;
+    const LongSpans l = LONG ? count_long(p, 2 * p.tile_tokens, x.lane) : LongSpans();
     while (ok && more) {
         Item &now = x.c.items[item & 1];
         if (item >= 2) ok = x.wait(x.bars.item_empty(item & 1), item / 2 - 1);
         if (!ok) break;
-        const int found = find_item<LONG>(x, claims, now);
+        const int found = find_item<LONG>(x, claims, now, l);
         ok = found >= 0;
         more = found > 0;
         if (!ok) break;
@@ -833,7 +834,9 @@ window_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     if (LONG) {                      // mostly there is nothing to do, and the other kernel wants the SMs
         grid_go_on();
-        if (!__syncthreads_or(sees_long(p, threadIdx.x, kThreads))) return;
+        bool any = false;
+        for (int n = threadIdx.x; n < p.N; n += kThreads) any |= long_spans(p, 1, n) > 0;
+        if (!__syncthreads_or(any)) return;
     }
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));

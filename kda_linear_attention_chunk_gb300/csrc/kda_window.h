@@ -94,43 +94,60 @@ __device__ __forceinline__ Sequence sequence_of(const WindowParams &p, int span,
 // head, the warp-MMA kernel the others.
 __device__ __forceinline__ bool is_long(const WindowParams &p, int len) { return p.longer && (int64_t)len * p.G > p.longer; }
 
-// Whether the block's share of the table, every `step`-th from `at` on, has a long one.
-__device__ __forceinline__ bool sees_long(const WindowParams &p, int at, int step)
+// spans of sequence n, if it is a long one
+__device__ __forceinline__ int long_spans(const WindowParams &p, int span, int n)
 {
-    bool any = false;
-    for (int n = at; n < p.N; n += step)
-        any |= is_long(p, clamp_row(p.cu[n + 1], p.T, nullptr) - clamp_row(p.cu[n], p.T, nullptr));
-    return any;
+    const int len = clamp_row(p.cu[n + 1], p.T, nullptr) - clamp_row(p.cu[n], p.T, nullptr);
+    return is_long(p, len) ? (len - 1) / span + 1 : 0;
 }
 
-// The sequence of the number-th span of the long ones alone, by a converged warp that
-// goes through the table; part -1: there are fewer spans.
-__device__ __forceinline__ Sequence sequence_of_long(const WindowParams &p, int span, int number, int lane)
+// The spans of the long sequences are numbered by lanes: first those of the sequences 0, 32,
+// 64 and so on.  A lane's own, and those before:
+struct LongSpans {
+    int mine = 0, before = 0;
+};
+__device__ __forceinline__ LongSpans count_long(const WindowParams &p, int span, int lane)
+{
+    LongSpans s;
+#pragma unroll 4
+    for (int n = lane; n < p.N; n += 32) s.mine += long_spans(p, span, n);
+    int end = s.mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += x;
+    }
+    s.before = end - s.mine;
+    return s;
+}
+
+// the sequence of a number, by a converged warp; part -1: there are fewer spans
+__device__ __forceinline__ Sequence sequence_of_long(const WindowParams &p, int span, int number, int lane, const LongSpans &l)
 {
     Sequence s = {0, 0, 0, 0, -1};
-    int before = 0;                  // spans in what was gone through
-    for (int base = 0; base < p.N; base += 32) {
-        const int at = min(base + lane, p.N - 1);
-        const int cu0 = p.cu[at], cu1 = p.cu[at + 1];
-        const int len = clamp_row(cu1, p.T, nullptr) - clamp_row(cu0, p.T, nullptr);
-        const int mine = base + lane < p.N && is_long(p, len) ? (len - 1) / span + 1 : 0;
-        int end = mine;              // spans up to this lane's
+    const uint32_t whose = __ballot_sync(0xffffffffu, number >= l.before && number < l.before + l.mine);
+    if (!whose) return s;
+    const int first = __ffs(whose) - 1;
+    int left = number - __shfl_sync(0xffffffffu, l.before, first);
+    for (int base = first; base < p.N; base += 32 * 32) {
+        const int n = base + 32 * lane, mine = n < p.N ? long_spans(p, span, n) : 0;
+        int end = mine;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const int x = __shfl_up_sync(0xffffffffu, end, o);
             if (lane >= o) end += x;
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, before + end > number);
+        const uint32_t past = __ballot_sync(0xffffffffu, end > left);
         if (past) {
-            const int who = __ffs(past) - 1;
-            s.cu0 = __shfl_sync(0xffffffffu, cu0, who);
-            s.cu1 = __shfl_sync(0xffffffffu, cu1, who);
-            s.part = number - before - __shfl_sync(0xffffffffu, end - mine, who);
-            s.start = p.starts ? p.starts[base + who] : 0;
-            s.slot = p.slots ? p.slots[base + who] : base + who;
+            const int who = __ffs(past) - 1, at = base + 32 * who;
+            s.part = left - __shfl_sync(0xffffffffu, end - mine, who);
+            s.cu0 = p.cu[at];
+            s.cu1 = p.cu[at + 1];
+            s.start = p.starts ? p.starts[at] : 0;
+            s.slot = p.slots ? p.slots[at] : at;
             return s;
         }
-        before += __shfl_sync(0xffffffffu, end, 31);
+        left -= __shfl_sync(0xffffffffu, end, 31);
     }
     return s;
 }

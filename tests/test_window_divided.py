@@ -110,3 +110,12 @@ def test_same_bytes_every_time_in_a_graph_and_behind_other_calls():
         graph.replay()
         t.cuda.synchronize()
         assert all(t.equal(x, y) for x, y in zip(out, want)) and t.equal(pool, first)
+
+
+def test_long_sequences_anywhere_in_a_large_table():
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 4, 2500)]
+    for n in (0, 31, 32, 1023, 1024, 1055, 1056, 2047, 2400, 2499):
+        lens[n] = int(rng.integers(60, 200))
+    b = Batch([int(x) for x in rng.integers(0, 30, 2500)], 4, 1, 64, window=20, sinks=1, dtype="bf16", seed=8)
+    b.prefill(lens, padded=(1024, 1700), check_rows=[0, 1, 2, 63, 64, 127, 128, 199])
