@@ -29,8 +29,8 @@
 // writes the rows that the cache keeps.
 //
 // On a GB300, 32 query heads on 8 key heads of 128: 8192 rows in the middle of a
-// context, window 4096, 0.39-0.41 ms (1.34-1.41 PFLOP/s); 32,768 rows at once
-// 1.36-1.44 ms; 16 prompts in 8192 rows, window 1024, 84 us.  With long windows the
+// context, window 4096, 0.40-0.43 ms (1.29-1.37 PFLOP/s); 32,768 rows at once
+// 1.41-1.48 ms; 16 prompts in 8192 rows, window 1024, 84-86 us.  With long windows the
 // chain of one query tile bounds it (scores, softmax, P V, the next scores: 2750 cycles
 // a key tile, 2050 of them the tensor core's work for both query tiles); with short
 // ones what an item costs beside its tiles.

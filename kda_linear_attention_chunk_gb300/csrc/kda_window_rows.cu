@@ -20,7 +20,7 @@
 // O) at the end.  In decode the new token's rows are taken from the call's arguments
 // by everyone, so nobody reads the cache row being written.  On a GB300, 64 sequences
 // of 32 query heads on 8 key heads of 128 over a window of 4096: 155 us, the copy
-// bandwidth; 8 drafted tokens of each over a window of 1024: 66 us, bound by a warp's
+// bandwidth; 8 drafted tokens of each over a window of 1024: 67 us, bound by a warp's
 // chain of products and exponentials.
 #include <cooperative_groups.h>
 #include <stdint.h>
