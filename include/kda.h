@@ -455,7 +455,7 @@ int kda_short_conv(const uint16_t *xq, const uint16_t *xk, const uint16_t *xv,
  *  Capture    every call can be captured into a CUDA graph, after any one call of
  *             this library on the device outside of a capture.
  */
-typedef enum { KDA_BF16 = 0, KDA_F16 = 1 } kda_dtype;
+typedef enum { KDA_BF16 = 0, KDA_F16 = 1, KDA_F32 = 2 /* only where a call says so */ } kda_dtype;
 typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
 
 /*
@@ -588,6 +588,157 @@ int kda_slots_copy(const kda_pool *pools, int num_pools, int num_slots, const in
 int kda_slots_compact(const kda_pool *pools, int num_pools, int num_slots, const int32_t *slots,
                       int32_t *new_slots, int N, void *stream);
 
+/*
+ * ---- paged caches, shared prefixes and beams ---------------------------------
+ *
+ * A softmax layer that sees its whole context needs a cache that grows.  It is kept
+ * in pages, and one slot id, the same that addresses the states and ring caches,
+ * selects a row of a page table.  The conventions of the softmax layers above hold
+ * (types, strides, heads, capture), with these additions:
+ *
+ *  Paged cache  kv_pages: [num_pages][2 (k, v)][Hk][page][d], page a power of two
+ *               from 16 to 256; page_table: int32 [num_slots][max_pages], device
+ *               memory.  Position p of a slot is kept in row p mod page of the page
+ *               page_table[slot][p / page].  Who owns which page is the caller's
+ *               affair (-1, or anything, where there is none); max_pages * page must
+ *               fit in 31 bits.  An id outside [0, num_pages) where a call needs a page
+ *               sets bit 128 of the device error word: nothing is written there, and
+ *               what is read from there is zero.
+ *  Rows         row t of sequence n (rows cu_seqlens[n] .. cu_seqlens[n+1] - 1) is at
+ *               position starts[n] + t - cu_seqlens[n].  With cu_seqlens NULL every
+ *               sequence has one row (T must be N).  Rows of no sequence and of padded
+ *               ones (slot -1) are left as they were in every output.
+ *  Tables       slots: int32 [N] or NULL (table row n; num_slots >= N then); an id
+ *               outside [-1, num_slots) is treated like -1 and sets bit 8.  starts: int32
+ *               [N] or NULL (all 0), >= 0 and starts[n] + rows <= max_pages * page;
+ *               otherwise clamped, setting bit 64 (rows that still lie past the table's
+ *               end are not cached).
+ */
+
+/*
+ * kda_paged_append -- kda_head_norm_rope of packed rows on their way into a paged
+ * cache: q is normed and rotated into q_out, k into the sequence's pages, and v is
+ * copied there.  The rotation's positions are those of the cache.
+ *
+ *   q, k, v        16-bit rows of [Hq][d], [Hk][d], [Hk][d] (strides as above).
+ *   q_weight, k_weight, table, max_pos, rotary, layout, norm, eps  as for
+ *                  kda_head_norm_rope (a position from max_pos on takes the table's
+ *                  last row and sets bit 64).
+ *   kv_pages       written in place.  Two rows of a call must not share a place.
+ *   q_out          [T][Hq][d]; may be q itself where q is dense.
+ *   N >= 1, T >= 0.  Other outputs must not overlap an input's span or each other.
+ * Returns a kda_status.
+ */
+int kda_paged_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                     int64_t v_stride, const float *q_weight, const float *k_weight, const float *table,
+                     int max_pos, const int32_t *cu_seqlens, const int32_t *starts, const int32_t *slots,
+                     void *kv_pages, int num_pages, int page, const int32_t *page_table, int num_slots,
+                     int max_pages, void *q_out, int N, int T, int Hq, int Hk, int d, int rotary, int layout,
+                     int norm, float eps, int dtype, void *stream);
+
+/*
+ * kda_paged_attention -- causal softmax attention of packed rows over a paged cache
+ * that holds the rows' own keys and values already (kda_paged_append):
+ *
+ *     out_t[h] = sum_j softmax_j(scale q_t[h] . k_j) v_j   over the positions j <= p_t
+ *
+ * Serves decode steps (cu_seqlens NULL), drafted tokens, and chunks of prompts.
+ * Sequences may share a prefix, kept once: group g, the sequences groups[g] ..
+ * groups[g+1] - 1, finds its positions below prefix_lens[g] in the pages of slot
+ * prefix_slots[g], and those from prefix_lens[g] on in its sequences' own pages (at
+ * their positions, so a page that the prefix ends in is each sequence's own from that
+ * row on; earlier entries of their table rows are not used).  The prefix is read once
+ * for all rows of the group.
+ *
+ *   groups        int32 [P+1], device memory, nondecreasing, within [0, N] (else clamped,
+ *                 setting bit 2; results of overlapping groups are undefined); sequences
+ *                 of no group have no prefix.
+ *   prefix_lens   int32 [P], 0 .. max_pages * page (else clamped, bit 64).
+ *   prefix_slots  int32 [P]; -1: no prefix; an id outside [-1, num_slots) likewise, bit 8.
+ *                 With P = 0 all three are NULL.
+ *   starts        at least the sequence's prefix length (else clamped, bit 64).
+ *   out           [T][Hq][d].
+ *   scale         > 0, at most 1e37.
+ *   workspace     device memory of at least kda_paged_attention_workspace(...) bytes,
+ *                 16-byte aligned, of this call until it has run: calls that may run at
+ *                 the same time, captured ones too, need one each.
+ * A value row that is not finite reaches, besides the rows that see it, rows of the same
+ * sequence or group in the same tile (up to 128 keys by 256 query rows).  Probabilities are
+ * rounded to 16 bits as in kda_window_prefill, sums and joins are fp32; the same call
+ * gives the same bytes.
+ * Returns a kda_status (KDA_ERR_SHAPE where the workspace is too small).
+ */
+int kda_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_seqlens, const int32_t *starts,
+                        const int32_t *slots, const void *kv_pages, int num_pages, int page,
+                        const int32_t *page_table, int num_slots, int max_pages, const int32_t *groups,
+                        const int32_t *prefix_lens, const int32_t *prefix_slots, int P, void *out,
+                        void *workspace, int64_t workspace_bytes, int N, int T, int Hq, int Hk, int d,
+                        float scale, int dtype, void *stream);
+/* The bytes that such a call needs; -1 for sizes that no call may have. */
+int64_t kda_paged_attention_workspace(int N, int T, int P, int Hq, int Hk, int d);
+
+/*
+ * kda_pages_copy -- copies positions between slots in several paged caches at once
+ * (the caches of a stack's layers, which share one page table): positions start[i] ..
+ * end[i] - 1 of slot src[i] to the same positions of slot dst[i].
+ *
+ *   caches      HOST array of num_caches (at most KDA_MAX_POOLS) caches, read before the
+ *               call returns; entry_bytes is a page's, 2 Hk page row_bytes of its own Hk.
+ *               They must not overlap.
+ *   row_bytes   bytes of one row (of a head's key or value), a multiple of 16, at most 1024.
+ *   src, dst    int32 [M], device memory.  -1 in either skips row i; an id outside
+ *               [-1, num_slots) does too and sets bit 8.  No position that the call writes
+ *               may be written or read by another row of it.
+ *   start, end  int32 [M]; start NULL: 0.  0 <= start, end <= max_pages * page (else
+ *               clamped, bit 64); an empty range copies nothing.
+ * Returns a kda_status.
+ */
+int kda_pages_copy(const kda_pool *caches, int num_caches, int num_pages, int page, int row_bytes,
+                   const int32_t *page_table, int num_slots, int max_pages, const int32_t *src,
+                   const int32_t *dst, const int32_t *start, const int32_t *end, int M, void *stream);
+
+/*
+ * kda_beam_select -- one selection step of beam search for G prompts of B beams each.
+ * Beam b of prompt g has the score scores[g][b] (the sum of its tokens' log
+ * probabilities; -inf: no hypothesis) and the logits x of its next token; its
+ * candidates are
+ *
+ *     (b, t) with the score  scores[g][b] + x_t - log sum_u exp(x_u),   0 <= t < V,
+ *
+ * or, where ended[g][b] is not 0, only (b, end_token) with the score unchanged.  The B best
+ * candidates of the prompt become its beams, best first, equal ones by the lowest
+ * b V + t.  A candidate whose score is -inf or NaN is none; beams without a candidate
+ * get parent and token -1 and the score -inf.
+ *
+ *   logits      [G * B][V] rows, `row_stride` elements apart (at least V), KDA_BF16,
+ *               KDA_F16 or KDA_F32.
+ *   scores      fp32 [G][B].
+ *   ended       int32 [G][B] or NULL (none has ended).
+ *   end_token   the token that ends a hypothesis, or -1 (NULL ended and ended_out then).
+ *   scores_out, parents, tokens   [G][B]: fp32, int32 (a beam index in 0 .. B-1), int32.
+ *   ended_out   int32 [G][B]: 1 where the parent had ended or the token is end_token.
+ *   slots       int32 [G][B] or NULL: the slots that hold the beams' states and caches.
+ *               Then new_slots, src and dst, int32 [G][B], say how they follow: a
+ *               parent's first child stays in its slot, its other children (and beams
+ *               without a candidate), in order, take the slots of the beams without a
+ *               child, lowest beam first; new_slots is each new beam's slot, src its
+ *               parent's slot, and dst its slot where it has to be copied there, else -1.
+ *               No target is a source, so (src, dst) are rows for kda_slots_copy and
+ *               kda_pages_copy.  A padded prompt has slots -1.
+ *   workspace   device memory of at least kda_beam_select_workspace(...) bytes, 16-byte
+ *               aligned, of this call until it has run.
+ *   G >= 1; 1 <= B <= 64; 1 <= V <= 2^24; G * B at most 2^20.
+ * Sums are fp32 within a row's part of some thousand tokens and fp64 beyond; candidates are
+ * compared in fp64.  Logits must be aligned to their element (rows need no alignment).
+ * Outputs must not overlap an input or each other.  Returns a kda_status.
+ */
+int kda_beam_select(const void *logits, int64_t row_stride, int dtype, const float *scores, const int32_t *ended,
+                    int end_token, const int32_t *slots, float *scores_out, int32_t *parents, int32_t *tokens,
+                    int32_t *ended_out, int32_t *new_slots, int32_t *src, int32_t *dst, void *workspace,
+                    int64_t workspace_bytes, int G, int B, int V, void *stream);
+/* The bytes that such a call needs; -1 for sizes that no call may have. */
+int64_t kda_beam_select_workspace(int G, int B, int V);
+
 /* Human-readable name of a kda_status value (static string, never NULL). */
 const char *kda_status_string(int status);
 
@@ -601,8 +752,9 @@ const char *kda_status_string(int status);
  * outside [0, W] (clamped).  Bit 32: the tensor-core prefill met a chunk whose
  * decay is outside its fp16 operand range (see "Range" above; use
  * kda_chunk_prefill_fullrange for such inputs).  Bit 64: a position or context
- * length was outside its range (clamped).  0 means no kernel of this library
- * has reported an error.
+ * length was outside its range (clamped).  Bit 128: a page id was outside
+ * [0, num_pages) where a page was needed.  0 means no kernel of this library has
+ * reported an error.
  * Synchronises the current device.  If `reset` is nonzero the word is
  * cleared after reading.  Returns KDA_OK or KDA_ERR_CUDA.
  */

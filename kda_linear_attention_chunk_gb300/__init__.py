@@ -22,7 +22,9 @@ KDA_NOALLOC_MAX_SEQS = 16384
 EXPORTED = ("kda_chunk_prefill", "kda_chunk_prefill_f32", "kda_chunk_prefill_fullrange", "kda_status_string",
             "kda_device_error", "kda_chunk_prefill_noalloc", "kda_chunk_prefill_slots", "kda_chunk_prefill_conv",
             "kda_decode", "kda_fold_commit", "kda_short_conv", "kda_decode_conv", "kda_head_norm_rope",
-            "kda_window_prefill", "kda_window_decode", "kda_slots_copy", "kda_slots_compact")
+            "kda_window_prefill", "kda_window_decode", "kda_slots_copy", "kda_slots_compact", "kda_paged_append",
+            "kda_paged_attention", "kda_paged_attention_workspace", "kda_pages_copy", "kda_beam_select",
+            "kda_beam_select_workspace")
 # device error word bits (kda_device_error)
 ERR_WAIT_TIMEOUT = 1    # a bounded wait ran out; the kernel wound down early
 ERR_BAD_SEQLENS = 2     # a cu_seqlens entry broke its contract (clamped)
@@ -30,8 +32,9 @@ ERR_BAD_SLOT = 8        # a state slot id outside [-1, num_slots)
 ERR_BAD_ACCEPTED = 16   # an accepted count outside [0, window]
 ERR_DECAY_RANGE = 32    # the tensor-core prefill met a decay beyond its fp16 operand range
 ERR_BAD_POSITION = 64   # a position or context length outside its range (clamped)
+ERR_BAD_PAGE = 128      # a page id outside [0, num_pages) where a page was needed
 
-KDA_BF16, KDA_F16 = 0, 1
+KDA_BF16, KDA_F16, KDA_F32 = 0, 1, 2
 KDA_ROPE_HALF, KDA_ROPE_INTERLEAVED = 0, 1
 KDA_MAX_POOLS, KDA_MAX_POOL_SLOTS = 128, 524288
 
@@ -79,8 +82,18 @@ def load(path: str = LIB_PATH):
     lib.kda_window_decode.argtypes = [P, L, P, L, P, L, P, P, P, I, I, P, I, I, I, I, I, I, F, I, P]
     lib.kda_slots_copy.argtypes = [P, I, I, P, P, I, P]
     lib.kda_slots_compact.argtypes = [P, I, I, P, P, I, P]
-    for name in EXPORTED[-5:]:
+    for name in ("kda_head_norm_rope", "kda_window_prefill", "kda_window_decode", "kda_slots_copy", "kda_slots_compact"):
         getattr(lib, name).restype = I
+    lib.kda_paged_append.argtypes = [P, L, P, L, P, L, P, P, P, I, P, P, P, P, I, I, P, I, I, P, I, I, I, I, I, I, I, I, F,
+                                     I, P]
+    lib.kda_paged_attention.argtypes = [P, L, P, P, P, P, I, I, P, I, I, P, P, P, I, P, P, L, I, I, I, I, I, F, I, P]
+    lib.kda_pages_copy.argtypes = [P, I, I, I, I, P, I, I, P, P, P, P, I, P]
+    lib.kda_beam_select.argtypes = [P, L, I, P, P, I, P, P, P, P, P, P, P, P, P, L, I, I, I, P]
+    for name in ("kda_paged_append", "kda_paged_attention", "kda_pages_copy", "kda_beam_select"):
+        getattr(lib, name).restype = I
+    lib.kda_paged_attention_workspace.argtypes = [I, I, I, I, I, I]
+    lib.kda_beam_select_workspace.argtypes = [I, I, I]
+    lib.kda_paged_attention_workspace.restype = lib.kda_beam_select_workspace.restype = L
     lib.kda_status_string.argtypes = [I]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), I]
@@ -205,6 +218,51 @@ def kda_slots_copy(pools, num_pools: int, num_slots: int, src, dst, M: int, stre
 def kda_slots_compact(pools, num_pools: int, num_slots: int, slots, new_slots, N: int, stream) -> int:
     """Raw C-ABI call: moves the live slot entries to the front of every pool."""
     return load().kda_slots_compact(pools, num_pools, num_slots, slots, new_slots, N, stream)
+
+
+def kda_paged_append(q, q_stride: int, k, k_stride: int, v, v_stride: int, q_weight, k_weight, table, max_pos: int,
+                     cu_seqlens, starts, slots, kv_pages, num_pages: int, page: int, page_table, num_slots: int,
+                     max_pages: int, q_out, N: int, T: int, Hq: int, Hk: int, d: int, rotary: int, layout: int, norm: int,
+                     eps: float, dtype: int, stream) -> int:
+    """Raw C-ABI call: norm and rotation of packed rows, k and v on their way into a paged cache."""
+    return load().kda_paged_append(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, table, max_pos, cu_seqlens,
+                                   starts, slots, kv_pages, num_pages, page, page_table, num_slots, max_pages, q_out, N,
+                                   T, Hq, Hk, d, rotary, layout, norm, eps, dtype, stream)
+
+
+def kda_paged_attention(q, q_stride: int, cu_seqlens, starts, slots, kv_pages, num_pages: int, page: int, page_table,
+                        num_slots: int, max_pages: int, groups, prefix_lens, prefix_slots, P: int, out, workspace,
+                        workspace_bytes: int, N: int, T: int, Hq: int, Hk: int, d: int, scale: float, dtype: int,
+                        stream) -> int:
+    """Raw C-ABI call: causal attention of packed rows over a paged cache with shared prefixes."""
+    return load().kda_paged_attention(q, q_stride, cu_seqlens, starts, slots, kv_pages, num_pages, page, page_table,
+                                      num_slots, max_pages, groups, prefix_lens, prefix_slots, P, out, workspace,
+                                      workspace_bytes, N, T, Hq, Hk, d, scale, dtype, stream)
+
+
+def kda_paged_attention_workspace(N: int, T: int, P: int, Hq: int, Hk: int, d: int) -> int:
+    """Raw C-ABI call: the workspace bytes of a kda_paged_attention call, -1 for sizes that none may have."""
+    return load().kda_paged_attention_workspace(N, T, P, Hq, Hk, d)
+
+
+def kda_pages_copy(caches, num_caches: int, num_pages: int, page: int, row_bytes: int, page_table, num_slots: int,
+                   max_pages: int, src, dst, start, end, M: int, stream) -> int:
+    """Raw C-ABI call: copies position ranges between slots in several paged caches; caches is the address of a host
+    array of (base, bytes of a page) pairs of 64-bit integers."""
+    return load().kda_pages_copy(caches, num_caches, num_pages, page, row_bytes, page_table, num_slots, max_pages, src,
+                                 dst, start, end, M, stream)
+
+
+def kda_beam_select(logits, row_stride: int, dtype: int, scores, ended, end_token: int, slots, scores_out, parents, tokens,
+                    ended_out, new_slots, src, dst, workspace, workspace_bytes: int, G: int, B: int, V: int, stream) -> int:
+    """Raw C-ABI call: one selection step of beam search."""
+    return load().kda_beam_select(logits, row_stride, dtype, scores, ended, end_token, slots, scores_out, parents, tokens,
+                                  ended_out, new_slots, src, dst, workspace, workspace_bytes, G, B, V, stream)
+
+
+def kda_beam_select_workspace(G: int, B: int, V: int) -> int:
+    """Raw C-ABI call: the workspace bytes of a kda_beam_select call, -1 for sizes that none may have."""
+    return load().kda_beam_select_workspace(G, B, V)
 
 
 def device_error(reset: bool = False) -> int:
@@ -565,6 +623,18 @@ def _new(shape, dtype, device, stream):
     return out
 
 
+def _scratch(size: int, device, stream):
+    """A workspace of a call on ``stream``: its memory belongs to that stream, so a later call on the stream may get it
+    again, and none on another."""
+    torch = _torch()
+    if stream is None or _handle(stream, device) == _handle(None, device):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    handle = _handle(stream, device)
+    given = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(given):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def _dtype16(t, name: str) -> int:
     torch = _torch()
     if t.dtype is torch.bfloat16:
@@ -794,3 +864,188 @@ def slots_compact(pools, slots, new_slots=None, stream=None):
     if st != KDA_OK:
         raise KdaError(st, "kda_slots_compact")
     return new_slots
+
+
+def _paged(kv_pages, page_table, dtype, Hk, d, at: int):
+    """Checks a paged cache and its page table; returns what the calls pass on of them."""
+    if kv_pages.dim() != 5 or not kv_pages.numel():
+        raise ValueError("kv_pages must be [num_pages][2][Hk][page][d]")
+    num_pages, _, heads, page, _ = kv_pages.shape
+    if page_table.dim() != 2 or not page_table.numel():
+        raise ValueError("page_table must be [num_slots][max_pages]")
+    pages = _dense("kv_pages", kv_pages, (num_pages, 2, heads if Hk is None else Hk, page, d), dtype, at)
+    num_slots, max_pages = shape = page_table.shape
+    return pages, num_pages, page, _dense("page_table", page_table, shape, _torch().int32, at), num_slots, max_pages
+
+
+def _packed(cu_seqlens, starts, slots, T: int, at: int):
+    """Checks the tables of packed rows (or, without cu_seqlens, of a row each); returns N and their addresses."""
+    N = T if cu_seqlens is None else int(cu_seqlens.shape[0]) - 1
+    return (N, 0 if cu_seqlens is None else _table32("cu_seqlens", cu_seqlens, N + 1, at),
+            0 if starts is None else _table32("starts", starts, N, at),
+            0 if slots is None else _table32("slots", slots, N, at))
+
+
+def paged_append(q, k, v, kv_pages, page_table, starts=None, cu_seqlens=None, slots=None, q_weight=None, k_weight=None,
+                 table=None, layout: str = "half", eps: float = 1e-6, norm: bool = True, out=None, stream=None):
+    """head_norm_rope of new rows with k and v on their way into a paged cache, on torch CUDA tensors.
+
+    q: [T][Hq][d], k, v: [T][Hk][d], bfloat16 or float16, d 64 or 128, dense within a row; kv_pages:
+    [num_pages][2][Hk][page][d], updated in place, with page_table: [num_slots][max_pages] int32 (position p of a slot is
+    row p % page of page page_table[slot][p // page]); starts: [N] int32, the position of each sequence's first row, or
+    None (0); cu_seqlens: [N+1] int32, or None (a row for each sequence); slots: [N] int32 (-1 = padded sequence, skipped)
+    or None for table row n; q_weight, k_weight, table (rope_table), layout, eps, norm as for head_norm_rope, the
+    positions being the cache's.  Returns q, dense (rows of padded sequences keep what ``out`` held; ``out`` may be a
+    dense q).
+    """
+    torch = _torch()
+    dtype = q.dtype
+    dt, at = _dtype16(q, "q"), _device_of("q", q)
+    (T, Hq, d), sq = _rows_of_heads("q", q, dtype, at)
+    k_shape, sk = _rows_of_heads("k", k, dtype, at)
+    v_shape, sv = _rows_of_heads("v", v, dtype, at)
+    Hk = k_shape[1]
+    if k_shape != (T, Hk, d) or v_shape != k_shape:
+        raise ValueError("k and v must have q's rows and head size, and the same heads")
+    cache = _paged(kv_pages, page_table, dtype, Hk, d, at)
+    N, cu, first, ids = _packed(cu_seqlens, starts, slots, T, at)
+    qw = kw = tab = rotary = max_pos = 0
+    if q_weight is not None:
+        qw = _dense("q_weight", q_weight, (d,), torch.float32, at)
+    if k_weight is not None:
+        kw = _dense("k_weight", k_weight, (d,), torch.float32, at)
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must be [max_pos][rotary]")
+        max_pos, rotary = shape = table.shape
+        tab = _dense("table", table, shape, torch.float32, at)
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    if out is None:
+        out = _new((T, Hq, d), dtype, q.device, stream)
+    else:
+        _dense("out", out, (T, Hq, d), dtype, at)
+    if not T and cu_seqlens is None:             # no sequence
+        return out
+    st = load().kda_paged_append(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, qw, kw, tab, max_pos, cu, first, ids,
+                                 *cache, out.data_ptr(), N, T, Hq, Hk, d, rotary, ROPE_LAYOUTS[layout], 1 if norm else 0,
+                                 eps, dt, _handle(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_paged_append")
+    return out
+
+
+def paged_attention(q, kv_pages, page_table, starts=None, cu_seqlens=None, slots=None, prefixes=None,
+                    scale: Optional[float] = None, out=None, stream=None):
+    """Causal attention of new rows over a paged cache that holds their keys and values already (paged_append), on torch
+    CUDA tensors.
+
+    q: [T][Hq][d], bfloat16 or float16, d 64 or 128, dense within a row; kv_pages, page_table, starts, cu_seqlens and
+    slots as for paged_append; scale: d^-0.5 by default.  ``prefixes`` (groups [P+1], lengths [P], slots [P], int32 on the
+    device): the sequences groups[g] .. groups[g+1]-1 share their first lengths[g] positions, which are kept (and read)
+    once, in the pages of slots[g] (-1: no prefix); their own pages hold the positions from there on.  Returns out
+    [T][Hq][d] (rows of padded sequences keep what ``out`` held).
+    """
+    dtype = q.dtype
+    dt, at = _dtype16(q, "q"), _device_of("q", q)
+    (T, Hq, d), sq = _rows_of_heads("q", q, dtype, at)
+    cache = _paged(kv_pages, page_table, dtype, None, d, at)
+    Hk = kv_pages.shape[2]
+    N, cu, first, ids = _packed(cu_seqlens, starts, slots, T, at)
+    P = groups = lens = kept = 0
+    if prefixes is not None:
+        P = int(prefixes[1].shape[0])
+        groups = _table32("prefixes[0]", prefixes[0], P + 1, at)
+        lens, kept = _table32("prefixes[1]", prefixes[1], P, at), _table32("prefixes[2]", prefixes[2], P, at)
+        if not P:
+            groups = lens = kept = 0
+    if out is None:
+        out = _new((T, Hq, d), dtype, q.device, stream)
+    else:
+        _dense("out", out, (T, Hq, d), dtype, at)
+    if not T:
+        return out
+    lib = load()
+    size = lib.kda_paged_attention_workspace(N, T, P, Hq, Hk, d)
+    work = _scratch(size, q.device, stream) if size > 0 else None
+    st = lib.kda_paged_attention(q.data_ptr(), sq, cu, first, ids, *cache, groups, lens, kept, P, out.data_ptr(),
+                                 0 if work is None else work.data_ptr(), size, N, T, Hq, Hk, d,
+                                 d ** -0.5 if scale is None else scale, dt, _handle(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_paged_attention")
+    return out
+
+
+def pages_copy(caches, page_table, src, dst, end, start=None, stream=None) -> None:
+    """Copies positions between slots in every paged cache of a list at once (the layers' caches, which share one page
+    table), on torch CUDA tensors: positions start[i] .. end[i]-1 of slot src[i] become those of slot dst[i]; -1 in either
+    skips a row.  caches: [num_pages][2][Hk][page][d] tensors of one num_pages, page, d and element size; page_table:
+    [num_slots][max_pages] int32; src, dst, end: [M] int32 on the device, start: [M] int32 or None (0).  No position that
+    is written may be read or written by another row.  Without rows nothing is done.
+    """
+    array, n, device = _pools(caches)
+    at = device.index
+    like = caches[0]
+    for c in caches:
+        if c.dim() != 5 or c.shape[1] != 2 or c.shape[3:] != like.shape[3:] or c.element_size() != like.element_size():
+            raise ValueError("every cache must be [num_pages][2][Hk][page][d] of the same page, d and element size")
+    if page_table.dim() != 2 or not page_table.numel():
+        raise ValueError("page_table must be [num_slots][max_pages]")
+    num_slots, max_pages = shape = page_table.shape
+    pages = _dense("page_table", page_table, shape, _torch().int32, at)
+    M = int(src.shape[0])
+    ids = _table32("src", src, M, at), _table32("dst", dst, M, at)
+    first = 0 if start is None else _table32("start", start, M, at)
+    last = _table32("end", end, M, at)
+    if not M:
+        return
+    st = load().kda_pages_copy(ctypes.addressof(array), len(caches), n, like.shape[3], like.shape[4] * like.element_size(),
+                               pages, num_slots, max_pages, *ids, first, last, M, _handle(stream, device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_pages_copy")
+
+
+def beam_select(logits, scores, ended=None, end_token: int = -1, slots=None, stream=None):
+    """One selection step of beam search, on torch CUDA tensors.
+
+    logits: [G * B][V] bfloat16, float16 or float32, dense within a row, row g B + b for beam b of prompt g; scores: [G][B]
+    float32, the beams' summed log probabilities (-inf: no hypothesis); ended: [G][B] int32 or None, with end_token: an
+    ended beam stays as it is.  The best B of each prompt's candidates scores + log_softmax(logits), ties by the lowest
+    beam and token.  slots: [G][B] int32 or None, the slots that hold the beams' states and caches.
+
+    Returns (scores [G][B] float32, parents, tokens, ended, new_slots, src, dst), int32 [G][B]: each new beam's parent and
+    token (-1 without a candidate), whether it has ended (None without an end_token), and, with slots, where its slot now
+    is and which copies bring that about (src, dst for slots_copy and pages_copy, flattened; dst -1: none).
+    """
+    torch = _torch()
+    at = _device_of("logits", logits)
+    kinds = {torch.bfloat16: KDA_BF16, torch.float16: KDA_F16, torch.float32: KDA_F32}
+    if logits.dtype not in kinds or logits.dim() != 2 or scores.dim() != 2:
+        raise ValueError("logits must be [G * B][V] bfloat16, float16 or float32, scores [G][B]")
+    rows, V = logits.shape
+    G, B = shape = scores.shape
+    if rows != G * B:
+        raise ValueError("logits must have a row for each score")
+    row, one = logits.stride()
+    if one != 1 and V > 1:
+        raise ValueError("logits must be dense within each row")
+    s = _dense("scores", scores, shape, torch.float32, at)
+    was = 0 if ended is None else _dense("ended", ended, shape, torch.int32, at)
+    ids = 0 if slots is None else _dense("slots", slots, shape, torch.int32, at)
+    device = logits.device
+    lib = load()
+    size = lib.kda_beam_select_workspace(G, B, V)
+    if size <= 0:
+        raise KdaError(KDA_ERR_SHAPE if B <= 64 and V <= 1 << 24 else KDA_ERR_UNSUPPORTED, "kda_beam_select")
+    work = _scratch(size, device, stream)
+    best = _new(shape, torch.float32, device, stream)
+    ints = _new((6, G, B), torch.int32, device, stream).unbind(0)   # one allocation for all
+    parents, tokens, stopped, new_slots, src, dst = ints
+    stops, moves = end_token >= 0, slots is not None
+    st = lib.kda_beam_select(logits.data_ptr(), row if rows > 1 else V, kinds[logits.dtype], s, was, end_token, ids,
+                             best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), stopped.data_ptr() if stops else 0,
+                             *((new_slots.data_ptr(), src.data_ptr(), dst.data_ptr()) if moves else (0, 0, 0)),
+                             work.data_ptr(), size, G, B, V, _handle(stream, device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_beam_select")
+    return (best, parents, tokens, stopped if stops else None) + ((new_slots, src, dst) if moves else (None, None, None))

@@ -6,39 +6,14 @@
 #include <stdint.h>
 
 #include "kda.h"
+#include "kda_checks.h"
 #include "kda_hybrid.h"
 
 namespace {
 
 static_assert(kda::kMaxPools == KDA_MAX_POOLS && kda::kMaxPoolSlots == KDA_MAX_POOL_SLOTS, "the header's limits");
 
-constexpr int64_t kMaxBytes = (int64_t)1 << 40;   // a tensor's span; keeps every product below in 64 bits
-
-struct Span {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Span span(const void *p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (p && bytes > 0 ? (uintptr_t)bytes : 0)}; }
-bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-bool misaligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
-
-// rows of `width` elements, `stride` apart, 2 bytes an element
-int64_t strided_bytes(int T, int64_t stride, int64_t width) { return T > 0 ? ((T - 1) * stride + width) * 2 : 0; }
-
-// row widths and strides: whole 16-byte pieces, rows that do not overlap
-int check_rows(int T, int64_t stride, int64_t width)
-{
-    if (stride < width || stride >= ((int64_t)1 << 31)) return KDA_ERR_SHAPE;
-    if (T > 0 && (int64_t)T * stride * 2 >= kMaxBytes) return KDA_ERR_SHAPE;
-    return stride % 8 ? KDA_ERR_ALIGN : KDA_OK;
-}
-
-int check_heads(int Hq, int Hk, int d, int dtype)
-{
-    if (Hq < 1 || Hk < 1 || Hq > (1 << 16) || Hk > (1 << 16) || d < 1) return KDA_ERR_SHAPE;
-    if ((d != 64 && d != 128) || (dtype != KDA_BF16 && dtype != KDA_F16)) return KDA_ERR_UNSUPPORTED;
-    return KDA_OK;
-}
+using namespace kda::checks;
 
 // what the two attention calls share; rows = T (prefill) or N (decode)
 int check_window(const kda::WindowArgs &a, int rows, int dtype)
@@ -77,34 +52,6 @@ int check_window(const kda::WindowArgs &a, int rows, int dtype)
         if (overlap(out, s) || overlap(pool, s)) return KDA_ERR_ALIAS;
     return overlap(out, pool) ? KDA_ERR_ALIAS : KDA_OK;
 }
-
-int check_pools(const kda_pool *pools, int num_pools, int num_slots, kda::SlotPools *to)
-{
-    if (num_pools < 1 || num_slots < 1) return KDA_ERR_SHAPE;
-    if (num_pools > KDA_MAX_POOLS || num_slots > KDA_MAX_POOL_SLOTS) return KDA_ERR_UNSUPPORTED;
-    for (int i = 0; i < num_pools; i++) {
-        if (!pools[i].base) return KDA_ERR_NULL;
-        if (pools[i].entry_bytes < 1 || pools[i].entry_bytes >= kMaxBytes / num_slots) return KDA_ERR_SHAPE;
-        if (misaligned(pools[i].base, 16) || pools[i].entry_bytes % 16) return KDA_ERR_ALIGN;
-        to->base[i] = pools[i].base;
-        to->entry_bytes[i] = pools[i].entry_bytes;
-        for (int j = 0; j < i; j++)
-            if (overlap(span(to->base[i], to->entry_bytes[i] * num_slots),
-                        span(to->base[j], to->entry_bytes[j] * num_slots)))
-                return KDA_ERR_ALIAS;
-    }
-    to->n = num_pools;
-    return KDA_OK;
-}
-
-bool in_pools(const kda::SlotPools &p, int num_slots, Span s)
-{
-    for (int i = 0; i < p.n; i++)
-        if (overlap(span(p.base[i], p.entry_bytes[i] * num_slots), s)) return true;
-    return false;
-}
-
-int status_of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 }  // namespace
 
@@ -205,7 +152,7 @@ int kda_slots_copy(const kda_pool *pools, int num_pools, int num_slots, const in
     if (!pools || !src || !dst) return KDA_ERR_NULL;
     if (M < 1) return KDA_ERR_SHAPE;
     kda::SlotMoveArgs a;
-    int st = check_pools(pools, num_pools, num_slots, &a.pools);
+    int st = check_pools(pools, num_pools, num_slots, KDA_MAX_POOL_SLOTS, &a.pools);
     if (st != KDA_OK) return st;
     if (misaligned(src, 4) || misaligned(dst, 4)) return KDA_ERR_ALIGN;
     if (in_pools(a.pools, num_slots, span(src, (int64_t)M * 4)) ||
@@ -223,7 +170,7 @@ int kda_slots_compact(const kda_pool *pools, int num_pools, int num_slots, const
     if (!pools || !slots || !new_slots) return KDA_ERR_NULL;
     if (N < 1) return KDA_ERR_SHAPE;
     kda::SlotMoveArgs a;
-    int st = check_pools(pools, num_pools, num_slots, &a.pools);
+    int st = check_pools(pools, num_pools, num_slots, KDA_MAX_POOL_SLOTS, &a.pools);
     if (st != KDA_OK) return st;
     if (misaligned(slots, 4) || misaligned(new_slots, 4)) return KDA_ERR_ALIGN;
     const Span si = span(slots, (int64_t)N * 4), so = span(new_slots, (int64_t)N * 4);
