@@ -4,14 +4,17 @@
 //
 // The best B of a prompt's B V candidates, with one pass over the logits, which bound
 // it by HBM.  Within a row the order of the candidates is that of the logits, so the
-// first kernel needs no normaliser: a CTA holds kSlice logits of one row in registers,
-// and writes their best B and their maximum and sum of exponentials.  The second, one
-// CTA a prompt, joins the sums (fp64), compares what is left of the candidates in fp64,
-// where different beams' may lie close together, and gives the children their slots.
+// first kernel needs no normaliser: a CTA takes a slice of one row, and writes the
+// slice's best B and its maximum and sum of exponentials.  The second, one CTA a prompt,
+// joins the sums, compares what is left of the candidates and gives the children their
+// slots.  Candidates of different beams may lie close together: they are compared as
+// unevaluated sums of two fp32 numbers (the card's fp64 rate, a 64th of fp32's, made this
+// kernel take 23-37 us in fp64).
 //
 // The best B of many values: the values fall into at least B groups by threads; the
 // smallest of the groups' maxima has at least B values at or above it, and mostly few
-// more (B groups of equal size: about B ln B).  Those are collected and ranked by
+// more (B groups of equal size: about B ln B).  Only the threads whose own maximum
+// reaches it look at their values again and collect those that do, and these are ranked by
 // counting.  Where equal or unevenly spread values make them too many, B rounds of a
 // maximum below the one before find the same.  Ties go to the lowest index either way.
 #include <cuda_bf16.h>
@@ -27,8 +30,8 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kEach = 32;                    // logits of a thread
-constexpr int kSlice = kThreads * kEach;
+constexpr int kAtOnce = 4;                   // 16-byte loads of a thread on their way
+constexpr int kLeast = 2048, kLongest = 32768;   // logits of a slice
 constexpr int kMost = 512;                   // candidates that are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -42,22 +45,51 @@ struct BeamParams {
     int32_t *parents, *tokens, *ended_out, *new_slots, *src, *dst;
     uint64_t *best;                  // [G * B][slices][B]: keys, best first, 0 behind the last
     float2 *sums;                    // [G * B][slices]: maximum, sum of exponentials relative to it
-    int G, B, V, slices, spread;     // spread: lanes of a group
+    int G, B, V, slices, slice;      // slice: logits of one, a multiple of kLeast
+    int spread;                      // lanes of a group
 };
 
-// A value and its token as a number that is larger for a better candidate; 0 for none.
+// A number that grows with the value, and back; that of -inf is kNone.
+constexpr uint32_t kNone = 0x007fffffu;
+__device__ __forceinline__ uint32_t rank_of(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.f);         // -0 and 0 are equal
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_at(uint32_t rank)
+{
+    return __uint_as_float(rank & 0x80000000u ? rank & 0x7fffffffu : ~rank);
+}
+
+// A logit and its token as a number that is larger for a better candidate; 0 for none.
 __device__ __forceinline__ uint64_t key_of(float x, int token)
 {
-    if (!(x > -INFINITY)) return 0;
-    const uint32_t b = __float_as_uint(x + 0.f);         // -0 and 0 are equal
-    return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~token;
+    return x > -INFINITY ? (uint64_t)rank_of(x) << 32 | (uint32_t)~token : 0;
 }
-__device__ __forceinline__ float value_of(uint64_t key)
-{
-    const uint32_t b = (uint32_t)(key >> 32);
-    return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-}
+__device__ __forceinline__ float value_of(uint64_t key) { return value_at((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int token_of(uint64_t key) { return (int)~(uint32_t)key; }
+
+// a + b = s + e exactly
+__device__ __forceinline__ float two_sum(float a, float b, float &e)
+{
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t));
+    return s;
+}
+
+// log l of 0 < l < 2^126 as a sum of two numbers, off by some 2^-25: l = 2^k f with f in
+// [2^-1/2, 2^1/2], and f to 48 bits by the logarithm's slope
+__device__ __forceinline__ float2 log_of(double l)
+{
+    const float top = (float)l;
+    const int k = (int)((__float_as_uint(top) - 0x3f3504f3u) >> 23) - (__float_as_uint(top) < 0x3f3504f3u ? 512 : 0);
+    const float unit = __uint_as_float((uint32_t)(127 - k) << 23);
+    const float f = top * unit, rest = (float)(l - (double)top) * unit;
+    const float ln2_hi = 0.693145751953125f, ln2_lo = 1.42860677e-6f;      // k ln2_hi is exact
+    float e;
+    const float s = two_sum(k * ln2_hi, logf(f), e);
+    return make_float2(s, e + fmaf((float)k, ln2_lo, rest / f));
+}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -112,10 +144,9 @@ __device__ __forceinline__ bool extends(const BeamParams &p, int beam)
 template <typename E>
 __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__ BeamParams p)
 {
-    constexpr int kN = Vec<E>::kN, kVecs = kEach / kN;
-    __shared__ uint64_t found[kMost];
+    constexpr int kN = Vec<E>::kN;
+    __shared__ uint64_t found[kMost], best_w[kWarps];
     __shared__ float top_w[kWarps], sum_w[kWarps], low_w[kWarps];
-    __shared__ uint64_t best_w[kWarps];
     __shared__ int count;
     grid_go_on();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -127,31 +158,42 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
     const int before = min(p.V, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(E));
     const int vecs = (p.V - before) / kN, behind = p.V - before - vecs * kN;
     const uint4 *body = reinterpret_cast<const uint4 *>(row + before);
-    const int v0 = slice * (kSlice / kN) + tid;
-    float x[kEach + 1];
-#pragma unroll
-    for (int i = 0; i < kVecs; i++) {
-        const int v = v0 + i * kThreads;
-        if (v < vecs) {
-            Vec<E>::up(__ldcs(body + v), x + i * kN);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kN; j++) x[i * kN + j] = -INFINITY;
-        }
-    }
+    const int first = slice * (p.slice / kN) + tid, end = min(vecs, (slice + 1) * (p.slice / kN));
     // the few others are the first slice's, one to a thread
     int odd = -1;
     if (slice == 0) odd = tid < before ? tid : tid >= 32 && tid - 32 < behind ? before + vecs * kN + tid - 32 : -1;
-    x[kEach] = odd >= 0 ? Vec<E>::one(row[odd]) : -INFINITY;
-    auto token = [&](int i) { return i < kEach ? before + (v0 + i / kN * kThreads) * kN + i % kN : odd; };
+    const float single = odd >= 0 ? Vec<E>::one(row[odd]) : -INFINITY;
 
-    float top = -INFINITY, sum = 0.f;
+    // the thread's maximum (without NaN) and the sum of exponentials relative to it, or to
+    // 0 where nothing is finite; a NaN among the logits makes the sum NaN, and with it the
+    // row's normaliser
+    float top = single, sum = ex2(single > -INFINITY ? 0.f : single);
+    auto take = [&](const uint4 &v) {
+        float x[kN], high;
+        Vec<E>::up(v, x);
+        high = x[0];
 #pragma unroll
-    for (int i = 0; i <= kEach; i++) top = fmaxf(top, x[i]);       // (without NaN)
-    // (a NaN among the logits makes the sum NaN, and with it the row's normaliser)
-    const float base = top > -INFINITY ? top : 0.f;
+        for (int j = 1; j < kN; j++) high = fmaxf(high, x[j]);
+        if (high > top) {
+            if (top > -INFINITY) sum *= ex2((top - high) * kLog2e);
+            top = high;
+        }
+        const float base = top > -INFINITY ? top : 0.f;
+        float part = 0.f;
 #pragma unroll
-    for (int i = 0; i <= kEach; i++) sum += ex2((x[i] - base) * kLog2e);
+        for (int j = 0; j < kN; j++) part += ex2((x[j] - base) * kLog2e);
+        sum += part;
+    };
+    int v = first;
+    for (; v + (kAtOnce - 1) * kThreads < end; v += kAtOnce * kThreads) {
+        uint4 r[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; i++) r[i] = __ldg(body + v + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; i++) take(r[i]);
+    }
+    for (; v < end; v += kThreads) take(__ldg(body + v));
+
     float wide = top;
     for (int o = 1; o < p.spread; o *= 2) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
     float low = wide, high = wide;                       // of the warp's groups
@@ -181,14 +223,23 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
         for (int w = 0; w < kWarps; w++) l += top_w[w] > -INFINITY ? sum_w[w] * ex2((top_w[w] - m) * kLog2e) : sum_w[w];
         p.sums[at] = make_float2(m, l);
     }
-    if (top >= bound && top > -INFINITY) {
+    // every value of the thread's, once more, with its token
+    auto each = [&](auto &&use) {
+        if (odd >= 0) use(single, odd);
+        for (int v = first; v < end; v += kThreads) {
+            float x[kN];
+            Vec<E>::up(__ldg(body + v), x);
 #pragma unroll
-        for (int i = 0; i <= kEach; i++)
-            if (x[i] >= bound && x[i] > -INFINITY) {
+            for (int j = 0; j < kN; j++) use(x[j], before + v * kN + j);
+        }
+    };
+    if (top >= bound && top > -INFINITY)
+        each([&](float x, int token) {
+            if (x >= bound && x > -INFINITY) {
                 const int k = atomicAdd(&count, 1);
-                if (k < kMost) found[k] = key_of(x[i], token(i));
+                if (k < kMost) found[k] = key_of(x, token);
             }
-    }
+        });
     __syncthreads();
     uint64_t *to = p.best + at * p.B;
     const int n = count;
@@ -208,11 +259,10 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
     uint64_t last = ~(uint64_t)0;
     for (int k = 0; k < p.B; k++) {
         uint64_t mine = 0;
-#pragma unroll
-        for (int i = 0; i <= kEach; i++) {
-            const uint64_t key = key_of(x[i], token(i));
+        each([&](float x, int token) {
+            const uint64_t key = key_of(x, token);
             if (key < last && key > mine) mine = key;
-        }
+        });
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) {
             const uint64_t other = __shfl_xor_sync(0xffffffffu, mine, o);
@@ -231,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
 // A candidate of a prompt.  Those of a beam are in the order of their keys, which also tells
 // logits apart that are equal beside the normaliser.
 struct Candidate {
-    double score;
+    uint64_t score;                  // ranks of the score's two parts, 0 for none
     uint64_t key;
     int beam;
 };
@@ -245,8 +295,10 @@ constexpr int kMaxBeams = 64;
 
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ BeamParams p)
 {
-    __shared__ double lse[kMaxBeams], score[kMaxBeams], low_w[kWarps];
     __shared__ Candidate found[kMost], best_w[kWarps], best[kMaxBeams];
+    __shared__ float2 lse[kMaxBeams];
+    __shared__ float score[kMaxBeams];
+    __shared__ uint32_t low_w[kWarps];
     __shared__ int kind[kMaxBeams];                      // 0 no hypothesis, 1 extends, 2 ended
     __shared__ int parent[kMaxBeams], slot[kMaxBeams];
     __shared__ int count;
@@ -270,41 +322,54 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         double l = 0.0;
         for (int s = lane; s < p.slices; s += 32) {
             const float2 v = __ldcg(&sums[s]);
-            l += v.x > -INFINITY ? (double)v.y * exp((double)v.x - (double)m) : (double)v.y;
+            l += v.x > -INFINITY ? v.y * expf(v.x - m) : v.y;
         }
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) lse[b] = (double)m + log(l);
+        if (lane == 0) {
+            const float2 y = log_of(l);
+            float e;
+            const float s = two_sum(m, y.x, e);
+            lse[b] = make_float2(s, e + y.y);            // not finite where m or l is not
+        }
     }
     __syncthreads();
     const int per = p.slices * B, all = B * per;         // places of a beam's candidates
-    // the candidate at place e; score -inf: none
+    // the candidate at place e
     auto candidate = [&](int e) {
         const int b = e / per, at = e - b * per;
-        Candidate c = {-INFINITY, 0, b};
+        Candidate c = {0, 0, b};
+        float high = -INFINITY, low = 0.f;
         if (kind[b] == 2 && at == 0) {
-            c.score = score[b];
+            high = score[b];
             c.key = key_of(0.f, p.end_token);
         } else if (kind[b] == 1) {
             c.key = __ldcg(p.best + (int64_t)(first + b) * per + at);
-            const double v = c.key ? score[b] + ((double)value_of(c.key) - lse[b]) : -INFINITY;
-            if (v > -INFINITY) c.score = v;              // (not NaN)
+            if (c.key) {
+                float e1, e2;
+                const float2 n = lse[b];
+                const float sum = two_sum(two_sum(score[b], value_of(c.key), e1), -n.x, e2), rest = e1 + (e2 - n.y);
+                high = sum + rest;                       // (NaN where the normaliser is)
+                low = rest - (high - sum);
+                if (isinf(sum)) high = sum, low = 0.f;
+                if (n.x != n.x || isinf(n.x)) high = -INFINITY;
+            }
         }
+        if (high > -INFINITY) c.score = (uint64_t)rank_of(high) << 32 | rank_of(low);   // (not NaN)
         return c;
     };
-    double top = -INFINITY;
-    for (int e = tid; e < all; e += kThreads) top = fmax(top, candidate(e).score);
-    for (int o = 1; o < p.spread; o *= 2) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) top = fmin(top, __shfl_xor_sync(0xffffffffu, top, o));
+    uint32_t top = 0;
+    for (int e = tid; e < all; e += kThreads) top = max(top, (uint32_t)(candidate(e).score >> 32));
+    for (int o = 1; o < p.spread; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = __reduce_min_sync(0xffffffffu, top);
     if (lane == 0) low_w[warp] = top;
     __syncthreads();
-    double bound = low_w[0];
+    uint32_t bound = low_w[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; w++) bound = fmin(bound, low_w[w]);
+    for (int w = 1; w < kWarps; w++) bound = min(bound, low_w[w]);
     for (int e = tid; e < all; e += kThreads) {
         const Candidate c = candidate(e);
-        if (c.score >= bound && c.score > -INFINITY) {
+        if (c.score && (uint32_t)(c.score >> 32) >= bound) {
             const int k = atomicAdd(&count, 1);
             if (k < kMost) found[k] = c;
         }
@@ -314,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     if (n <= kMost) {
         for (int i = tid; i < max(n, B); i += kThreads) {
             if (i >= n) {
-                best[i] = {-INFINITY, 0, 0};
+                best[i] = {0, 0, 0};
                 continue;
             }
             const Candidate mine = found[i];
@@ -323,12 +388,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
             if (rank < B) best[rank] = mine;
         }
     } else {
-        Candidate last = {INFINITY, 0, -1};
+        Candidate last = {~(uint64_t)0, 0, -1};
         for (int k = 0; k < B; k++) {
-            Candidate mine = {-INFINITY, 0, B};
+            Candidate mine = {0, 0, B};
             for (int e = tid; e < all; e += kThreads) {
                 const Candidate c = candidate(e);
-                if (c.score > -INFINITY && better(last, c) && better(c, mine)) mine = c;
+                if (c.score && better(last, c) && better(c, mine)) mine = c;
             }
 #pragma unroll
             for (int o = 16; o > 0; o /= 2) {
@@ -347,52 +412,64 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    const bool live = tid < B && best[tid < B ? tid : 0].score > -INFINITY;
-    if (tid < B) {
+    if (tid >= kMaxBeams) return;                        // the first two warps stay
+    const bool mine = tid < B, live = mine && best[tid].score;
+    if (mine) {
         const Candidate c = best[tid];
         const int from = live ? c.beam : -1, token = live ? token_of(c.key) : -1;
         parent[tid] = from;
-        p.scores_out[first + tid] = (float)c.score;
+        p.scores_out[first + tid] = live ? value_at((uint32_t)(c.score >> 32)) : -INFINITY;
         p.parents[first + tid] = from;
         p.tokens[first + tid] = token;
         if (p.ended_out) p.ended_out[first + tid] = live && (kind[from] == 2 || token == p.end_token);
     }
     if (!p.slots) return;
-    __syncthreads();
-    if (tid >= B) return;
-    // the n-th child that moves takes the slot of the n-th beam without a child
-    auto moves = [&](int k) {
-        if (parent[k] < 0) return true;
-        for (int j = 0; j < k; j++)
-            if (parent[j] == parent[k]) return true;
-        return false;
-    };
-    int to = live ? slot[parent[tid]] : -1;
-    const int from = to;
-    const bool moving = moves(tid);
-    if (moving) {
-        int nth = 0, b = 0;
-        for (int j = 0; j < tid; j++) nth += moves(j);
-        for (;; b++) {
-            bool childless = true;
-            for (int j = 0; j < B; j++) childless = childless && parent[j] != b;
-            if (childless && nth-- == 0) break;
-        }
-        to = slot[b];
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    // bit b: beam b has a child; bit k: child k moves
+    uint64_t parents = 0;
+    bool moving = mine && !live;
+    for (int j = 0; j < B; j++) {
+        const int from = parent[j];
+        if (from >= 0) parents |= (uint64_t)1 << from;
+        moving = moving || (mine && j < tid && from == parent[tid]);
+    }
+    __shared__ uint32_t moves[2];
+    const uint32_t vote = __ballot_sync(0xffffffffu, moving);
+    if (lane == 0) moves[warp] = vote;
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (!mine) return;
+    const int from = live ? slot[parent[tid]] : -1;
+    int to = from;
+    if (moving) {                                        // the n-th of them: the n-th beam without a child
+        const uint64_t before = (((uint64_t)moves[1] << 32 | moves[0])) & (((uint64_t)1 << tid) - 1);
+        uint64_t free_beams = ~parents;
+        for (int k = __popcll(before); k > 0; k--) free_beams &= free_beams - 1;
+        to = slot[__ffsll(free_beams) - 1];
     }
     p.new_slots[first + tid] = to;
     p.src[first + tid] = from;
     p.dst[first + tid] = moving && live ? to : -1;
 }
 
-int slices_of(int V) { return V <= kSlice ? 1 : (V + kSlice - 1) / kSlice; }
+// Logits of a slice: enough slices to fill the card four times over where the rows are few,
+// and no slice longer than kLongest.
+int slice_of(int rows, int V)
+{
+    const int64_t want = ((int64_t)rows * V / 608 + kLeast - 1) / kLeast * kLeast;
+    return (int)(want < kLeast ? kLeast : want > kLongest ? kLongest : want);
+}
+int slices_of(int rows, int V)
+{
+    const int slice = slice_of(rows, V);
+    return V <= slice ? 1 : (V + slice - 1) / slice;
+}
 
 }  // namespace
 
 int64_t beam_workspace(int G, int B, int V)
 {
     if (G < 1 || B < 1 || B > kMaxBeams || V < 1 || V > (1 << 24) || (int64_t)G * B > (1 << 20)) return -1;
-    const int64_t parts = (int64_t)G * B * slices_of(V);
+    const int64_t parts = (int64_t)G * B * slices_of(G * B, V);
     return parts > 0x7fffffff ? -1 : parts * (B + 1) * 8;
 }
 
@@ -403,7 +480,9 @@ cudaError_t launch_beam_select(const BeamArgs &a)
     p.scores = a.scores; p.ended = a.ended; p.slots = a.slots; p.end_token = a.end_token;
     p.scores_out = a.scores_out; p.parents = a.parents; p.tokens = a.tokens; p.ended_out = a.ended_out;
     p.new_slots = a.new_slots; p.src = a.src; p.dst = a.dst;
-    p.G = a.G; p.B = a.B; p.V = a.V; p.slices = slices_of(a.V);
+    p.G = a.G; p.B = a.B; p.V = a.V;
+    p.slice = slice_of(a.G * a.B, a.V);
+    p.slices = slices_of(a.G * a.B, a.V);
     int groups = kWarps;                                 // at least B
     while (groups < a.B) groups *= 2;
     p.spread = kThreads / groups;

@@ -1,9 +1,9 @@
 """Beam selection: parents, tokens and slots equal to a plain 64-bit form's, scores within the bound of their sums.
 
-Bound of a score (fp64 sums aside): the kernel's exponentials are off by at most 2^-22 relative (2 ulp of exp2 and the
-rounding of its argument x log2 e, whose error of 2^-24 |x| exp(x) stays below 2^-24), each part's fp32 sum over at most
-33 + 8 + 8 additions by 49 2^-24: together below 2^-18 of a sum of one sign, which is the error of its logarithm;
-and half a last place of the result."""
+Bound of a score: the kernel's exponentials are off by at most 2^-22 relative (2 ulp of exp2 and the rounding of its argument
+x log2 e, whose error of 2^-24 |x| exp(x) stays below 2^-24), each part's fp32 sum by 2^-24 for each addition on a term's
+way, at most 8 + 17 in a thread of 128 logits and 5 + 8 over the CTA, the factors on the way (where a maximum moves) likewise:
+together below 2^-18 of a sum of one sign, which is the error of its logarithm; and half a last place of the result."""
 import math
 import random
 
