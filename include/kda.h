@@ -600,8 +600,8 @@ int kda_slots_compact(const kda_pool *pools, int num_pools, int num_slots, const
  *               from 16 to 256; page_table: int32 [num_slots][max_pages], device
  *               memory.  Position p of a slot is kept in row p mod page of the page
  *               page_table[slot][p / page].  Who owns which page is the caller's
- *               affair (-1, or anything, where there is none); max_pages * page must
- *               fit in 31 bits.  An id outside [0, num_pages) where a call needs a page
+ *               affair (-1, or anything, where there is none); max_pages * page at
+ *               most 2^30.  An id outside [0, num_pages) where a call needs a page
  *               sets bit 128 of the device error word: nothing is written there, and
  *               what is read from there is zero.
  *  Rows         row t of sequence n (rows cu_seqlens[n] .. cu_seqlens[n+1] - 1) is at
@@ -612,7 +612,7 @@ int kda_slots_compact(const kda_pool *pools, int num_pools, int num_slots, const
  *               outside [-1, num_slots) is treated like -1 and sets bit 8.  starts: int32
  *               [N] or NULL (all 0), >= 0 and starts[n] + rows <= max_pages * page;
  *               otherwise clamped, setting bit 64 (rows that still lie past the table's
- *               end are not cached).
+ *               end are neither cached nor answered).
  */
 
 /*

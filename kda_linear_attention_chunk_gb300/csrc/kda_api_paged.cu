@@ -17,7 +17,7 @@ int check_table(int num_pages, int page, int num_slots, int max_pages, int *log2
 {
     if (num_pages < 1 || page < 1 || num_slots < 1 || max_pages < 1) return KDA_ERR_SHAPE;
     if (page < 16 || page > 256 || (page & (page - 1))) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)max_pages * page > 0x7fffffff) return KDA_ERR_SHAPE;
+    if ((int64_t)max_pages * page > (1 << 30)) return KDA_ERR_SHAPE;   // so that a tile behind any position fits in 32 bits
     if ((double)num_slots * max_pages * 4 >= (double)kMaxBytes) return KDA_ERR_SHAPE;
     for (*log2 = 4; 1 << *log2 < page;) ++*log2;
     return KDA_OK;

@@ -10,7 +10,7 @@
 
 namespace kda {
 
-// positions that a table row has pages for (at most 2^31 - 1)
+// positions that a table row has pages for (at most 2^30)
 __device__ __forceinline__ int capacity(const PagedCache &c) { return c.max_pages << c.page_log2; }
 
 // The page of position pos of a table row, -1 if there is none (an id out of range, or a

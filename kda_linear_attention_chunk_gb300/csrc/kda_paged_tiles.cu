@@ -1,0 +1,697 @@
+// kda_paged_tiles.cu -- attention over a paged cache for parts of many query rows (a
+// group's prefix, chunks of prompts, drafts), on the tensor cores.
+//
+// A tile of 128 query rows is the G query heads that share a key head for floor(128 / G)
+// consecutive rows of the part; a span is two of them.  Per key tile of 128 positions (whole
+// pages, or half of one) and query tile, with S, P and O in TMEM:
+//
+//     S = Q K^T            (tcgen05.mma, both operands in shared memory)
+//     P = 2^(c S - c m)    one thread per query row: 128 scores in registers
+//     O += P V             (P from TMEM in place of S, V MN-major as loaded)
+//
+// The two query tiles take turns on the tensor core: while one's scores are exponentiated,
+// the other's products run.  The maximum m only follows the true one when it falls behind by
+// more than 2^8, so O is rarely rescaled, and the threads that own the rows do it.
+//
+// One CTA an SM takes an equal share of the line of all tiles, so a long prefix is spread
+// over the card and short parts share a CTA; what it computes of a span whose keys it
+// does not have to itself goes to the workspace in fp32.  A page is one or several TMA boxes;
+// pages without visible positions are boxes outside the tensor, which read as zeros
+// without a trip to memory.
+//
+// Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 the items and loads (a
+// ring of four key and value tiles), warps 9 and 11 the MMAs of the two query tiles, warp 10
+// the zeros in place of values that no row sees.
+#include <stdint.h>
+
+#include "kda_paged_attend.cuh"
+#include "kda_sm100.cuh"
+#include "kda_tiles.cuh"
+
+// Poll limit of the softmax's wait for scores.  A test build of the library sets it to
+// zero: the wait then gives up at once although its MMAs complete, which takes every
+// CTA through the wind-down.
+#ifndef KDA_WAIT_LIMIT_PAGED
+#define KDA_WAIT_LIMIT_PAGED (1u << 18)
+#endif
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+using namespace tiles;
+
+constexpr int kThreads = 384;
+constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
+constexpr int kBars = 3 * kStages + 22;
+constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
+// Registers: a softmax thread holds a row of 128 scores.  The block starts with
+// kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
+// 384 x 168 (the launch checks that the kernel was built with that number).
+constexpr int kRegs = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegs, "more registers than the block has");
+constexpr float kLag = 8.f;          // log2 of what the running maximum may lag behind
+
+// One item of work: a span's rows, one key head, some of the span's key tiles.
+struct Item {
+    int tokens;                      // rows of the span; 0: there are no more items
+    int t0, first;                   // its first row and that row's position
+    int hk, shared;
+    int tile0, tiles;                // key tiles
+    int key0, end;                   // visible positions: key0 .. end - 1, and up to the row's own (not shared)
+    int where;                       // goes_to(), and the first row of a cut piece
+    int64_t cut;
+};
+
+struct Ctl {
+    Item items[2];
+    int abort;
+    uint32_t tmem;
+    uint64_t bars[kBars];
+};
+
+// TMEM columns
+constexpr int kTmS = 0, kTmO = 256;
+
+template <typename E, int D> struct Layout {
+    static constexpr int kTile = 128 * D * 2;            // bytes of a query, key or value tile
+    static constexpr int kHalf = 128 * 128;              // bytes of its 64 leftmost columns
+    static constexpr int kOut = (2 + kStages) * kTile, kCtl = kOut + 8 * kStage;
+    static constexpr int kSmem = 1024 + kCtl + sizeof(Ctl);
+    static_assert(kSmem <= 227 * 1024, "more shared memory than a CTA has");
+    static constexpr bool kF16 = !__is_same(E, __nv_bfloat16);
+};
+
+// The barriers; q is a query tile, s a stage of the key / value ring, i a place of
+// the item ring.
+struct Bars {
+    uint32_t at;
+    __device__ uint32_t full(int s) const { return at + 8 * s; }                    // tile loaded
+    __device__ uint32_t empty(int s) const { return at + 8 * (kStages + s); }       // tile consumed by both products
+    __device__ uint32_t values(int s) const { return at + 8 * (2 * kStages + s); }  // value tile without garbage
+    __device__ uint32_t q_full(int q) const { return at + 8 * (3 * kStages + q); }
+    __device__ uint32_t q_empty(int q) const { return at + 8 * (3 * kStages + 2 + q); }
+    __device__ uint32_t s_full(int q) const { return at + 8 * (3 * kStages + 4 + q); }    // scores in TMEM
+    __device__ uint32_t p_half(int q) const { return at + 8 * (3 * kStages + 6 + q); }    // probabilities of 64 keys
+    __device__ uint32_t p_ready(int q) const { return at + 8 * (3 * kStages + 8 + q); }   // of all
+    __device__ uint32_t o_done(int q) const { return at + 8 * (3 * kStages + 10 + q); }   // O complete
+    __device__ uint32_t o_free(int q) const { return at + 8 * (3 * kStages + 12 + q); }   // O read
+    __device__ uint32_t turn(int q) const { return at + 8 * (3 * kStages + 14 + q); }
+    __device__ uint32_t drained(int q) const { return at + 8 * (3 * kStages + 16 + q); }
+    __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kStages + 18 + i); }
+    __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kStages + 20 + i); }
+};
+constexpr int kItemReaders = 8 + 2 + 1;   // softmax warps, product warps, patch warp
+
+struct Maps {
+    CUtensorMap q, pages;
+};
+
+// What every role knows.
+struct Ctx {
+    const AttendParams &p;
+    Ctl &c;
+    Bars bars;
+    uint8_t *smem;                   // 1024-byte aligned
+    uint32_t base;                   // its shared-memory address
+    uint32_t tmem;
+    int lane;
+    volatile int *abort;
+    __device__ void give_up() const
+    {
+        atomicOr(p.err, kErrWaitTimeout);
+        *abort = 1;
+    }
+    // A wait of the whole warp, the same answer in every lane: lanes poll and see the abort
+    // flag one by one, and one that ran on without the others would meet no partner at
+    // the next instruction of the whole warp.
+    __device__ bool wait(uint32_t bar, int phase, uint32_t limit = 1u << 18) const
+    {
+        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, limit)) != 0;
+    }
+};
+
+// columns of key tile i of an item that may hold visible keys, a multiple of 16
+__device__ __forceinline__ int tile_keys(int end, int tile) { return min(kTileKeys, (end - tile * kTileKeys + 15) & ~15); }
+
+// An item's query tile q: its rows of the batch, the last one's position, and how many of the
+// item's key tiles any of them sees (the first ones).
+struct Span {
+    int first, tokens, last, seen;
+    __device__ Span(const Item &item, int tile_tokens, int q)
+    {
+        tokens = max(0, q ? item.tokens - tile_tokens : min(item.tokens, tile_tokens));
+        first = item.first + q * tile_tokens;
+        last = first + tokens - 1;
+        const int end = item.shared ? item.end : min(item.end, last + 1);
+        seen = tokens ? min(item.tiles, max(0, (int)(((int64_t)end + kTileKeys - 1) / kTileKeys) - item.tile0)) : 0;
+    }
+};
+
+// ---- items and loads ---------------------------------------------------------
+template <typename E, int D>
+__device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
+{
+    using L = Layout<E, D>;
+    const AttendParams &p = x.p;
+    const PagedCache &cache = p.cache;
+    const uint32_t sq = x.base, skv = x.base + 2 * L::kTile;
+    const int parts = p.P + p.N, span = 2 * p.tile_tokens, page = 1 << cache.page_log2;
+    const int box = min(page, kTileKeys), outside = cache.num_pages * 2 * p.Hk;
+    const int64_t total = __ldcg(p.tiles + parts), share = share_of(total, p.Hk, p.tile_workers, kLeastTiles);
+    const int64_t from = blockIdx.x * share, to = min(total * p.Hk, from + share);
+    int64_t at = from;
+    int it = 0, item = 0, qs[2] = {0, 0};                // tiles and query tiles loaded, items written
+    bool ok = true;
+    for (;; item++) {
+        Item &now = x.c.items[item & 1];
+        if (item >= 2) ok = x.wait(x.bars.item_empty(item & 1), item / 2 - 1);
+        if (!ok) break;
+        if (at >= to) {
+            if (x.lane == 0) {
+                now.tokens = 0;
+                mbar_arrive(x.bars.item_full(item & 1));
+            }
+            break;
+        }
+        // the part, span and key head of this place in the line
+        const int hk = (int)(at / total), part = part_at(p.tiles, parts, at - hk * total, x.lane);
+        const bool shared = part < p.P;
+        const Part y = load_part(p.parts + part);
+        int64_t begin = hk * total + __ldcg(p.tiles + part);
+        const int j = span_at(y, shared, span, at - begin, x.lane);
+        begin += tiles_before(y, shared, span, j);
+        const int64_t stop = begin + span_tiles(y, shared, span, j);
+        const int tile0 = first_tile(y) + (int)(at - begin), n = (int)(min(stop, to) - at);
+        const int t0 = y.t0 + j * span, end = span_end(y, shared, span, j);
+        at += n;
+        if (x.lane == 0) {
+            now.tokens = min(span, y.tokens - j * span);
+            now.t0 = t0;
+            now.first = shared ? 0 : y.first + j * span;
+            now.hk = hk;
+            now.shared = shared;
+            now.tile0 = tile0;
+            now.tiles = n;
+            now.key0 = y.key0;
+            now.end = end;
+            now.where = goes_to(y, shared, begin, stop, from, to);
+            now.cut = cut_piece(blockIdx.x, begin, from) * kPieceRows;
+            mbar_arrive(x.bars.item_full(item & 1));
+        }
+        __syncwarp();
+        const int seen[2] = {Span(now, p.tile_tokens, 0).seen, Span(now, p.tile_tokens, 1).seen};
+        const int32_t *table = cache.table + (int64_t)y.entry * cache.max_pages;
+        int ids_from = 0, ids = 0;                       // 32 entries of the page table, a lane each
+        bool have_ids = false, queries = false;
+#pragma unroll 1
+        for (int i = 0; i < n && ok; i++) {
+            const int pos = (tile0 + i) * kTileKeys, boxes = (tile_keys(end, tile0 + i) + box - 1) / box;
+            const int j0 = pos >> cache.page_log2, j1 = (pos + (boxes - 1) * box) >> cache.page_log2;
+            if (!have_ids || j1 >= ids_from + 32) {
+                have_ids = true;
+                ids_from = j0;
+                ids = j0 + x.lane < cache.max_pages ? __ldg(table + j0 + x.lane) : -1;
+            }
+#pragma unroll 1
+            for (int kv = 0; kv < 2; kv++) {
+                const int s = it % kStages;
+                if (it >= kStages) ok = x.wait(x.bars.empty(s), it / kStages - 1);
+                if (!ok) break;
+                const uint32_t bar = x.bars.full(s), dst = skv + s * L::kTile;
+                if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * (D / 64)));
+                __syncwarp();
+#pragma unroll 1
+                for (int b = 0; b < boxes; b++) {
+                    const int at_b = pos + b * box;
+                    const int id = __shfl_sync(0xffffffffu, ids, (at_b >> cache.page_log2) - ids_from);
+                    const bool there = id >= 0 && id < cache.num_pages, needed = at_b + box > y.key0;
+                    if (elect_one()) {
+                        if (needed && !there && kv == 0) atomicOr(p.err, kErrBadPage);
+                        const int c2 = needed && there ? (id * 2 + kv) * p.Hk + hk : outside;
+#pragma unroll 1
+                        for (int h = 0; h < D / 64; h++)
+                            tma_load_3d(dst + h * L::kHalf + b * box * 128, &maps.pages, 64 * h, at_b & (page - 1), c2, bar);
+                    }
+                    __syncwarp();
+                }
+                it++;
+                if (queries) continue;
+                queries = true;                          // after the first keys, which need not wait for their room
+#pragma unroll 1
+                for (int q = 0; q < 2 && ok; q++) {
+                    if (!seen[q]) continue;
+                    if (qs[q]) ok = x.wait(x.bars.q_empty(q), qs[q] - 1);
+                    if (ok && elect_one()) {
+                        // half a query tile is G tile_tokens rows of 128 bytes
+                        mbar_arrive_expect_tx(x.bars.q_full(q), (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64)));
+#pragma unroll
+                        for (int h = 0; h < D / 64; h++)
+                            tma_load_3d(sq + q * L::kTile + h * L::kHalf, &maps.q, 64 * h, hk * p.G,
+                                        t0 + q * p.tile_tokens, x.bars.q_full(q));
+                    }
+                    __syncwarp();
+                    if (ok) qs[q]++;
+                }
+            }
+        }
+        if (!ok) break;
+    }
+    if (!ok && x.lane == 0) x.give_up();
+    // nothing may still be on its way into shared memory when the CTA ends
+#pragma unroll 1
+    for (int q = 0; q < 2; q++)
+        if (qs[q]) mbar_wait_drain(x.bars.q_full(q), (qs[q] - 1) & 1);
+#pragma unroll 1
+    for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(x.bars.full(i % kStages), (i / kStages) & 1);
+}
+
+// ---- products of one query tile ---------------------------------------------------
+// The whole warp walks the loop and one elected lane issues: operands that are
+// uniform over the warp stay in uniform registers, where the instruction takes them.
+// The two query tiles take turns, so that one's scores are exponentiated during the
+// other's products.
+template <typename E, int D>
+__device__ __forceinline__ void product_role(const Ctx &x, int which)
+{
+    using L = Layout<E, D>;
+    const AttendParams &p = x.p;
+    const int q = __shfl_sync(0xffffffffu, which, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
+    const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q;
+    const uint32_t qs = x.base + q * L::kTile, skv = x.base + 2 * L::kTile;
+    int it = 0, parts = 0, turns = 0, mine = 0;          // tiles consumed; products P V issued; turns taken; items with rows
+    bool ok = true;
+    for (int item = 0; ok; item++) {
+        const Item &now = x.c.items[item & 1];
+        ok = x.wait(x.bars.item_full(item & 1), item / 2);
+        const int tokens = __shfl_sync(0xffffffffu, now.tokens, 0);
+        if (!ok || tokens == 0) break;
+        const int seen = __shfl_sync(0xffffffffu, Span(now, p.tile_tokens, q).seen, 0);
+        const int n = __shfl_sync(0xffffffffu, now.tiles, 0), tile0 = __shfl_sync(0xffffffffu, now.tile0, 0);
+        const int end = __shfl_sync(0xffffffffu, now.end, 0);
+        const bool both = tokens > p.tile_tokens, any = seen > 0;
+        int keys = tile_keys(end, tile0);
+        ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), mine));
+        if (elect_one()) {
+            if (ok && any) {
+                mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc(keys, 0, L::kF16));
+                mma_commit(x.bars.s_full(q));
+            }
+            mma_commit(x.bars.empty(it % kStages));
+        }
+        __syncwarp();
+        it++;
+        for (int i = 0; i < n && ok; i++) {
+            const int sv = it % kStages, steps = keys / 16;       // this tile's values
+            ok = x.wait(x.bars.values(sv), it / kStages);
+            it++;
+            const int sk = it % kStages;                 // the next tile's keys
+            const bool have = i + 1 < n;
+            if (have) {
+                keys = tile_keys(end, tile0 + i + 1);
+                ok = ok && x.wait(x.bars.full(sk), it / kStages);
+                it++;
+            } else if (any && elect_one()) {
+                mma_commit(x.bars.q_empty(q));           // every product with the query tile is issued
+            }
+            __syncwarp();
+            if (both && ok && (q || turns)) ok = x.wait(x.bars.turn(q), q ? turns : turns - 1);
+            if (ok && i < seen) {
+                if (i == 0 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
+                ok = ok && x.wait(x.bars.p_half(q), parts);
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 0, steps, i > 0);
+                    ok = x.wait(x.bars.p_ready(q), parts);
+                }
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 4, steps, true);
+                    parts++;
+                }
+            }
+            if (elect_one()) {
+                if (ok && have && i + 1 < seen) {
+                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc(keys, 0, L::kF16));
+                    mma_commit(x.bars.s_full(q));
+                }
+                if (both) mbar_arrive(x.bars.turn(!q));
+                mma_commit(x.bars.empty(sv));
+                if (have) mma_commit(x.bars.empty(sk));
+                else if (any) mma_commit(x.bars.o_done(q));
+            }
+            __syncwarp();
+            if (both) turns++;
+        }
+        if (any) mine++;
+        __syncwarp();
+        if (x.lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
+    }
+    if (!ok && x.lane == 0) x.give_up();
+    // every product is finished before the TMEM and shared memory go
+    if (elect_one()) mma_commit(x.bars.drained(q));
+    mbar_wait_drain(x.bars.drained(q), 0);
+}
+
+// ---- zeros in place of values that no row sees ----------------------------------------
+// Value rows before the first key and behind the last hold anything, and 0 x NaN is NaN.
+// Every value tile passes through here.
+template <typename E, int D>
+__device__ __forceinline__ void patch_role(const Ctx &x)
+{
+    using L = Layout<E, D>;
+    bool ok = true;
+    for (int item = 0, it = 1; ok; item++) {
+        const Item &now = x.c.items[item & 1];
+        ok = x.wait(x.bars.item_full(item & 1), item / 2);
+        if (!ok || now.tokens == 0) break;
+        const int n = now.tiles;
+        for (int i = 0; i < n && ok; i++, it += 2) {
+            const int s = it % kStages;
+            ok = x.wait(x.bars.full(s), it / kStages);
+            if (!ok) break;
+            const int pos = (now.tile0 + i) * kTileKeys, keys = tile_keys(now.end, now.tile0 + i);
+            if (pos < now.key0 || pos + keys > now.end) {
+#pragma unroll 1
+                for (int e = x.lane; e < keys * (D / 8); e += 32) {
+                    const int r = e / (D / 8), v = e % (D / 8);
+                    if (pos + r < now.key0 || pos + r >= now.end)
+                        *reinterpret_cast<uint4 *>(x.smem + (2 + s) * L::kTile + (v / 8) * L::kHalf + r * 128 + (v % 8) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (x.lane == 0) mbar_arrive(x.bars.values(s));
+        }
+        __syncwarp();
+        if (x.lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
+    }
+    if (!ok && x.lane == 0) x.give_up();
+}
+
+// ---- softmax, one thread per query row, and the output -------------------------------
+template <typename E, int D>
+__device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
+{
+    using L = Layout<E, D>;
+    const AttendParams &p = x.p;
+    const int q = warp >> 2, row = 32 * (warp & 3) + x.lane, lane = x.lane;
+    const int token = row * p.inv_G >> 16;               // row / G
+    const uint32_t lanes = x.tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t ts = lanes + kTmS + 128 * q, to = lanes + kTmO + 128 * q;
+    const float c2 = p.scale_log2;
+    uint8_t *stage = x.smem + L::kOut + warp * kStage;
+    int it = 0, mine = 0;                                // score tiles, items with rows
+    bool ok = true;
+    for (int item = 0; ok; item++) {
+        const Item &now = x.c.items[item & 1];
+        ok = x.wait(x.bars.item_full(item & 1), item / 2);
+        if (!ok || now.tokens == 0) break;
+        const Span rows(now, p.tile_tokens, q);
+        const bool dead = 32 * (warp & 3) >= rows.tokens * p.G;      // no row of this warp is one: O may be anything
+        const int key0 = now.key0, tile0 = now.tile0, t0 = now.t0 + q * p.tile_tokens, hk = now.hk, where = now.where;
+        const int64_t cut = now.cut + q * kTileRows;
+        // behind the last key that this row sees, and that the warp's first row does
+        const int see = now.shared ? now.end : min(now.end, rows.first + token + 1);
+        const int least = now.shared ? now.end : min(now.end, rows.first + (32 * (warp & 3) * p.inv_G >> 16) + 1);
+        float m = -INFINITY, sum = 0.f;
+        const int end = now.end;
+        for (int i = 0; i < rows.seen; i++) {
+            const int pos = (tile0 + i) * kTileKeys, keys = tile_keys(end, tile0 + i);
+            // every key of the tile visible to every row of the warp: no test per key
+            const bool whole = pos >= key0 && pos + kTileKeys <= least;
+            // Lanes may give up one by one: the vote on the maxima below is also the one on
+            // that; a lane that gave up goes on until then with what its row of TMEM holds.
+            const bool got = mbar_wait(x.bars.s_full(q), it & 1, x.abort, KDA_WAIT_LIMIT_PAGED);
+            it++;
+            if (dead) {                                  // whatever is there will do as these rows' P
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive(x.bars.p_half(q));
+                    mbar_arrive(x.bars.p_ready(q));
+                }
+                continue;
+            }
+            __syncwarp();
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (32 * k < keys) tmem_ld32(ts + 32 * k, s[k]);
+            loaded(s[0], s[1], s[2], s[3]);
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) {            // visible columns
+                    const uint32_t seen = below(see - pos - 32 * k) & ~below(key0 - pos - 32 * k);
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        if (!(seen & (1u << j))) s[k][j] = 0xff800000u;   // -inf
+                }
+            }
+            float mx[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                mx[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+                for (int j = 1; j < 32; j++) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][j]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float was = slope<E>(m, c2);
+            const bool behind = m != -INFINITY && (top - m) * was > kLag;
+            if (__any_sync(0xffffffffu, behind || !got)) {
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                // the products into O so far were complete before these scores were, and
+                // the next one waits for this warp
+                const float f = behind ? ex2(fmaf(m - top, c2, residue(top, slope<E>(top, c2)) - residue(m, was))) : 1.f;
+                for (int k = 0; k < D / 32; k++) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * k, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st32(to + 32 * k, o);
+                }
+                tmem_wait_st();
+                sum *= f;
+                if (behind) m = top;
+            }
+            if (m == -INFINITY) m = top;                 // the row's first visible keys: its O is still zero
+            const float now_c = slope<E>(m, c2), z = m == -INFINITY ? 0.f : -m * now_c;
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (k == 2) {                            // the first 64 keys are in TMEM: their product can start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x.bars.p_half(q));
+                }
+                if (32 * k < keys) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        float2 e = fma2(make_float2(__uint_as_float(s[k][2 * j]), __uint_as_float(s[k][2 * j + 1])),
+                                        make_float2(now_c, now_c), make_float2(z, z));
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        part[j & 1] = add2(part[j & 1], e);
+                        w[j] = Half2<E>::pack(e.x, e.y);
+                    }
+                    tmem_st16(ts + 16 * k, w);
+                }
+            }
+            sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x.bars.p_ready(q));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
+        if (!ok || !rows.tokens) continue;
+        const int live = rows.tokens * p.G - 32 * (warp & 3);        // of this warp's rows
+        const int64_t dense = (int64_t)t0 * p.Hq + hk * p.G;         // row of [T][Hq] of the tile's first row
+        if (where != kToOut && lane < live) {            // the row's maximum (or what stands for it) and sum
+            float2 *ml = where == kToCut ? p.cut_tiles_ml + cut + row
+                                         : p.whole_ml[where == kToPrefix] + dense + token * (p.Hq - p.G) + row;
+            *ml = make_float2(m, sum);
+        }
+        if (!rows.seen) continue;                        // nothing visible in this piece: no O
+        ok = x.wait(x.bars.o_done(q), mine);
+        if (!ok) break;
+        tc_fence_after();
+        mine++;
+        if (where != kToOut) {
+            // O in fp32, 32 columns at a time through shared memory, so that a store
+            // instruction writes four rows of 128 bytes
+            float *out = where == kToCut ? p.cut_tiles + cut * D : p.whole[where == kToPrefix] + dense * D;
+            const int skip = where == kToCut ? 0 : p.Hq - p.G;       // rows between two tokens'
+#pragma unroll 1
+            for (int h = 0; h < D / 32; h++) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * h, o);
+                tmem_wait_ld();
+                if (h == D / 32 - 1) {                   // O is free for the next item
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x.bars.o_free(q));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                        make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int rr = 4 * j + (lane >> 3), r = 32 * (warp & 3) + rr, tok = r * p.inv_G >> 16;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                    if (rr < live) *reinterpret_cast<uint4 *>(out + ((int64_t)tok * skip + r) * D + 32 * h + 4 * (lane & 7)) = v;
+                }
+                __syncwarp();
+            }
+            continue;
+        }
+        // O / sum in 16 bits, 64 columns at a time
+        const float inv = 1.f / sum;
+        uint16_t *out = p.out + dense * D + 8 * (lane & 7);
+#pragma unroll 1
+        for (int h = 0; h < D / 64; h++) {
+            uint32_t o[2][32];
+            tmem_ld32(to + 64 * h, o[0]);
+            tmem_ld32(to + 64 * h + 32, o[1]);
+            tmem_wait_ld();
+            if (h == D / 64 - 1) {                       // O is free for the next item
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x.bars.o_free(q));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t *v = &o[j / 4][8 * (j & 3)];
+                uint4 r;
+                r.x = Half2<E>::pack(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
+                r.y = Half2<E>::pack(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
+                r.z = Half2<E>::pack(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
+                r.w = Half2<E>::pack(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = r;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int rr = 4 * j + (lane >> 3), r = 32 * (warp & 3) + rr, tok = r * p.inv_G >> 16;
+                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                if (rr < live) *reinterpret_cast<uint4 *>(out + ((int64_t)tok * (p.Hq - p.G) + r) * D + 64 * h) = v;
+            }
+            __syncwarp();
+        }
+    }
+    if (!ok) x.give_up();
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttendParams p)
+{
+    using L = Layout<E, D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));
+    Ctl &c = *reinterpret_cast<Ctl *>(smem + L::kCtl);
+    const Bars bars{smem_u32(c.bars)};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp == 8 && lane == 0) {
+        c.abort = 0;
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(bars.full(s), 1);
+            mbar_init(bars.empty(s), 2);
+            mbar_init(bars.values(s), 1);
+        }
+        for (int q = 0; q < 2; q++) {
+            mbar_init(bars.q_full(q), 1);
+            mbar_init(bars.q_empty(q), 1);
+            mbar_init(bars.s_full(q), 1);
+            mbar_init(bars.p_half(q), 4);
+            mbar_init(bars.p_ready(q), 4);
+            mbar_init(bars.o_done(q), 1);
+            mbar_init(bars.o_free(q), 4);
+            mbar_init(bars.turn(q), 1);
+            mbar_init(bars.drained(q), 1);
+            mbar_init(bars.item_full(q), 1);
+            mbar_init(bars.item_empty(q), kItemReaders);
+        }
+        mbar_fence_init();
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.pages);
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&c.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // the plan is complete, for this kernel and for the rows kernel behind it
+    grid_wait();
+    grid_go_on();
+    const Ctx x{p, c, bars, smem, base, c.tmem, lane, &c.abort};
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 8) load_role<E, D>(x, maps);
+        else if (warp == 10) patch_role<E, D>(x);
+        else product_role<E, D>(x, warp == 11);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        softmax_role<E, D>(x, warp);
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(x.tmem, 512);
+}
+
+template <typename E, int D>
+cudaError_t launch(const PagedAttentionArgs &a, const AttendParams &p)
+{
+    const int page = 1 << a.cache.page_log2, box = page < kTileKeys ? page : kTileKeys;
+    Maps maps;
+    if (!make_map(&maps.q, a.q, a.f16, D, a.Hq, D, a.T, a.q_stride, p.G, p.tile_tokens) ||
+        !make_map(&maps.pages, a.cache.pages, a.f16, D, page, D, (int64_t)a.cache.num_pages * 2 * a.Hk, (int64_t)page * D, box, 1))
+        return cudaErrorInvalidValue;
+    const int smem = Layout<E, D>::kSmem;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = once_per_device(ready, a.device, [&]() {
+        cudaFuncAttributes built;
+        cudaError_t r = cudaFuncGetAttributes(&built, paged_tiles_kernel<E, D>);
+        if (r == cudaSuccess && built.numRegs != kRegs) r = cudaErrorInvalidConfiguration;
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(paged_tiles_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.tile_workers);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_tiles_kernel<E, D>, maps, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tiles(const PagedAttentionArgs &a, const AttendParams &p)
+{
+    if (a.d == 128) return a.f16 ? launch<__half, 128>(a, p) : launch<__nv_bfloat16, 128>(a, p);
+    return a.f16 ? launch<__half, 64>(a, p) : launch<__nv_bfloat16, 64>(a, p);
+}
+
+}  // namespace kda

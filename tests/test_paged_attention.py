@@ -150,7 +150,8 @@ def test_bad_tables_are_reported_and_stay_in_bounds():
     slots = b.slots.clone()
     slots[1], slots[2] = 1000, -7
     out, w = word(slots=slots)
-    assert w == kda.ERR_BAD_SLOT and (out[1:22] == 9).all() and t.equal(out[0], want[0]) and t.equal(out[22], want[22])
+    assert w == kda.ERR_BAD_SLOT and (out[1:22] == 9).all()
+    b.check(out, skip=(1, 2))                          # (another batch is cut up in another way: not the same bytes)
     groups, lens, kept = b.prefixes
     out, w = word(prefixes=(groups, lens, i32(99)))
     assert w & kda.ERR_BAD_SLOT
