@@ -25,15 +25,19 @@
 #include "kda.h"
 #include "kda_paged.h"
 #include "kda_pdl.cuh"
+#include "kda_tiles.cuh"
 
 namespace kda {
 namespace {
+
+using tiles::add2;
+using tiles::fma2;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kAtOnce = 4;                   // 16-byte loads of a thread on their way
 constexpr int kLeast = 2048, kLongest = 32768;   // logits of a slice
 constexpr int kMost = 512;                   // candidates that are ranked by counting
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct BeamParams {
     const void *logits;
@@ -98,17 +102,31 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-template <typename E> struct Vec;    // 16 bytes of logits
+// Two values of 16 bytes of logits at a time (of 32 bits: one): unpacked, and the larger ones of
+// two words (without NaN).
+template <typename E> struct Vec;
 template <> struct Vec<float> {
     static constexpr int kN = 4;
+    static constexpr uint32_t kLowest = 0xff800000u;     // -inf
     static __device__ __forceinline__ void up(const uint4 &v, float *x)
     {
         x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
     }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
+    {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static __device__ __forceinline__ float largest(uint32_t w) { return __uint_as_float(w); }
     static __device__ __forceinline__ float one(float x) { return x; }
 };
+template <typename E2> __device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b)
+{
+    const E2 m = __hmax2(*reinterpret_cast<const E2 *>(&a), *reinterpret_cast<const E2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int kN = 8;
+    static constexpr uint32_t kLowest = 0xff80ff80u;
     static __device__ __forceinline__ void up(const uint4 &v, float *x)
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -118,10 +136,16 @@ template <> struct Vec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return larger2<__nv_bfloat162>(a, b); }
+    static __device__ __forceinline__ float largest(uint32_t w)
+    {
+        return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
     static __device__ __forceinline__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
 };
 template <> struct Vec<__half> {
     static constexpr int kN = 8;
+    static constexpr uint32_t kLowest = 0xfc00fc00u;
     static __device__ __forceinline__ void up(const uint4 &v, float *x)
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -131,6 +155,12 @@ template <> struct Vec<__half> {
             x[2 * i] = f.x;
             x[2 * i + 1] = f.y;
         }
+    }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return larger2<__half2>(a, b); }
+    static __device__ __forceinline__ float largest(uint32_t w)
+    {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        return fmaxf(f.x, f.y);
     }
     static __device__ __forceinline__ float one(__half x) { return __half2float(x); }
 };
@@ -167,32 +197,52 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
     // the thread's maximum (without NaN) and the sum of exponentials relative to it, or to
     // 0 where nothing is finite; a NaN among the logits makes the sum NaN, and with it the
     // row's normaliser
-    float top = single, sum = ex2(single > -INFINITY ? 0.f : single);
-    auto take = [&](const uint4 &v) {
-        float x[kN], high;
-        Vec<E>::up(v, x);
-        high = x[0];
-#pragma unroll
-        for (int j = 1; j < kN; j++) high = fmaxf(high, x[j]);
-        if (high > top) {
-            if (top > -INFINITY) sum *= ex2((top - high) * kLog2e);
-            top = high;
-        }
-        const float base = top > -INFINITY ? top : 0.f;
-        float part = 0.f;
-#pragma unroll
-        for (int j = 0; j < kN; j++) part += ex2((x[j] - base) * kLog2e);
-        sum += part;
-    };
-    int v = first;
-    for (; v + (kAtOnce - 1) * kThreads < end; v += kAtOnce * kThreads) {
+    float top = single, sum = ex2(single > -INFINITY ? 0.f : single), base = 0.f, base2 = 0.f;
+    if (top > -INFINITY) base = top, base2 = base * kLog2e;
+    for (int v = first; v < end; v += kAtOnce * kThreads) {
         uint4 r[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < kAtOnce; i++) r[i] = __ldg(body + v + i * kThreads);
+        for (int i = 0; i < kAtOnce; i++) {
+            const uint32_t none = Vec<E>::kLowest;
+            r[i] = v + i * kThreads < end ? __ldg(body + v + i * kThreads) : make_uint4(none, none, none, none);
+        }
+        uint32_t most = Vec<E>::kLowest;
 #pragma unroll
-        for (int i = 0; i < kAtOnce; i++) take(r[i]);
+        for (int i = 0; i < kAtOnce; i++)
+            most = Vec<E>::larger(Vec<E>::larger(Vec<E>::larger(r[i].x, r[i].y), Vec<E>::larger(r[i].z, r[i].w)), most);
+        const float high = Vec<E>::largest(most);
+        if (high > top) {
+            if (top > -INFINITY) sum *= ex2((top - high) * kLog2e);
+            base = top = high;
+            base2 = base * kLog2e;
+        }
+        if (fabsf(base) < 1024.f) {                      // a paired instruction for two exponents
+            float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                float x[kN];
+                Vec<E>::up(r[i], x);
+#pragma unroll
+                for (int j = 0; j < kN; j += 2) {
+                    float2 e = fma2(make_float2(x[j], x[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-base2, -base2));
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    part = add2(part, e);
+                }
+            }
+            // what base2 was rounded by, at most 2^-14, is in every exponent
+            const float all = part.x + part.y;
+            sum += fmaf(all, -kLn2 * fmaf(base, kLog2e, -base2), all);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                float x[kN];
+                Vec<E>::up(r[i], x);
+#pragma unroll
+                for (int j = 0; j < kN; j++) sum += ex2((x[j] - base) * kLog2e);
+            }
+        }
     }
-    for (; v < end; v += kThreads) take(__ldg(body + v));
 
     float wide = top;
     for (int o = 1; o < p.spread; o *= 2) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
@@ -359,7 +409,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         return c;
     };
     uint32_t top = 0;
-    for (int e = tid; e < all; e += kThreads) top = max(top, (uint32_t)(candidate(e).score >> 32));
+    constexpr int kKept = 4;
+    Candidate kept[kKept];                               // the thread's first ones
+#pragma unroll
+    for (int i = 0; i < kKept; i++) {
+        kept[i] = tid + i * kThreads < all ? candidate(tid + i * kThreads) : Candidate{0, 0, 0};
+        top = max(top, (uint32_t)(kept[i].score >> 32));
+    }
+    for (int e = tid + kKept * kThreads; e < all; e += kThreads) top = max(top, (uint32_t)(candidate(e).score >> 32));
     for (int o = 1; o < p.spread; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = __reduce_min_sync(0xffffffffu, top);
     if (lane == 0) low_w[warp] = top;
@@ -367,25 +424,34 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     uint32_t bound = low_w[0];
 #pragma unroll
     for (int w = 1; w < kWarps; w++) bound = min(bound, low_w[w]);
-    for (int e = tid; e < all; e += kThreads) {
-        const Candidate c = candidate(e);
+    auto collect = [&](const Candidate &c) {
         if (c.score && (uint32_t)(c.score >> 32) >= bound) {
             const int k = atomicAdd(&count, 1);
             if (k < kMost) found[k] = c;
         }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kKept; i++) collect(kept[i]);
+    for (int e = tid + kKept * kThreads; e < all; e += kThreads) collect(candidate(e));
     __syncthreads();
     const int n = count;
     if (n <= kMost) {
-        for (int i = tid; i < max(n, B); i += kThreads) {
-            if (i >= n) {
-                best[i] = {0, 0, 0};
-                continue;
-            }
-            const Candidate mine = found[i];
+        // eight lanes count for a candidate
+        for (int i0 = tid / 8; i0 - tid / 8 < max(n, B); i0 += kThreads / 8) {
+            const bool there = i0 < n;
+            const Candidate mine = there ? found[i0] : Candidate{0, 0, 0};
             int rank = 0;
-            for (int j = 0; j < n; j++) rank += better(found[j], mine);
-            if (rank < B) best[rank] = mine;
+            if (there)
+                for (int j = tid % 8; j < n; j += 8) {
+                    const uint64_t other = found[j].score;
+                    rank += other > mine.score || (other == mine.score && better(found[j], mine));
+                }
+#pragma unroll
+            for (int o = 4; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+            if (tid % 8 == 0) {
+                if (there && rank < B) best[rank] = mine;
+                if (!there && i0 < B) best[i0] = {0, 0, 0};
+            }
         }
     } else {
         Candidate last = {~(uint64_t)0, 0, -1};

@@ -56,13 +56,19 @@ struct AttendParams {
     float *cut_tiles, *cut_rows;     // [2 workers][kPieceRows | kFewRows][d]: pieces with some of them
     float2 *cut_tiles_ml, *cut_rows_ml;
     int tile_workers, row_workers;
+    int few;                         // parts of so many query rows a key head go to the rows kernel
     int after_tiles;                 // the rows kernel runs behind the tiles kernel
 };
+
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);   // 32 bits, mostly: fewer instructions
+}
 
 // A worker's share of a line of `total` steps a head: at least `least`.
 __device__ __forceinline__ int64_t share_of(int64_t total, int Hk, int workers, int least)
 {
-    const int64_t all = total * Hk, each = (all + workers - 1) / workers;
+    const int64_t each = quotient(total * Hk + workers - 1, workers);
     return each < least ? least : each;
 }
 constexpr int kLeastTiles = 2, kLeastSteps = 8;
@@ -70,20 +76,21 @@ constexpr int kLeastTiles = 2, kLeastSteps = 8;
 // Sum of floor((a i + b) / 128) over i < n, for a, b >= 0: the whole parts of a / 128 and b / 128
 // sum up at once, and what is left counts the lattice points below a line, which turns into
 // the same problem with the axes exchanged.
-__device__ __forceinline__ int64_t sum_of_tiles(int64_t n, int64_t a, int64_t b)
+__device__ __forceinline__ int64_t sum_of_tiles(int64_t n, int a, int64_t b)
 {
-    int64_t sum = 0, m = kTileKeys;
+    int64_t sum = n * (n - 1) / 2 * (a / kTileKeys) + n * (b / kTileKeys);
+    uint32_t m = kTileKeys, x = a % kTileKeys, y = (uint32_t)(b % kTileKeys);
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const int64_t top = a * n + b;
+        const int64_t top = x * n + y;
         if (top < m) break;
-        n = top / m;
-        b = top % m;
-        const int64_t was = a;
-        a = m;
+        n = quotient(top, m);
+        y = (uint32_t)(top - n * m);
+        const uint32_t was = x;
+        x = m;
         m = was;
+        sum += n * (n - 1) / 2 * (x / m) + n * (y / m);
+        x %= m;
+        y %= m;
     }
     return sum;
 }

@@ -10,6 +10,7 @@
 // Four kernels: the plan (one CTA), the tiles and the rows kernel, and the join; each
 // is launched early (programmatic dependent launch) and waits for what it needs.
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "kda_paged_attend.cuh"
 
@@ -69,7 +70,7 @@ __device__ __forceinline__ Part make_part(const AttendParams &p, int i)
             x.key1 = r.start + x.tokens;
         }
     }
-    x.kind = x.tokens <= 0 || x.key1 <= x.key0 ? kNoWork : (int64_t)x.tokens * p.G <= kFewRows ? kRowsWork : kTilesWork;
+    x.kind = x.tokens <= 0 || x.key1 <= x.key0 ? kNoWork : (int64_t)x.tokens * p.G <= p.few ? kRowsWork : kTilesWork;
     return x;
 }
 
@@ -125,165 +126,179 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
 }
 
-// Joins the pieces of rows.  A CTA of eight warps takes one row of the batch and `heads`
-// of its query heads; `team` warps share one head.
-constexpr int kJoinWarps = 8;
+// Joins the pieces of rows.  A CTA takes one row of the batch and `heads` of its query heads;
+// `team` groups of eight lanes share one head, every team-th piece each, and then every
+// team-th pair of its columns.  What bounds it is the latency of a few loads that depend on
+// one another, so a head has few lanes and each of them several loads on its way, and all
+// heads of a CTA go at once.  Most of a row's facts are the same for all its heads; a head
+// then costs two divisions, and nothing more where its answer is written already (a chunk of
+// a prompt: all but the spans that two workers share).
+constexpr int kJoinThreads = 256, kLanes = 8, kGroups = kJoinThreads / kLanes;
 
-// the pieces of one of a row's two parts
+// a row's place in one of its two parts
+struct Place {
+    int64_t total, share;            // of the kernel's line
+    int64_t begin, n;                // the row's span in the line of a key head
+    int row, rows;                   // the row's first query head in a piece; rows of a piece
+    bool tiles, any;
+};
+__device__ __forceinline__ Place place_of(const AttendParams &p, int part, const Part &x, bool shared, int t)
+{
+    Place r = {};
+    r.any = x.kind != kNoWork;
+    r.tiles = x.kind == kTilesWork;
+    const int i = t - x.t0, span = 2 * p.tile_tokens;
+    const int64_t *before = r.tiles ? p.tiles : p.steps;
+    r.total = __ldcg(before + p.P + p.N);
+    r.begin = __ldcg(before + part);
+    r.share = share_of(r.total, p.Hk, r.tiles ? p.tile_workers : p.row_workers, r.tiles ? kLeastTiles : kLeastSteps);
+    if (r.tiles) {
+        const int j = i / span, u = i - j * span, q = u >= p.tile_tokens;
+        r.begin += tiles_before(x, shared, span, j);
+        r.n = span_tiles(x, shared, span, j);
+        r.row = q * kTileRows + (u - q * p.tile_tokens) * p.G;
+        r.rows = kPieceRows;
+    } else {
+        r.n = part_steps(x);
+        r.row = i * p.G;
+        r.rows = kFewRows;
+    }
+    return r;
+}
+
+// the pieces of one of a row's parts, for one head
 struct Pieces {
-    const float *whole;              // if there is only one, with all keys
-    const float2 *whole_ml;
-    const float *cut;                // else the first worker's, and so on
-    const float2 *cut_ml;
-    int64_t apart, first;            // rows between two pieces; the first piece's row
-    int64_t later;                   // and the second one's
+    const float *o;                  // the row in the first piece,
+    const float2 *ml;
+    int64_t second, apart;           // rows from there to the second one's, and between later ones'
     int n;                           // 0: there are none, or the row's answer is written
 };
-
-__device__ __forceinline__ Pieces pieces_of(const AttendParams &p, int part, const Part &x, int t, int hq, int which, bool alone)
+template <int D>
+__device__ __forceinline__ Pieces pieces_of(const AttendParams &p, const Place &y, int t, int hq, bool shared, bool alone)
 {
     Pieces r = {};
-    if (x.kind == kNoWork) return r;
-    const bool shared = which == 1, tiles = x.kind == kTilesWork;
-    const int hk = hq / p.G, g = hq - hk * p.G, i = t - x.t0, span = 2 * p.tile_tokens;
-    const int64_t *before = tiles ? p.tiles : p.steps;
-    const int64_t total = __ldcg(before + p.P + p.N);
-    const int64_t share = tiles ? share_of(total, p.Hk, p.tile_workers, kLeastTiles)
-                                : share_of(total, p.Hk, p.row_workers, kLeastSteps);
-    int64_t begin = hk * total + __ldcg(before + part), end;
-    int row;                                             // of the piece
-    if (tiles) {
-        const int j = i / span, u = i - j * span, q = u >= p.tile_tokens;
-        begin += tiles_before(x, shared, span, j);
-        end = begin + span_tiles(x, shared, span, j);
-        row = q * kTileRows + (u - q * p.tile_tokens) * p.G + g;
-    } else {
-        end = begin + part_steps(x);
-        row = i * p.G + g;
-    }
-    const int64_t w0 = begin / share, w1 = (end - 1) / share;
+    if (!y.any) return r;
+    const int hk = hq / p.G;
+    const int64_t begin = hk * y.total + y.begin, w0 = quotient(begin, y.share), w1 = quotient(begin + y.n - 1, y.share);
     if (w0 == w1) {
-        if (alone) return r;
-        r.whole = p.whole[which];
-        r.whole_ml = p.whole_ml[which];
-        r.first = (int64_t)t * p.Hq + hq;
-        r.n = 1;
-        return r;
+        const int64_t row = (int64_t)t * p.Hq + hq;
+        r.o = p.whole[shared] + row * D;
+        r.ml = p.whole_ml[shared] + row;
+        r.n = !alone;
+    } else {
+        const int64_t first = cut_piece(w0, begin, w0 * y.share) * y.rows + y.row + hq - hk * p.G;
+        r.o = (y.tiles ? p.cut_tiles : p.cut_rows) + first * D;
+        r.ml = (y.tiles ? p.cut_tiles_ml : p.cut_rows_ml) + first;
+        r.second = y.rows;                               // (the first is its worker's second cut piece)
+        r.apart = 2 * y.rows;
+        r.n = (int)(w1 - w0 + 1);
     }
-    const int rows = tiles ? kPieceRows : kFewRows;
-    r.cut = tiles ? p.cut_tiles : p.cut_rows;
-    r.cut_ml = tiles ? p.cut_tiles_ml : p.cut_rows_ml;
-    r.first = cut_piece(w0, begin, w0 * share) * rows + row;
-    r.later = 2 * (w0 + 1) * rows + row;
-    r.apart = 2 * rows;
-    r.n = (int)(w1 - w0 + 1);
     return r;
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttendParams p, int heads, int team)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendParams p, int heads, int team)
 {
-    constexpr int kEach = D / 32;
-    __shared__ float os[kJoinWarps][D], ms[kJoinWarps], ls[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kVecs = D / 4 / kLanes, kBatch = 2;    // 16-byte vectors of a lane in a row; pieces at a time
+    __shared__ float4 os[kGroups][D / 4];
+    __shared__ float ms[kGroups], ls[kGroups];
+    __shared__ Place at[2];
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int chunks = (p.Hq + heads - 1) / heads, t = blockIdx.x / chunks, head0 = (blockIdx.x - t * chunks) * heads;
-    const int n = p.cu ? sequence_with(p.cu, p.N, t, lane) : t;
+    const int n = p.cu ? sequence_with(p.cu, p.N, t, threadIdx.x & 31) : t;
     grid_wait();
     if (n < 0) return;
     const Part own = load_part(p.parts + p.P + n);
     if (own.kind == kNoWork || t - own.t0 >= own.tokens) return;
-    Part prefix = {};
-    if (own.prefix >= 0) prefix = load_part(p.parts + own.prefix);
-    const int teams = kJoinWarps / team, place = warp % team;
-    for (int h0 = head0; h0 < min(p.Hq, head0 + heads); h0 += teams) {
-        const int hq = h0 + warp / team;
-        const bool mine = hq < min(p.Hq, head0 + heads);
-        Pieces ps[2] = {};
-        if (mine) {
-            ps[0] = pieces_of(p, p.P + n, own, t, hq, 0, own.prefix < 0);
-            if (own.prefix >= 0) ps[1] = pieces_of(p, own.prefix, prefix, t, hq, 1, false);
-        }
-        const int all = ps[0].n + ps[1].n;               // the same in the whole team
-        float m = -INFINITY, l = 0.f, acc[kEach];
+    if (threadIdx.x == 0) at[0] = place_of(p, p.P + n, own, false, t);
+    if (threadIdx.x == 32) {                             // (another warp, at the same time)
+        at[1].any = false;
+        if (own.prefix >= 0) at[1] = place_of(p, own.prefix, load_part(p.parts + own.prefix), true, t);
+    }
+    __syncthreads();
+    const int place = group % team, end = min(p.Hq, head0 + heads);
+    for (int h0 = head0; h0 < end; h0 += kGroups / team) {
+        const int hq = h0 + group / team;
+        float m = -INFINITY, l = 0.f;
+        float4 acc[kVecs];
 #pragma unroll
-        for (int e = 0; e < kEach; e++) acc[e] = 0.f;
-        for (int i0 = 32 * place; i0 < all; i0 += 32 * team) {
-            // a piece for each lane
-            const int i = i0 + lane;
-            const float *from = nullptr;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (i < all) {
-                const Pieces &x = i < ps[0].n ? ps[0] : ps[1];
-                const int k = i < ps[0].n ? i : i - ps[0].n;
-                const int64_t at = k == 0 ? x.first : x.later + (k - 1) * x.apart;
-                from = (x.whole ? x.whole : x.cut) + at * D;
-                ml = __ldcg((x.whole ? x.whole_ml : x.cut_ml) + at);
-            }
-            float top = fmaxf(m, ml.x);
+        for (int v = 0; v < kVecs; v++) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int all = 0;                                     // pieces: the same in the whole team
+        if (hq < end) {
+#pragma unroll 1
+            for (int part = 0; part < 2; part++) {
+                const Pieces x = pieces_of<D>(p, at[part], t, hq, part, own.prefix < 0);
+                // piece i of both parts is that of group i % team
+                for (int i0 = (place - all % team + team) % team; i0 < x.n; i0 += kBatch * team) {
+                    float2 ml[kBatch];
+                    float4 o[kBatch][kVecs];
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float was = m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
-            const float f = ml.x == -INFINITY ? 0.f : ex2((ml.x - top) * p.scale_log2);
-            float sum = ml.x == -INFINITY ? 0.f : f * ml.y;
+                    for (int k = 0; k < kBatch; k++) {
+                        const int i = i0 + k * team;
+                        ml[k] = make_float2(-INFINITY, 0.f);
+                        if (i < x.n) {
+                            const int64_t row = i ? x.second + (i - 1) * x.apart : 0;
+                            ml[k] = __ldcg(x.ml + row);
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = l * was + sum;
-            m = top;
+                            for (int v = 0; v < kVecs; v++)
+                                o[k][v] = __ldcg(reinterpret_cast<const float4 *>(x.o + row * D) + v * kLanes + lane);
+                        }
+                    }
 #pragma unroll
-            for (int e = 0; e < kEach; e++) acc[e] *= was;
-            const int here = min(32, all - i0);
-#pragma unroll 8
-            for (int k = 0; k < here; k++) {
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                const float *at = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)from, k));
-                if (fk == 0.f) continue;                 // nothing visible there: it may not even be written
-                float o[kEach];
-                if (kEach == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(at) + lane);
-                    o[0] = v.x; o[1] = v.y; o[2 % kEach] = v.z; o[3 % kEach] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(at) + lane);
-                    o[0] = v.x; o[1] = v.y;
+                    for (int k = 0; k < kBatch; k++) {
+                        if (ml[k].x == -INFINITY) continue;      // nothing visible there: o may not even be written
+                        const float top = fmaxf(m, ml[k].x);
+                        const float was = m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
+                        const float f = ex2((ml[k].x - top) * p.scale_log2);
+                        l = fmaf(f, ml[k].y, l * was);
+                        m = top;
+#pragma unroll
+                        for (int v = 0; v < kVecs; v++) {
+                            acc[v].x = fmaf(f, o[k][v].x, acc[v].x * was);
+                            acc[v].y = fmaf(f, o[k][v].y, acc[v].y * was);
+                            acc[v].z = fmaf(f, o[k][v].z, acc[v].z * was);
+                            acc[v].w = fmaf(f, o[k][v].w, acc[v].w * was);
+                        }
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < kEach; e++) acc[e] = fmaf(fk, o[e], acc[e]);
+                all += x.n;
             }
         }
-        if (team > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < kEach; e++) os[warp][kEach * lane + e] = acc[e];
-            if (lane == 0) {
-                ms[warp] = m;
-                ls[warp] = l;
-            }
-            __syncthreads();
-            if (place == 0) {
-                float top = m;
-                for (int w = 1; w < team; w++) top = fmaxf(top, ms[warp + w]);
-                float sum = 0.f, o[kEach];
-#pragma unroll
-                for (int e = 0; e < kEach; e++) o[e] = 0.f;
-                for (int w = 0; w < team; w++) {
-                    if (ms[warp + w] == -INFINITY) continue;
-                    const float f = ex2((ms[warp + w] - top) * p.scale_log2);
-                    sum = fmaf(f, ls[warp + w], sum);
-#pragma unroll
-                    for (int e = 0; e < kEach; e++) o[e] = fmaf(f, os[warp + w][kEach * lane + e], o[e]);
-                }
-                l = sum;
-#pragma unroll
-                for (int e = 0; e < kEach; e++) acc[e] = o[e];
-            }
-        }
-        if (all && place == 0) {
+        uint16_t *to = p.out + ((int64_t)t * p.Hq + hq) * D;
+        if (team == 1) {
+            if (!all) continue;
             const float inv = 1.f / l;
-            uint16_t *to = p.out + ((int64_t)t * p.Hq + hq) * D + kEach * lane;
-            if (kEach == 4)
-                *reinterpret_cast<uint2 *>(to) = make_uint2(Half2<E>::pack(acc[0] * inv, acc[1] * inv),
-                                                            Half2<E>::pack(acc[2 % kEach] * inv, acc[3 % kEach] * inv));
-            else
-                *reinterpret_cast<uint32_t *>(to) = Half2<E>::pack(acc[0] * inv, acc[1] * inv);
+#pragma unroll
+            for (int v = 0; v < kVecs; v++)
+                reinterpret_cast<uint2 *>(to)[v * kLanes + lane] =
+                    make_uint2(Half2<E>::pack(acc[v].x * inv, acc[v].y * inv), Half2<E>::pack(acc[v].z * inv, acc[v].w * inv));
+            continue;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < kVecs; v++) os[group][v * kLanes + lane] = acc[v];
+        if (lane == 0) {
+            ms[group] = m;
+            ls[group] = l;
+        }
+        __syncthreads();
+        if (!all) continue;
+        const int first = group - place;                 // the team's first group
+        float top = -INFINITY, sum = 0.f;
+        for (int w = 0; w < team; w++) top = fmaxf(top, ms[first + w]);
+        for (int w = 0; w < team; w++)
+            if (ms[first + w] != -INFINITY) sum = fmaf(ex2((ms[first + w] - top) * p.scale_log2), ls[first + w], sum);
+        const float inv = 1.f / sum;
+        for (int c = threadIdx.x - first * kLanes; c < D / 2; c += team * kLanes) {
+            float2 x = make_float2(0.f, 0.f);
+            for (int w = 0; w < team; w++) {
+                if (ms[first + w] == -INFINITY) continue;
+                const float f = ex2((ms[first + w] - top) * p.scale_log2);
+                const float2 o = reinterpret_cast<const float2 *>(os[first + w])[c];
+                x.x = fmaf(f, o.x, x.x);
+                x.y = fmaf(f, o.y, x.y);
+            }
+            reinterpret_cast<uint32_t *>(to)[c] = Half2<E>::pack(x.x * inv, x.y * inv);
         }
     }
 }
@@ -323,15 +338,15 @@ Room room_of(int N, int T, int P, int Hq, int Hk, int d)
 
 template <typename E, int D> cudaError_t launch_join(const PagedAttentionArgs &a, const AttendParams &p)
 {
-    // few rows: a CTA a head, whose warps share the pieces; many: all heads of a row
-    int heads = a.Hq, team = 1;
-    while (heads > 1 && (int64_t)a.T * ((a.Hq + heads - 1) / heads) < 4 * a.num_sms) heads = (heads + 1) / 2;
-    while (team < kJoinWarps && heads * team < kJoinWarps) team *= 2;
+    // many rows: a group of lanes a head; few: a CTA a head, whose groups share the pieces
+    int heads = a.Hq < kGroups ? a.Hq : kGroups, team = 1;
+    while (heads > 1 && (int64_t)a.T * ((a.Hq + heads - 1) / heads) < 2 * a.num_sms) heads = (heads + 1) / 2;
+    while (heads * team * 2 <= kGroups) team *= 2;
     const int64_t blocks = (int64_t)a.T * ((a.Hq + heads - 1) / heads);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -374,6 +389,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a)
     // many heads none for the rows kernel
     const bool tiles = can_have_tiles(a.T, p.G) && (a.cu_seqlens || a.P || p.G > kFewRows), rows = p.G <= kFewRows;
     p.after_tiles = tiles;
+    p.few = getenv("FEW") && tiles ? atoi(getenv("FEW")) : kFewRows;
     plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && tiles) e = launch_paged_tiles(a, p);

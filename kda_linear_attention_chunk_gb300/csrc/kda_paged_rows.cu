@@ -47,7 +47,7 @@ paged_rows_kernel(const __grid_constant__ AttendParams p)
     int64_t at = from;
     while (at < to) {
         // the part and key head of this place in the line, and the worker's steps of it
-        const int hk = (int)(at / total), part = part_at(p.steps, parts, at - hk * total, lane);
+        const int hk = (int)quotient(at, total), part = part_at(p.steps, parts, at - hk * total, lane);
         const bool shared = part < p.P;
         const Part x = load_part(p.parts + part);
         const int64_t begin = hk * total + __ldcg(p.steps + part), end = begin + part_steps(x);

@@ -175,7 +175,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             break;
         }
         // the part, span and key head of this place in the line
-        const int hk = (int)(at / total), part = part_at(p.tiles, parts, at - hk * total, x.lane);
+        const int hk = (int)quotient(at, total), part = part_at(p.tiles, parts, at - hk * total, x.lane);
         const bool shared = part < p.P;
         const Part y = load_part(p.parts + part);
         int64_t begin = hk * total + __ldcg(p.tiles + part);
