@@ -1038,9 +1038,8 @@ def beam_select(logits, scores, ended=None, end_token: int = -1, slots=None, str
     if size <= 0:
         raise KdaError(KDA_ERR_SHAPE if B <= 64 and V <= 1 << 24 else KDA_ERR_UNSUPPORTED, "kda_beam_select")
     work = _scratch(size, device, stream)
-    best = _new(shape, torch.float32, device, stream)
-    ints = _new((6, G, B), torch.int32, device, stream).unbind(0)   # one allocation for all
-    parents, tokens, stopped, new_slots, src, dst = ints
+    best, parents, tokens, stopped, new_slots, src, dst = _new((7, G, B), torch.int32, device, stream).unbind(0)
+    best = best.view(torch.float32)              # one allocation for all
     stops, moves = end_token >= 0, slots is not None
     st = lib.kda_beam_select(logits.data_ptr(), row if rows > 1 else V, kinds[logits.dtype], s, was, end_token, ids,
                              best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), stopped.data_ptr() if stops else 0,

@@ -276,11 +276,19 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
     // every value of the thread's, once more, with its token
     auto each = [&](auto &&use) {
         if (odd >= 0) use(single, odd);
-        for (int v = first; v < end; v += kThreads) {
-            float x[kN];
-            Vec<E>::up(__ldg(body + v), x);
+        for (int v = first; v < end; v += kAtOnce * kThreads) {
+            uint4 r[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < kN; j++) use(x[j], before + v * kN + j);
+            for (int i = 0; i < kAtOnce; i++)
+                if (v + i * kThreads < end) r[i] = __ldg(body + v + i * kThreads);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                if (v + i * kThreads >= end) break;
+                float x[kN];
+                Vec<E>::up(r[i], x);
+#pragma unroll
+                for (int j = 0; j < kN; j++) use(x[j], before + (v + i * kThreads) * kN + j);
+            }
         }
     };
     if (top >= bound && top > -INFINITY)
@@ -385,11 +393,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     }
     __syncthreads();
     const int per = p.slices * B, all = B * per;         // places of a beam's candidates
-    // the candidate at place e
+    // The candidate at place e.  Warp w's places are w, w + 8, ..., and the beams' order moves on by
+    // one with each of a beam's places, so that the groups, whose maxima bound the best, get
+    // beams and ranks alike (a beam a group: nearly all candidates are above the bound).
     auto candidate = [&](int e) {
-        const int b = e / per, at = e - b * per;
+        const int i = e % kThreads, at = (e - i + i % 32 * kWarps + i / 32) / B, turn = (e - i + i % 32 * kWarps + i / 32) % B;
+        const int b = (turn + at) % B;
         Candidate c = {0, 0, b};
         float high = -INFINITY, low = 0.f;
+        if (at >= per) return c;                         // behind the last place
         if (kind[b] == 2 && at == 0) {
             high = score[b];
             c.key = key_of(0.f, p.end_token);
@@ -413,10 +425,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     Candidate kept[kKept];                               // the thread's first ones
 #pragma unroll
     for (int i = 0; i < kKept; i++) {
-        kept[i] = tid + i * kThreads < all ? candidate(tid + i * kThreads) : Candidate{0, 0, 0};
+        kept[i] = i * kThreads < all ? candidate(tid + i * kThreads) : Candidate{0, 0, 0};
         top = max(top, (uint32_t)(kept[i].score >> 32));
     }
-    for (int e = tid + kKept * kThreads; e < all; e += kThreads) top = max(top, (uint32_t)(candidate(e).score >> 32));
+    for (int e = tid + kKept * kThreads; e - tid < all; e += kThreads) top = max(top, (uint32_t)(candidate(e).score >> 32));
     for (int o = 1; o < p.spread; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = __reduce_min_sync(0xffffffffu, top);
     if (lane == 0) low_w[warp] = top;
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     };
 #pragma unroll
     for (int i = 0; i < kKept; i++) collect(kept[i]);
-    for (int e = tid + kKept * kThreads; e < all; e += kThreads) collect(candidate(e));
+    for (int e = tid + kKept * kThreads; e - tid < all; e += kThreads) collect(candidate(e));
     __syncthreads();
     const int n = count;
     if (n <= kMost) {
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         Candidate last = {~(uint64_t)0, 0, -1};
         for (int k = 0; k < B; k++) {
             Candidate mine = {0, 0, B};
-            for (int e = tid; e < all; e += kThreads) {
+            for (int e = tid; e - tid < all; e += kThreads) {
                 const Candidate c = candidate(e);
                 if (c.score && better(last, c) && better(c, mine)) mine = c;
             }

@@ -37,6 +37,12 @@ struct alignas(16) Part {
     int entry;                       // whose pages they are in
     int prefix;                      // own keys: the part of the prefix, -1 if there is none
     int kind;
+    int64_t begin, pad;              // its tiles' or steps' place in the line of a key head
+};
+
+// the lines of the tiles and of the rows kernel
+struct alignas(16) Lines {
+    int64_t total[2], share[2];      // steps of a key head, and a worker's share of all
 };
 
 struct AttendParams {
@@ -50,13 +56,13 @@ struct AttendParams {
     float scale_log2;
     int *err;
     Part *parts;                     // [P + N]
-    int64_t *tiles, *steps;          // [P + N + 1]: of one key head, before each part
+    Lines *lines;
+    int64_t *tiles, *steps;          // [P + N]: of one key head, before each part
     float *whole[2];                 // [T][Hq][d]: pieces with all of a part's keys, of own keys and of prefixes
     float2 *whole_ml[2];             // [T][Hq]: their maxima and sums
     float *cut_tiles, *cut_rows;     // [2 workers][kPieceRows | kFewRows][d]: pieces with some of them
     float2 *cut_tiles_ml, *cut_rows_ml;
     int tile_workers, row_workers;
-    int few;                         // parts of so many query rows a key head go to the rows kernel
     int after_tiles;                 // the rows kernel runs behind the tiles kernel
 };
 
@@ -125,9 +131,79 @@ __device__ __forceinline__ int part_steps(const Part &x)
 __device__ __forceinline__ Part load_part(const Part *p)
 {
     Part x;
-    const int4 a = __ldcg(reinterpret_cast<const int4 *>(p)), b = __ldcg(reinterpret_cast<const int4 *>(p) + 1);
+    const int4 *from = reinterpret_cast<const int4 *>(p);
+    const int4 a = __ldcg(from), b = __ldcg(from + 1);
+    const longlong2 c = __ldcg(reinterpret_cast<const longlong2 *>(from + 2));
     x.t0 = a.x; x.tokens = a.y; x.first = a.z; x.key0 = a.w;
     x.key1 = b.x; x.entry = b.y; x.prefix = b.z; x.kind = b.w;
+    x.begin = c.x;
+    return x;
+}
+__device__ __forceinline__ void store_part(Part *p, const Part &x)
+{
+    int4 *to = reinterpret_cast<int4 *>(p);
+    to[0] = make_int4(x.t0, x.tokens, x.first, x.key0);
+    to[1] = make_int4(x.key1, x.entry, x.prefix, x.kind);
+    reinterpret_cast<longlong2 *>(to)[2] = make_longlong2(x.begin, 0);
+}
+__device__ __forceinline__ Lines load_lines(const Lines *p)
+{
+    const longlong2 a = __ldcg(reinterpret_cast<const longlong2 *>(p)), b = __ldcg(reinterpret_cast<const longlong2 *>(p) + 1);
+    return {{a.x, a.y}, {b.x, b.y}};
+}
+
+// the positions that group g shares, and whose pages they are in
+struct Prefix {
+    int len, entry;
+};
+__device__ __forceinline__ Prefix prefix_of(const AttendParams &p, int g, int *err)
+{
+    Prefix x;
+    x.entry = entry_of(p.prefix_slots, g, p.cache.num_slots, p.err, err != nullptr);
+    const int was = p.prefix_lens[g];
+    x.len = x.entry < 0 ? 0 : min(max(was, 0), capacity(p.cache));
+    if (err && x.entry >= 0 && x.len != was) atomicOr(err, kErrBadPosition);
+    return x;
+}
+__device__ __forceinline__ int group_start(const AttendParams &p, int g) { return min(max(p.groups[g], 0), p.N); }
+
+__device__ __forceinline__ Part make_part(const AttendParams &p, int i)
+{
+    Part x = {};
+    x.prefix = -1;
+    if (i < p.P) {
+        const int a = group_start(p, i), b = group_start(p, i + 1);
+        if (p.groups[i] != a || p.groups[i + 1] != b || a > b) atomicOr(p.err, kErrBadSeqlens);
+        const Prefix y = prefix_of(p, i, p.err);
+        x.t0 = p.cu ? clamp_row(p.cu[a], p.T, nullptr) : a;
+        x.tokens = (p.cu ? clamp_row(p.cu[b], p.T, nullptr) : b) - x.t0;
+        x.key1 = y.len;
+        x.entry = y.entry;
+    } else {
+        const int n = i - p.P;
+        int least = 0;
+        x.entry = entry_of(p.slots, n, p.cache.num_slots, p.err, true);
+        if (p.P) {
+            int a = 0, b = p.P - 1;                      // the last group that starts at or before n
+            while (a < b) {
+                const int c = (a + b + 1) / 2;
+                if (group_start(p, c) <= n) a = c; else b = c - 1;
+            }
+            if (group_start(p, a) <= n && n < group_start(p, a + 1)) {
+                least = prefix_of(p, a, nullptr).len;
+                if (least) x.prefix = a;
+            }
+        }
+        if (x.entry >= 0) {
+            const RowsAt r = rows_at(p.cu, p.starts, p.cache, n, p.T, least, p.err);
+            x.t0 = r.bos;
+            x.tokens = min(r.len, capacity(p.cache) - r.start);
+            x.first = r.start;
+            x.key0 = least;
+            x.key1 = r.start + x.tokens;
+        }
+    }
+    x.kind = x.tokens <= 0 || x.key1 <= x.key0 ? kNoWork : (int64_t)x.tokens * p.G <= kFewRows ? kRowsWork : kTilesWork;
     return x;
 }
 

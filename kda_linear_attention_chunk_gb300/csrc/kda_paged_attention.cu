@@ -10,7 +10,6 @@
 // Four kernels: the plan (one CTA), the tiles and the rows kernel, and the join; each
 // is launched early (programmatic dependent launch) and waits for what it needs.
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "kda_paged_attend.cuh"
 
@@ -18,61 +17,6 @@ namespace kda {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-
-// the positions that group g shares, and whose pages they are in
-struct Prefix {
-    int len, entry;
-};
-__device__ __forceinline__ Prefix prefix_of(const AttendParams &p, int g, int *err)
-{
-    Prefix x;
-    x.entry = entry_of(p.prefix_slots, g, p.cache.num_slots, p.err, err != nullptr);
-    const int was = p.prefix_lens[g];
-    x.len = x.entry < 0 ? 0 : min(max(was, 0), capacity(p.cache));
-    if (err && x.entry >= 0 && x.len != was) atomicOr(err, kErrBadPosition);
-    return x;
-}
-__device__ __forceinline__ int group_start(const AttendParams &p, int g) { return min(max(p.groups[g], 0), p.N); }
-
-__device__ __forceinline__ Part make_part(const AttendParams &p, int i)
-{
-    Part x = {};
-    x.prefix = -1;
-    if (i < p.P) {
-        const int a = group_start(p, i), b = group_start(p, i + 1);
-        if (p.groups[i] != a || p.groups[i + 1] != b || a > b) atomicOr(p.err, kErrBadSeqlens);
-        const Prefix y = prefix_of(p, i, p.err);
-        x.t0 = p.cu ? clamp_row(p.cu[a], p.T, nullptr) : a;
-        x.tokens = (p.cu ? clamp_row(p.cu[b], p.T, nullptr) : b) - x.t0;
-        x.key1 = y.len;
-        x.entry = y.entry;
-    } else {
-        const int n = i - p.P;
-        int least = 0;
-        x.entry = entry_of(p.slots, n, p.cache.num_slots, p.err, true);
-        if (p.P) {
-            int a = 0, b = p.P - 1;                      // the last group that starts at or before n
-            while (a < b) {
-                const int c = (a + b + 1) / 2;
-                if (group_start(p, c) <= n) a = c; else b = c - 1;
-            }
-            if (group_start(p, a) <= n && n < group_start(p, a + 1)) {
-                least = prefix_of(p, a, nullptr).len;
-                if (least) x.prefix = a;
-            }
-        }
-        if (x.entry >= 0) {
-            const RowsAt r = rows_at(p.cu, p.starts, p.cache, n, p.T, least, p.err);
-            x.t0 = r.bos;
-            x.tokens = min(r.len, capacity(p.cache) - r.start);
-            x.first = r.start;
-            x.key0 = least;
-            x.key1 = r.start + x.tokens;
-        }
-    }
-    x.kind = x.tokens <= 0 || x.key1 <= x.key0 ? kNoWork : (int64_t)x.tokens * p.G <= p.few ? kRowsWork : kTilesWork;
-    return x;
-}
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ AttendParams p)
 {
@@ -83,11 +27,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     for (int base = 0; base < all; base += kPlanThreads) {
         const int i = base + tid;
         int64_t mine[2] = {0, 0};
+        Part x = {};
         if (i < all) {
-            const Part x = make_part(p, i);
-            int4 *to = reinterpret_cast<int4 *>(p.parts + i);
-            to[0] = make_int4(x.t0, x.tokens, x.first, x.key0);
-            to[1] = make_int4(x.key1, x.entry, x.prefix, x.kind);
+            x = make_part(p, i);
             if (x.kind == kTilesWork) mine[0] = part_tiles(x, i < p.P, 2 * p.tile_tokens);
             if (x.kind == kRowsWork) mine[1] = part_steps(x);
         }
@@ -112,17 +54,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             sums[warp][lane] = y;
         }
         __syncthreads();
+        int64_t before[2];
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-            int64_t *to = k ? p.steps : p.tiles;
-            if (i < all) to[i] = done[k] + upto[k] - mine[k] + (warp ? sums[k][warp - 1] : 0);
+            before[k] = done[k] + upto[k] - mine[k] + (warp ? sums[k][warp - 1] : 0);
             done[k] += sums[k][kPlanThreads / 32 - 1];
+        }
+        if (i < all) {
+            x.begin = before[x.kind == kRowsWork];
+            store_part(p.parts + i, x);
+            p.tiles[i] = before[0];
+            p.steps[i] = before[1];
         }
         __syncthreads();
     }
     if (tid == 0) {
-        p.tiles[all] = done[0];
-        p.steps[all] = done[1];
+        p.lines->total[0] = done[0];
+        p.lines->total[1] = done[1];
+        p.lines->share[0] = share_of(done[0], p.Hk, p.tile_workers, kLeastTiles);
+        p.lines->share[1] = share_of(done[1], p.Hk, p.row_workers, kLeastSteps);
     }
 }
 
@@ -142,16 +92,15 @@ struct Place {
     int row, rows;                   // the row's first query head in a piece; rows of a piece
     bool tiles, any;
 };
-__device__ __forceinline__ Place place_of(const AttendParams &p, int part, const Part &x, bool shared, int t)
+__device__ __forceinline__ Place place_of(const AttendParams &p, const Lines &lines, const Part &x, bool shared, int t)
 {
     Place r = {};
     r.any = x.kind != kNoWork;
     r.tiles = x.kind == kTilesWork;
+    r.total = lines.total[!r.tiles];
+    r.share = lines.share[!r.tiles];
+    r.begin = x.begin;
     const int i = t - x.t0, span = 2 * p.tile_tokens;
-    const int64_t *before = r.tiles ? p.tiles : p.steps;
-    r.total = __ldcg(before + p.P + p.N);
-    r.begin = __ldcg(before + part);
-    r.share = share_of(r.total, p.Hk, r.tiles ? p.tile_workers : p.row_workers, r.tiles ? kLeastTiles : kLeastSteps);
     if (r.tiles) {
         const int j = i / span, u = i - j * span, q = u >= p.tile_tokens;
         r.begin += tiles_before(x, shared, span, j);
@@ -196,10 +145,11 @@ __device__ __forceinline__ Pieces pieces_of(const AttendParams &p, const Place &
     return r;
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendParams p, int heads, int team)
+// kBatch: pieces at a time, more of them where there are few rows
+template <typename E, int D, int kBatch>
+__global__ void __launch_bounds__(kJoinThreads, 6 / kBatch) join_kernel(const __grid_constant__ AttendParams p, int heads, int team)
 {
-    constexpr int kVecs = D / 4 / kLanes, kBatch = 2;    // 16-byte vectors of a lane in a row; pieces at a time
+    constexpr int kVecs = D / 4 / kLanes;                // 16-byte vectors of a lane in a row
     __shared__ float4 os[kGroups][D / 4];
     __shared__ float ms[kGroups], ls[kGroups];
     __shared__ Place at[2];
@@ -209,11 +159,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     grid_wait();
     if (n < 0) return;
     const Part own = load_part(p.parts + p.P + n);
+    const Lines lines = load_lines(p.lines);
     if (own.kind == kNoWork || t - own.t0 >= own.tokens) return;
-    if (threadIdx.x == 0) at[0] = place_of(p, p.P + n, own, false, t);
+    if (threadIdx.x == 0) at[0] = place_of(p, lines, own, false, t);
     if (threadIdx.x == 32) {                             // (another warp, at the same time)
         at[1].any = false;
-        if (own.prefix >= 0) at[1] = place_of(p, own.prefix, load_part(p.parts + own.prefix), true, t);
+        if (own.prefix >= 0) at[1] = place_of(p, lines, load_part(p.parts + own.prefix), true, t);
     }
     __syncthreads();
     const int place = group % team, end = min(p.Hq, head0 + heads);
@@ -305,7 +256,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 // the workspace's pieces, each from a multiple of 256 bytes on
 struct Room {
-    int64_t parts, tiles, steps, whole[2], whole_ml[2], cut_tiles, cut_tiles_ml, cut_rows, cut_rows_ml, size;
+    int64_t parts, lines, tiles, steps, whole[2], whole_ml[2], cut_tiles, cut_tiles_ml, cut_rows, cut_rows_ml, size;
 };
 // no part has more rows than the call
 bool can_have_tiles(int T, int G) { return (int64_t)T * G > kFewRows; }
@@ -320,8 +271,9 @@ Room room_of(int N, int T, int P, int Hq, int Hk, int d)
     };
     const int64_t parts = (int64_t)P + N, heads = (int64_t)T * Hq;
     r.parts = take(parts * sizeof(Part));
-    r.tiles = take((parts + 1) * 8);
-    r.steps = take((parts + 1) * 8);
+    r.lines = take(sizeof(Lines));
+    r.tiles = take(parts * 8);
+    r.steps = take(parts * 8);
     for (int i = 0; i < 2; i++) {
         r.whole[i] = take(P ? heads * d * 4 : 0);
         r.whole_ml[i] = take(P ? heads * 8 : 0);
@@ -338,10 +290,13 @@ Room room_of(int N, int T, int P, int Hq, int Hk, int d)
 
 template <typename E, int D> cudaError_t launch_join(const PagedAttentionArgs &a, const AttendParams &p)
 {
-    // many rows: a group of lanes a head; few: a CTA a head, whose groups share the pieces
-    int heads = a.Hq < kGroups ? a.Hq : kGroups, team = 1;
-    while (heads > 1 && (int64_t)a.T * ((a.Hq + heads - 1) / heads) < 2 * a.num_sms) heads = (heads + 1) / 2;
-    while (heads * team * 2 <= kGroups) team *= 2;
+    // few rows: a CTA a head, whose groups share the pieces; more: as many heads a CTA as let
+    // all CTAs run at once, up to a group of lanes a head
+    int heads = 1, team = kGroups;
+    while (heads < a.Hq && team > 1 && (int64_t)a.T * ((a.Hq + heads - 1) / heads) > 3 * a.num_sms) {
+        heads *= 2;
+        team /= 2;
+    }
     const int64_t blocks = (int64_t)a.T * ((a.Hq + heads - 1) / heads);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
@@ -353,7 +308,7 @@ template <typename E, int D> cudaError_t launch_join(const PagedAttentionArgs &a
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<E, D>, p, heads, team);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, team < kGroups ? join_kernel<E, D, 2> : join_kernel<E, D, 4>, p, heads, team);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -374,6 +329,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a)
     const Room r = room_of(a.N, a.T, a.P, a.Hq, a.Hk, a.d);
     uint8_t *w = (uint8_t *)a.workspace;
     p.parts = (Part *)(w + r.parts);
+    p.lines = (Lines *)(w + r.lines);
     p.tiles = (int64_t *)(w + r.tiles);
     p.steps = (int64_t *)(w + r.steps);
     for (int i = 0; i < 2; i++) {
@@ -389,7 +345,6 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a)
     // many heads none for the rows kernel
     const bool tiles = can_have_tiles(a.T, p.G) && (a.cu_seqlens || a.P || p.G > kFewRows), rows = p.G <= kFewRows;
     p.after_tiles = tiles;
-    p.few = getenv("FEW") && tiles ? atoi(getenv("FEW")) : kFewRows;
     plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && tiles) e = launch_paged_tiles(a, p);

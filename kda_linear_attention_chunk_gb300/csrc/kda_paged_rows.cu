@@ -31,7 +31,8 @@ template <typename E, int D>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 paged_rows_kernel(const __grid_constant__ AttendParams p)
 {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+    // (a ring that starts inside a 128-byte line costs 20 %: each copied row then ends in another)
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     constexpr int kTile = kStepKeys * D * 2;             // bytes of a step's keys or values
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int64_t worker = (int64_t)blockIdx.x * kWarps + warp;
@@ -42,7 +43,8 @@ paged_rows_kernel(const __grid_constant__ AttendParams p)
     // The plan is complete: waited for here, or by the tiles kernel before it let this one start.
     if (!p.after_tiles) grid_wait();
     grid_go_on();
-    const int64_t total = __ldcg(p.steps + parts), share = share_of(total, p.Hk, p.row_workers, kLeastSteps);
+    const Lines lines = load_lines(p.lines);
+    const int64_t total = lines.total[1], share = lines.share[1];
     const int64_t from = worker * share, to = min(total * p.Hk, from + share);
     int64_t at = from;
     while (at < to) {
@@ -50,7 +52,7 @@ paged_rows_kernel(const __grid_constant__ AttendParams p)
         const int hk = (int)quotient(at, total), part = part_at(p.steps, parts, at - hk * total, lane);
         const bool shared = part < p.P;
         const Part x = load_part(p.parts + part);
-        const int64_t begin = hk * total + __ldcg(p.steps + part), end = begin + part_steps(x);
+        const int64_t begin = hk * total + x.begin, end = begin + part_steps(x);
         const int step0 = x.key0 / kStepKeys + (int)(at - begin);
         const int steps = (int)(min(end, to) - at);
         at += steps;

@@ -158,7 +158,8 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
     const uint32_t sq = x.base, skv = x.base + 2 * L::kTile;
     const int parts = p.P + p.N, span = 2 * p.tile_tokens, page = 1 << cache.page_log2;
     const int box = min(page, kTileKeys), outside = cache.num_pages * 2 * p.Hk;
-    const int64_t total = __ldcg(p.tiles + parts), share = share_of(total, p.Hk, p.tile_workers, kLeastTiles);
+    const Lines lines = load_lines(p.lines);
+    const int64_t total = lines.total[0], share = lines.share[0];
     const int64_t from = blockIdx.x * share, to = min(total * p.Hk, from + share);
     int64_t at = from;
     int it = 0, item = 0, qs[2] = {0, 0};                // tiles and query tiles loaded, items written
@@ -178,7 +179,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         const int hk = (int)quotient(at, total), part = part_at(p.tiles, parts, at - hk * total, x.lane);
         const bool shared = part < p.P;
         const Part y = load_part(p.parts + part);
-        int64_t begin = hk * total + __ldcg(p.tiles + part);
+        int64_t begin = hk * total + y.begin;
         const int j = span_at(y, shared, span, at - begin, x.lane);
         begin += tiles_before(y, shared, span, j);
         const int64_t stop = begin + span_tiles(y, shared, span, j);
