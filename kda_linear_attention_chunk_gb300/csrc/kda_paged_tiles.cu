@@ -10,7 +10,10 @@
 //     O += P V             (P from TMEM in place of S, V MN-major as loaded)
 //
 // The two query tiles take turns on the tensor core: while one's scores are exponentiated,
-// the other's products run.  The maximum m only follows the true one when it falls behind by
+// the other's products run.  Where a span is only one query tile (a small group's prefix, drafts),
+// the key tiles are dealt to the two pipelines instead, each with a maximum, sum and O of its
+// own, and the first joins them: a tile's chain of products and exponentials, 1.9 us, would
+// be longer than its way from HBM, 1.5.  The maximum m only follows the true one when it falls behind by
 // more than 2^8, so O is rarely rescaled, and the threads that own the rows do it.
 //
 // One CTA an SM takes an equal share of the line of all tiles, so a long prefix is spread
@@ -43,7 +46,8 @@ using namespace tiles;
 
 constexpr int kThreads = 384;
 constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
-constexpr int kBars = 3 * kStages + 22;
+constexpr int kAhead = 2;            // tiles that are on their way into L2 before a stage of the ring is free for them
+constexpr int kBars = 3 * kStages + 23;
 constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
@@ -56,15 +60,19 @@ constexpr float kLag = 8.f;          // log2 of what the running maximum may lag
 struct Item {
     int tokens;                      // rows of the span; 0: there are no more items
     int t0, first;                   // its first row and that row's position
-    int hk, shared;
+    int hk, shared, entry;
     int tile0, tiles;                // key tiles
     int key0, end;                   // visible positions: key0 .. end - 1, and up to the row's own (not shared)
     int where;                       // goes_to(), and the first row of a cut piece
     int64_t cut;
+    // One query tile only: its key tiles are dealt to both pipelines, the odd ones to the second,
+    // which are joined in the end.
+    __device__ bool dealt(int tile_tokens) const { return tokens <= tile_tokens && tiles > 1; }
 };
 
 struct Ctl {
     Item items[2];
+    float2 odd_ml[kTileRows];        // maxima and sums over the odd key tiles (Item::dealt)
     int abort;
     uint32_t tmem;
     uint64_t bars[kBars];
@@ -100,6 +108,7 @@ struct Bars {
     __device__ uint32_t drained(int q) const { return at + 8 * (3 * kStages + 16 + q); }
     __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kStages + 18 + i); }
     __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kStages + 20 + i); }
+    __device__ uint32_t odd_done() const { return at + 8 * (3 * kStages + 22); }    // a dealt item's odd tiles are
 };
 constexpr int kItemReaders = 8 + 2 + 1;   // softmax warps, product warps, patch warp
 
@@ -192,6 +201,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             now.first = shared ? 0 : y.first + j * span;
             now.hk = hk;
             now.shared = shared;
+            now.entry = y.entry;
             now.tile0 = tile0;
             now.tiles = n;
             now.key0 = y.key0;
@@ -203,17 +213,24 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         __syncwarp();
         const int seen[2] = {Span(now, p.tile_tokens, 0).seen, Span(now, p.tile_tokens, 1).seen};
         const int32_t *table = cache.table + (int64_t)y.entry * cache.max_pages;
-        int ids_from = 0, ids = 0;                       // 32 entries of the page table, a lane each
-        bool have_ids = false, queries = false;
+        // A lane has a box of its own: 64 columns of page rows box lb of a tile.  It loads the entry of
+        // the page table one tile ahead.  (One lane for all, as the products have it, took 0.2 us a box,
+        // 3 us a tile of small pages.)
+        const int lb = x.lane / (D / 64), lh = x.lane % (D / 64);
+        auto entry_at = [&](int tile) {
+            const int j = (tile * kTileKeys + lb * box) >> cache.page_log2;
+            return lb * box < kTileKeys && j < cache.max_pages ? __ldg(table + j) : -1;
+        };
+        int id = entry_at(tile0);
+        bool queries = false;
 #pragma unroll 1
         for (int i = 0; i < n && ok; i++) {
-            const int pos = (tile0 + i) * kTileKeys, boxes = (tile_keys(end, tile0 + i) + box - 1) / box;
-            const int j0 = pos >> cache.page_log2, j1 = (pos + (boxes - 1) * box) >> cache.page_log2;
-            if (!have_ids || j1 >= ids_from + 32) {
-                have_ids = true;
-                ids_from = j0;
-                ids = j0 + x.lane < cache.max_pages ? __ldg(table + j0 + x.lane) : -1;
-            }
+            const int pos = (tile0 + i) * kTileKeys, at_b = pos + lb * box;
+            const int boxes = (tile_keys(end, tile0 + i) + box - 1) / box;
+            const bool mine = lb < boxes, needed = mine && at_b + box > y.key0, there = id >= 0 && id < cache.num_pages;
+            if (needed && !there && lh == 0) atomicOr(p.err, kErrBadPage);
+            const int c1 = at_b & (page - 1), c2 = needed && there ? id * 2 * p.Hk + hk : outside;
+            if (i + 1 < n) id = entry_at(tile0 + i + 1);
 #pragma unroll 1
             for (int kv = 0; kv < 2; kv++) {
                 const int s = it % kStages;
@@ -222,20 +239,10 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                 const uint32_t bar = x.bars.full(s), dst = skv + s * L::kTile;
                 if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * (D / 64)));
                 __syncwarp();
-#pragma unroll 1
-                for (int b = 0; b < boxes; b++) {
-                    const int at_b = pos + b * box;
-                    const int id = __shfl_sync(0xffffffffu, ids, (at_b >> cache.page_log2) - ids_from);
-                    const bool there = id >= 0 && id < cache.num_pages, needed = at_b + box > y.key0;
-                    if (elect_one()) {
-                        if (needed && !there && kv == 0) atomicOr(p.err, kErrBadPage);
-                        const int c2 = needed && there ? (id * 2 + kv) * p.Hk + hk : outside;
-#pragma unroll 1
-                        for (int h = 0; h < D / 64; h++)
-                            tma_load_3d(dst + h * L::kHalf + b * box * 128, &maps.pages, 64 * h, at_b & (page - 1), c2, bar);
-                    }
-                    __syncwarp();
-                }
+                if (mine)
+                    tma_load_3d(dst + lh * L::kHalf + lb * box * 128, &maps.pages, 64 * lh, c1,
+                                c2 == outside ? outside : c2 + kv * p.Hk, bar);
+                __syncwarp();
                 it++;
                 if (queries) continue;
                 queries = true;                          // after the first keys, which need not wait for their room
@@ -281,71 +288,120 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
     const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
     const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q;
     const uint32_t qs = x.base + q * L::kTile, skv = x.base + 2 * L::kTile;
-    int it = 0, parts = 0, turns = 0, mine = 0;          // tiles consumed; products P V issued; turns taken; items with rows
+    // tiles consumed; products P V issued; turns taken; items with rows; query tiles used
+    int it = 0, parts = 0, turns = 0, mine = 0, queries[2] = {0, 0};
     bool ok = true;
     for (int item = 0; ok; item++) {
         const Item &now = x.c.items[item & 1];
         ok = x.wait(x.bars.item_full(item & 1), item / 2);
         const int tokens = __shfl_sync(0xffffffffu, now.tokens, 0);
         if (!ok || tokens == 0) break;
-        const int seen = __shfl_sync(0xffffffffu, Span(now, p.tile_tokens, q).seen, 0);
+        const bool both = tokens > p.tile_tokens, dealt = __shfl_sync(0xffffffffu, now.dealt(p.tile_tokens), 0);
+        const int seen = __shfl_sync(0xffffffffu, Span(now, p.tile_tokens, dealt ? 0 : q).seen, 0);
+        const int seen0 = __shfl_sync(0xffffffffu, Span(now, p.tile_tokens, 0).seen, 0);
         const int n = __shfl_sync(0xffffffffu, now.tiles, 0), tile0 = __shfl_sync(0xffffffffu, now.tile0, 0);
         const int end = __shfl_sync(0xffffffffu, now.end, 0);
-        const bool both = tokens > p.tile_tokens, any = seen > 0;
-        int keys = tile_keys(end, tile0);
-        ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), mine));
-        if (elect_one()) {
-            if (ok && any) {
-                mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc(keys, 0, L::kF16));
-                mma_commit(x.bars.s_full(q));
-            }
-            mma_commit(x.bars.empty(it % kStages));
-        }
-        __syncwarp();
-        it++;
-        for (int i = 0; i < n && ok; i++) {
-            const int sv = it % kStages, steps = keys / 16;       // this tile's values
-            ok = x.wait(x.bars.values(sv), it / kStages);
-            it++;
-            const int sk = it % kStages;                 // the next tile's keys
-            const bool have = i + 1 < n;
-            if (have) {
-                keys = tile_keys(end, tile0 + i + 1);
-                ok = ok && x.wait(x.bars.full(sk), it / kStages);
-                it++;
-            } else if (any && elect_one()) {
-                mma_commit(x.bars.q_empty(q));           // every product with the query tile is issued
-            }
-            __syncwarp();
-            if (both && ok && (q || turns)) ok = x.wait(x.bars.turn(q), q ? turns : turns - 1);
-            if (ok && i < seen) {
-                if (i == 0 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
+        const bool any = seen > 0;
+        if (dealt) {
+            ok = x.wait(x.bars.q_full(0), queries[0]);
+#pragma unroll 1
+            for (int i = 0; i < n && ok; i++) {
+                const int sk = it % kStages, sv = (it + 1) % kStages, phase = it / kStages, phase_v = (it + 1) / kStages;
+                it += 2;
+                ok = x.wait(x.bars.full(sk), phase);
+                if ((i & 1) != q) {                      // the other pipeline's: no phase of a barrier is left out,
+                    ok = ok && x.wait(x.bars.values(sv), phase_v);   // or the next wait could take an older one for its own
+                    continue;
+                }
+                const int keys = tile_keys(end, tile0 + i);
+                const bool last = i + 2 >= n;
+                if (ok && elect_one()) {
+                    mma_scores<D>(ts, x.base, skv + sk * L::kTile, idesc(keys, 0, L::kF16));
+                    mma_commit(x.bars.s_full(q));
+                    mma_commit(x.bars.empty(sk));        // for both pipelines
+                    mma_commit(x.bars.empty(sk));
+                    if (last) mma_commit(x.bars.q_empty(0));
+                }
+                __syncwarp();
+                ok = ok && x.wait(x.bars.values(sv), phase_v);
+                if (ok && i < 2 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
                 ok = ok && x.wait(x.bars.p_half(q), parts);
                 if (ok) {
                     tc_fence_after();
-                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 0, steps, i > 0);
+                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 0, keys / 16, i > 1);
                     ok = x.wait(x.bars.p_ready(q), parts);
                 }
                 if (ok) {
                     tc_fence_after();
-                    if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 4, steps, true);
+                    if (elect_one()) {
+                        mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 4, keys / 16, true);
+                        mma_commit(x.bars.empty(sv));
+                        mma_commit(x.bars.empty(sv));
+                        if (last) mma_commit(x.bars.o_done(q));
+                    }
                     parts++;
                 }
+                __syncwarp();
             }
+        } else {
+            int keys = tile_keys(end, tile0);
+            ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), queries[q]));
             if (elect_one()) {
-                if (ok && have && i + 1 < seen) {
-                    mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc(keys, 0, L::kF16));
+                if (ok && any) {
+                    mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc(keys, 0, L::kF16));
                     mma_commit(x.bars.s_full(q));
                 }
-                if (both) mbar_arrive(x.bars.turn(!q));
-                mma_commit(x.bars.empty(sv));
-                if (have) mma_commit(x.bars.empty(sk));
-                else if (any) mma_commit(x.bars.o_done(q));
+                mma_commit(x.bars.empty(it % kStages));
             }
             __syncwarp();
-            if (both) turns++;
+            it++;
+            for (int i = 0; i < n && ok; i++) {
+                const int sv = it % kStages, steps = keys / 16;   // this tile's values
+                ok = x.wait(x.bars.values(sv), it / kStages);
+                it++;
+                const int sk = it % kStages;             // the next tile's keys
+                const bool have = i + 1 < n;
+                if (have) {
+                    keys = tile_keys(end, tile0 + i + 1);
+                    ok = ok && x.wait(x.bars.full(sk), it / kStages);
+                    it++;
+                } else if (any && elect_one()) {
+                    mma_commit(x.bars.q_empty(q));       // every product with the query tile is issued
+                    mma_commit(x.bars.q_empty(q));       // (two, as of a dealt item's pipelines)
+                }
+                __syncwarp();
+                if (both && ok && (q || turns)) ok = x.wait(x.bars.turn(q), q ? turns : turns - 1);
+                if (ok && i < seen) {
+                    if (i == 0 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
+                    ok = ok && x.wait(x.bars.p_half(q), parts);
+                    if (ok) {
+                        tc_fence_after();
+                        if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 0, steps, i > 0);
+                        ok = x.wait(x.bars.p_ready(q), parts);
+                    }
+                    if (ok) {
+                        tc_fence_after();
+                        if (elect_one()) mma_values<D>(to, ts, skv + sv * L::kTile, idesc(D, 1, L::kF16), 4, steps, true);
+                        parts++;
+                    }
+                }
+                if (elect_one()) {
+                    if (ok && have && i + 1 < seen) {
+                        mma_scores<D>(ts, qs, skv + sk * L::kTile, idesc(keys, 0, L::kF16));
+                        mma_commit(x.bars.s_full(q));
+                    }
+                    if (both) mbar_arrive(x.bars.turn(!q));
+                    mma_commit(x.bars.empty(sv));
+                    if (have) mma_commit(x.bars.empty(sk));
+                    else if (any) mma_commit(x.bars.o_done(q));
+                }
+                __syncwarp();
+                if (both) turns++;
+            }
         }
         if (any) mine++;
+        if (seen0) queries[0]++;
+        if (q && any && !dealt) queries[1]++;
         __syncwarp();
         if (x.lane == 0) mbar_arrive(x.bars.item_empty(item & 1));
     }
@@ -362,14 +418,28 @@ template <typename E, int D>
 __device__ __forceinline__ void patch_role(const Ctx &x)
 {
     using L = Layout<E, D>;
+    const PagedCache &cache = x.p.cache;
+    const int page = 1 << cache.page_log2, box = min(page, kTileKeys);
     bool ok = true;
     for (int item = 0, it = 1; ok; item++) {
         const Item &now = x.c.items[item & 1];
         ok = x.wait(x.bars.item_full(item & 1), item / 2);
         if (!ok || now.tokens == 0) break;
         const int n = now.tiles;
+        const int32_t *table = cache.table + (int64_t)now.entry * cache.max_pages;
         for (int i = 0; i < n && ok; i++, it += 2) {
             const int s = it % kStages;
+            if (kAhead && i + kAhead < n) {              // on its way into L2
+                const int t = now.tile0 + i + kAhead, b = x.lane >> 1, at_b = t * kTileKeys + b * box, kv = x.lane & 1;
+                if (b < (tile_keys(now.end, t) + box - 1) / box) {
+                    const int id = __ldg(table + (at_b >> cache.page_log2));
+                    if (id >= 0 && id < cache.num_pages)
+                        prefetch_l2(cache.pages + (((int64_t)id * 2 + kv) * x.p.Hk + now.hk) * ((int64_t)D << cache.page_log2) +
+                                        (int64_t)(at_b & (page - 1)) * D,
+                                    (uint32_t)box * D * 2);
+                }
+                __syncwarp();
+            }
             ok = x.wait(x.bars.full(s), it / kStages);
             if (!ok) break;
             const int pos = (now.tile0 + i) * kTileKeys, keys = tile_keys(now.end, now.tile0 + i);
@@ -404,22 +474,24 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
     const uint32_t ts = lanes + kTmS + 128 * q, to = lanes + kTmO + 128 * q;
     const float c2 = p.scale_log2;
     uint8_t *stage = x.smem + L::kOut + warp * kStage;
-    int it = 0, mine = 0;                                // score tiles, items with rows
+    int it = 0, mine = 0, joined = 0;                    // score tiles, items with rows, dealt ones
     bool ok = true;
     for (int item = 0; ok; item++) {
         const Item &now = x.c.items[item & 1];
         ok = x.wait(x.bars.item_full(item & 1), item / 2);
         if (!ok || now.tokens == 0) break;
-        const Span rows(now, p.tile_tokens, q);
+        const bool dealt = now.dealt(p.tile_tokens);
+        const int qt = dealt ? 0 : q;                    // whose rows these are
+        const Span rows(now, p.tile_tokens, qt);
         const bool dead = 32 * (warp & 3) >= rows.tokens * p.G;      // no row of this warp is one: O may be anything
-        const int key0 = now.key0, tile0 = now.tile0, t0 = now.t0 + q * p.tile_tokens, hk = now.hk, where = now.where;
-        const int64_t cut = now.cut + q * kTileRows;
+        const int key0 = now.key0, tile0 = now.tile0, t0 = now.t0 + qt * p.tile_tokens, hk = now.hk, where = now.where;
+        const int64_t cut = now.cut + qt * kTileRows;
         // behind the last key that this row sees, and that the warp's first row does
         const int see = now.shared ? now.end : min(now.end, rows.first + token + 1);
         const int least = now.shared ? now.end : min(now.end, rows.first + (32 * (warp & 3) * p.inv_G >> 16) + 1);
         float m = -INFINITY, sum = 0.f;
         const int end = now.end;
-        for (int i = 0; i < rows.seen; i++) {
+        for (int i = dealt ? q : 0; i < rows.seen; i += dealt ? 2 : 1) {
             const int pos = (tile0 + i) * kTileKeys, keys = tile_keys(end, tile0 + i);
             // every key of the tile visible to every row of the warp: no test per key
             const bool whole = pos >= key0 && pos + kTileKeys <= least;
@@ -516,16 +588,61 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         if (!ok || !rows.tokens) continue;
         const int live = rows.tokens * p.G - 32 * (warp & 3);        // of this warp's rows
         const int64_t dense = (int64_t)t0 * p.Hq + hk * p.G;         // row of [T][Hq] of the tile's first row
+        if (rows.seen) {
+            ok = x.wait(x.bars.o_done(q), mine);
+            if (!ok) break;
+            tc_fence_after();
+            mine++;
+        }
+        float f0 = 1.f, f1 = 0.f;                        // what O, and that of the odd tiles, is multiplied by
+        if (dealt) {
+            if (q) {
+                x.c.odd_ml[row] = make_float2(m, sum);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x.bars.odd_done());
+                continue;
+            }
+            ok = x.wait(x.bars.odd_done(), joined++);
+            if (!ok) break;
+            tc_fence_after();
+            const float2 odd = x.c.odd_ml[row];
+            const float top = fmaxf(m, odd.x);
+            f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2);
+            f1 = odd.x == -INFINITY ? 0.f : ex2((odd.x - top) * c2);
+            sum = sum * f0 + odd.y * f1;
+            m = top;
+        }
         if (where != kToOut && lane < live) {            // the row's maximum (or what stands for it) and sum
             float2 *ml = where == kToCut ? p.cut_tiles_ml + cut + row
                                          : p.whole_ml[where == kToPrefix] + dense + token * (p.Hq - p.G) + row;
             *ml = make_float2(m, sum);
         }
         if (!rows.seen) continue;                        // nothing visible in this piece: no O
-        ok = x.wait(x.bars.o_done(q), mine);
-        if (!ok) break;
-        tc_fence_after();
-        mine++;
+        // 32 columns of O, multiplied by f; after the last ones it is free for the next item
+        auto load_o = [&](int h, float f, uint32_t (&o)[32]) {
+            tmem_ld32(to + 32 * h, o);
+            tmem_wait_ld();
+            if (dealt) {
+                uint32_t odd[32];
+                tmem_ld32(to + 128 + 32 * h, odd);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; j++)
+                    o[j] = __float_as_uint(fmaf(__uint_as_float(odd[j]), f1 * f, __uint_as_float(o[j]) * (f0 * f)));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            }
+            if (h == D / 32 - 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(x.bars.o_free(q));
+                    if (dealt) mbar_arrive(x.bars.o_free(1));
+                }
+            }
+        };
         if (where != kToOut) {
             // O in fp32, 32 columns at a time through shared memory, so that a store
             // instruction writes four rows of 128 bytes
@@ -534,13 +651,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
 #pragma unroll 1
             for (int h = 0; h < D / 32; h++) {
                 uint32_t o[32];
-                tmem_ld32(to + 32 * h, o);
-                tmem_wait_ld();
-                if (h == D / 32 - 1) {                   // O is free for the next item
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(x.bars.o_free(q));
-                }
+                load_o(h, 1.f, o);
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
@@ -561,24 +672,19 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         uint16_t *out = p.out + dense * D + 8 * (lane & 7);
 #pragma unroll 1
         for (int h = 0; h < D / 64; h++) {
-            uint32_t o[2][32];
-            tmem_ld32(to + 64 * h, o[0]);
-            tmem_ld32(to + 64 * h + 32, o[1]);
-            tmem_wait_ld();
-            if (h == D / 64 - 1) {                       // O is free for the next item
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(x.bars.o_free(q));
-            }
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const uint32_t *v = &o[j / 4][8 * (j & 3)];
-                uint4 r;
-                r.x = Half2<E>::pack(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
-                r.y = Half2<E>::pack(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
-                r.z = Half2<E>::pack(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
-                r.w = Half2<E>::pack(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
-                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = r;
+            for (int k = 0; k < 2; k++) {
+                uint32_t o[32];
+                load_o(2 * h + k, inv, o);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    uint4 r;
+                    r.x = Half2<E>::pack(__uint_as_float(o[8 * j]), __uint_as_float(o[8 * j + 1]));
+                    r.y = Half2<E>::pack(__uint_as_float(o[8 * j + 2]), __uint_as_float(o[8 * j + 3]));
+                    r.z = Half2<E>::pack(__uint_as_float(o[8 * j + 4]), __uint_as_float(o[8 * j + 5]));
+                    r.w = Half2<E>::pack(__uint_as_float(o[8 * j + 6]), __uint_as_float(o[8 * j + 7]));
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * k + j) ^ (lane & 7)) << 4)) = r;
+                }
             }
             __syncwarp();
 #pragma unroll
@@ -613,7 +719,7 @@ paged_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ At
         }
         for (int q = 0; q < 2; q++) {
             mbar_init(bars.q_full(q), 1);
-            mbar_init(bars.q_empty(q), 1);
+            mbar_init(bars.q_empty(q), 2);
             mbar_init(bars.s_full(q), 1);
             mbar_init(bars.p_half(q), 4);
             mbar_init(bars.p_ready(q), 4);
@@ -624,6 +730,7 @@ paged_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ At
             mbar_init(bars.item_full(q), 1);
             mbar_init(bars.item_empty(q), kItemReaders);
         }
+        mbar_init(bars.odd_done(), 4);
         mbar_fence_init();
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.pages);
