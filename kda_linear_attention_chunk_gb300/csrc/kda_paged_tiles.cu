@@ -65,14 +65,16 @@ struct Item {
     int key0, end;                   // visible positions: key0 .. end - 1, and up to the row's own (not shared)
     int where;                       // goes_to(), and the first row of a cut piece
     int64_t cut;
-    // One query tile only: its key tiles are dealt to both pipelines, the odd ones to the second,
-    // which are joined in the end.
+    // One query tile only: its key tiles are dealt to both pipelines, which are joined in the end.
+    // Pipeline q takes the tiles in the q-th half of the ring, so that it sees every phase of its
+    // barriers there, and need not see the others'.
+    int turn;                        // the half with the item's first tile
     __device__ bool dealt(int tile_tokens) const { return tokens <= tile_tokens && tiles > 1; }
 };
 
 struct Ctl {
     Item items[2];
-    float2 odd_ml[kTileRows];        // maxima and sums over the odd key tiles (Item::dealt)
+    float2 other_ml[kTileRows];      // maxima and sums over the second pipeline's tiles of a dealt item
     int abort;
     uint32_t tmem;
     uint64_t bars[kBars];
@@ -108,7 +110,7 @@ struct Bars {
     __device__ uint32_t drained(int q) const { return at + 8 * (3 * kStages + 16 + q); }
     __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kStages + 18 + i); }
     __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kStages + 20 + i); }
-    __device__ uint32_t odd_done() const { return at + 8 * (3 * kStages + 22); }    // a dealt item's odd tiles are
+    __device__ uint32_t other_done() const { return at + 8 * (3 * kStages + 22); }    // a dealt item's second pipeline is
 };
 constexpr int kItemReaders = 8 + 2 + 1;   // softmax warps, product warps, patch warp
 
@@ -206,6 +208,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             now.tiles = n;
             now.key0 = y.key0;
             now.end = end;
+            now.turn = it / 2 & 1;
             now.where = goes_to(y, shared, begin, stop, from, to);
             now.cut = cut_piece(blockIdx.x, begin, from) * kPieceRows;
             mbar_arrive(x.bars.item_full(item & 1));
@@ -263,6 +266,10 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                 }
             }
         }
+        // The first keys of the next item may be for a pipeline that did not see the tile before them in
+        // their room (as of values, the patch warp takes those one after the other).
+        if (n > 1 && !seen[1])
+            for (int i = it - 4; i < it && ok; i += 2) ok = x.wait(x.bars.full(i % kStages), i / kStages);
         if (!ok) break;
     }
     if (!ok && x.lane == 0) x.give_up();
@@ -305,14 +312,9 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
         if (dealt) {
             ok = x.wait(x.bars.q_full(0), queries[0]);
 #pragma unroll 1
-            for (int i = 0; i < n && ok; i++) {
-                const int sk = it % kStages, sv = (it + 1) % kStages, phase = it / kStages, phase_v = (it + 1) / kStages;
-                it += 2;
+            for (int i = (q + __shfl_sync(0xffffffffu, now.turn, 0)) & 1; i < n && ok; i += 2) {
+                const int g = it + 2 * i, sk = g % kStages, sv = (g + 1) % kStages, phase = g / kStages;
                 ok = x.wait(x.bars.full(sk), phase);
-                if ((i & 1) != q) {                      // the other pipeline's: no phase of a barrier is left out,
-                    ok = ok && x.wait(x.bars.values(sv), phase_v);   // or the next wait could take an older one for its own
-                    continue;
-                }
                 const int keys = tile_keys(end, tile0 + i);
                 const bool last = i + 2 >= n;
                 if (ok && elect_one()) {
@@ -323,7 +325,7 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
                     if (last) mma_commit(x.bars.q_empty(0));
                 }
                 __syncwarp();
-                ok = ok && x.wait(x.bars.values(sv), phase_v);
+                ok = ok && x.wait(x.bars.values(sv), phase);
                 if (ok && i < 2 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
                 ok = ok && x.wait(x.bars.p_half(q), parts);
                 if (ok) {
@@ -343,6 +345,7 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
                 }
                 __syncwarp();
             }
+            it += 2 * n;
         } else {
             int keys = tile_keys(end, tile0);
             ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), queries[q]));
@@ -481,7 +484,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         ok = x.wait(x.bars.item_full(item & 1), item / 2);
         if (!ok || now.tokens == 0) break;
         const bool dealt = now.dealt(p.tile_tokens);
-        const int qt = dealt ? 0 : q;                    // whose rows these are
+        const int qt = dealt ? 0 : q, now_turn = now.turn;           // whose rows these are
         const Span rows(now, p.tile_tokens, qt);
         const bool dead = 32 * (warp & 3) >= rows.tokens * p.G;      // no row of this warp is one: O may be anything
         const int key0 = now.key0, tile0 = now.tile0, t0 = now.t0 + qt * p.tile_tokens, hk = now.hk, where = now.where;
@@ -491,7 +494,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
         const int least = now.shared ? now.end : min(now.end, rows.first + (32 * (warp & 3) * p.inv_G >> 16) + 1);
         float m = -INFINITY, sum = 0.f;
         const int end = now.end;
-        for (int i = dealt ? q : 0; i < rows.seen; i += dealt ? 2 : 1) {
+        for (int i = dealt ? (q + now_turn) & 1 : 0; i < rows.seen; i += dealt ? 2 : 1) {
             const int pos = (tile0 + i) * kTileKeys, keys = tile_keys(end, tile0 + i);
             // every key of the tile visible to every row of the warp: no test per key
             const bool whole = pos >= key0 && pos + kTileKeys <= least;
@@ -594,23 +597,23 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             tc_fence_after();
             mine++;
         }
-        float f0 = 1.f, f1 = 0.f;                        // what O, and that of the odd tiles, is multiplied by
+        float f0 = 1.f, f1 = 0.f;                        // what O, and that of the second pipeline, is multiplied by
         if (dealt) {
             if (q) {
-                x.c.odd_ml[row] = make_float2(m, sum);
+                x.c.other_ml[row] = make_float2(m, sum);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(x.bars.odd_done());
+                if (lane == 0) mbar_arrive(x.bars.other_done());
                 continue;
             }
-            ok = x.wait(x.bars.odd_done(), joined++);
+            ok = x.wait(x.bars.other_done(), joined++);
             if (!ok) break;
             tc_fence_after();
-            const float2 odd = x.c.odd_ml[row];
-            const float top = fmaxf(m, odd.x);
+            const float2 other = x.c.other_ml[row];
+            const float top = fmaxf(m, other.x);
             f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2);
-            f1 = odd.x == -INFINITY ? 0.f : ex2((odd.x - top) * c2);
-            sum = sum * f0 + odd.y * f1;
+            f1 = other.x == -INFINITY ? 0.f : ex2((other.x - top) * c2);
+            sum = sum * f0 + other.y * f1;
             m = top;
         }
         if (where != kToOut && lane < live) {            // the row's maximum (or what stands for it) and sum
@@ -624,12 +627,12 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             tmem_ld32(to + 32 * h, o);
             tmem_wait_ld();
             if (dealt) {
-                uint32_t odd[32];
-                tmem_ld32(to + 128 + 32 * h, odd);
+                uint32_t other[32];
+                tmem_ld32(to + 128 + 32 * h, other);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; j++)
-                    o[j] = __float_as_uint(fmaf(__uint_as_float(odd[j]), f1 * f, __uint_as_float(o[j]) * (f0 * f)));
+                    o[j] = __float_as_uint(fmaf(__uint_as_float(other[j]), f1 * f, __uint_as_float(o[j]) * (f0 * f)));
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
@@ -730,7 +733,7 @@ paged_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ At
             mbar_init(bars.item_full(q), 1);
             mbar_init(bars.item_empty(q), kItemReaders);
         }
-        mbar_init(bars.odd_done(), 4);
+        mbar_init(bars.other_done(), 4);
         mbar_fence_init();
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.pages);
