@@ -57,7 +57,7 @@ __device__ __forceinline__ RowsAt rows_at(const int32_t *cu, const int32_t *star
     r.len = cu ? max(0, clamp_row(__ldg(cu + n + 1), T, err) - r.bos) : 1;
     const int was = starts ? __ldg(starts + n) : 0;
     r.start = max(least, min(was, capacity(c) - min(r.len, capacity(c))));
-    if (err && (r.start != was || r.len > capacity(c) - r.start)) atomicOr(err, kErrBadPosition);
+    if (err && r.len && (r.start != was || r.len > capacity(c) - r.start)) atomicOr(err, kErrBadPosition);
     return r;
 }
 

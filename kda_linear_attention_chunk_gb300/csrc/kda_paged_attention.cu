@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6 / kBatch) join_kernel(const __
 struct Room {
     int64_t parts, lines, tiles, steps, whole[2], whole_ml[2], cut_tiles, cut_tiles_ml, cut_rows, cut_rows_ml, size;
 };
+constexpr int kMostSequences = 1 << 24;
 // no part has more rows than the call
 bool can_have_tiles(int T, int G) { return (int64_t)T * G > kFewRows; }
 Room room_of(int N, int T, int P, int Hq, int Hk, int d)
@@ -314,7 +315,11 @@ template <typename E, int D> cudaError_t launch_join(const PagedAttentionArgs &a
 
 }  // namespace
 
-int64_t paged_attention_workspace(int N, int T, int P, int Hq, int Hk, int d) { return room_of(N, T, P, Hq, Hk, d).size; }
+int64_t paged_attention_workspace(int N, int T, int P, int Hq, int Hk, int d)
+{
+    if (N > kMostSequences || P > kMostSequences) return -1;
+    return room_of(N, T, P, Hq, Hk, d).size;
+}
 
 cudaError_t launch_paged_attention(const PagedAttentionArgs &a)
 {

@@ -69,7 +69,7 @@ def check(logits, scores, ended=None, end=-1, slots=None, **kw):
     s = got[0].double().cpu().numpy()
     assert np.array_equal(s == -math.inf, best == -math.inf)
     live = best > -math.inf
-    assert (np.abs(s - best)[live] <= 2.0 ** -18 + 2.0 ** -24 * np.abs(best[live])).all()
+    assert (np.abs(s[live] - best[live]) <= 2.0 ** -18 + 2.0 ** -24 * np.abs(best[live])).all()
     names = ["parent", "token", "ended", "new", "src", "dst"]
     for name, x in zip(names, got[1:]):
         if x is None:

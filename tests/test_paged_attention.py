@@ -305,3 +305,33 @@ def test_replayed_graphs():
             t.cuda.synchronize()
             x.check(out)
     assert torch_dtype("bf16") is b.q.dtype
+
+
+def test_rows_past_the_tables_end_are_left_as_they_were():
+    """More rows than the table has positions for: those that fit are answered."""
+    b = Batch([(0, 200)], page=64, seed=14, extra=0)
+    t = b.t
+    table = b.table[:, :2].contiguous()
+    out = t.full_like(b.q, 6.0)
+    b.call(page_table=table, out=out)
+    assert kda.device_error(reset=True) == kda.ERR_BAD_POSITION
+    ref, bound = b.want(0)
+    assert ((out[:128].double() - ref[:128]).abs() <= bound[:128]).all() and (out[128:] == 6).all()
+
+
+def test_an_empty_sequence_in_a_group_may_start_anywhere():
+    b = Batch([(5, 2), (0, 0), (3, 1)], [(3, 100)], seed=15)
+    starts = b.starts.clone()
+    starts[1] = 0
+    b.check(b.call(starts=starts))
+    assert kda.device_error(reset=True) == 0
+
+
+def test_infinite_scores_are_masked():
+    """Keys that no row sees yet hold values whose scores would be infinite; rows that do see one have no finite answer."""
+    b = Batch([(70, 20), (40, 1)], seed=16, dtype="fp16")
+    t, want = b.t, b.call()
+    p, r = b.places(b.ids[0], 85, 90)
+    b.pool[p, 0, :, r] = -math.inf
+    got = b.call()
+    assert t.equal(got[:15], want[:15]) and t.equal(got[20:], want[20:])
