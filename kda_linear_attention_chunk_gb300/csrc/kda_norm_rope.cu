@@ -49,32 +49,110 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p)
     if (which) chunk -= p.chunks[0];
     const int c = lane % kLanes, heads = p.heads[which];
     const int head0 = chunk * kPer * kUnroll + lane / kLanes;
-    Turn<E, D, HALF, FULL> turn(c, p.rotary);
+    const int half = FULL ? D / 2 : p.rotary / 2;
+    const bool turns = FULL || 4 * c < half;             // this lane's pairs
+    // elements ea .. ea + 3 and eb .. eb + 3 of a head
+    const int ea = HALF && turns ? 4 * c : 8 * c, eb = HALF && turns ? 4 * c + half : 8 * c + 4;
 
     const uint16_t *x = p.x[which] + t * p.stride[which];
     uint2 raw[kUnroll][2];
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
         const int h = head0 + u * kPer;
-        if (h < heads) turn.load(x + (int64_t)h * D, raw[u]);
-        else raw[u][0] = raw[u][1] = make_uint2(0, 0);
-    }
-    const float *row = nullptr;
-    if (turn.turns && turn.half) {
-        int pos = __ldg(p.positions + t);
-        if (pos < 0 || pos >= p.max_pos) {
-            if (lane == 0) atomicOr(p.err, kErrBadPosition);
-            pos = pos < 0 ? 0 : p.max_pos - 1;
+        const uint16_t *at = x + (int64_t)h * D;
+        if (h < heads) {
+            if (HALF) {
+                raw[u][0] = __ldcs(reinterpret_cast<const uint2 *>(at + ea));
+                raw[u][1] = __ldcs(reinterpret_cast<const uint2 *>(at + eb));
+            } else {
+                const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(at + ea));
+                raw[u][0] = make_uint2(r.x, r.y);
+                raw[u][1] = make_uint2(r.z, r.w);
+            }
+        } else {
+            raw[u][0] = raw[u][1] = make_uint2(0, 0);
         }
-        row = p.table + (int64_t)pos * 2 * turn.half + 4 * c;
     }
-    turn.fold(row, p.weight[which]);
+    // a' = rs (a ac - b bs),  b' = rs (b bc + a as): weights and angles are folded once
+    // for the warp's heads
+    float ac[4], as[4], bc[4], bs[4];
+    {
+        float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (turns && half) {
+            int pos = __ldg(p.positions + t);
+            if (pos < 0 || pos >= p.max_pos) {
+                if (lane == 0) atomicOr(p.err, kErrBadPosition);
+                pos = pos < 0 ? 0 : p.max_pos - 1;
+            }
+            const float *row = p.table + (int64_t)pos * 2 * half + 4 * c;
+            cs = __ldg(reinterpret_cast<const float4 *>(row));
+            sn = __ldg(reinterpret_cast<const float4 *>(row + half));
+        }
+        float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+        if (p.weight[which]) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(p.weight[which] + ea));
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(p.weight[which] + eb));
+            if (HALF) {
+                wa[0] = v.x; wa[1] = v.y; wa[2] = v.z; wa[3] = v.w;
+                wb[0] = w.x; wb[1] = w.y; wb[2] = w.z; wb[3] = w.w;
+            } else {
+                wa[0] = v.x; wb[0] = v.y; wa[1] = v.z; wb[1] = v.w;
+                wa[2] = w.x; wb[2] = w.y; wa[3] = w.z; wb[3] = w.w;
+            }
+        }
+        const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            ac[i] = wa[i] * cv[i];
+            as[i] = wa[i] * sv[i];
+            bc[i] = wb[i] * cv[i];
+            bs[i] = wb[i] * sv[i];
+        }
+    }
     uint16_t *y = p.y[which] + t * heads * D;
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
         const int h = head0 + u * kPer;
-        turn.apply(raw[u], p.norm, p.eps);
-        if (h < heads) turn.store(y + (int64_t)h * D, raw[u]);
+        float a[4], b[4];
+        unpack<E, HALF>(raw[u], a, b);
+        if (p.norm) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                s0 = fmaf(a[i], a[i], s0);
+                s1 = fmaf(b[i], b[i], s1);
+            }
+            float ss = s0 + s1;
+#pragma unroll
+            for (int k = kLanes / 2; k > 0; k /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+            const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                a[i] *= rs;
+                b[i] *= rs;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float v = a[i], w = b[i];
+            a[i] = v * ac[i];
+            b[i] = w * bc[i];
+            if (turns) {                                 // 0 times an infinity would not be 0
+                a[i] = fmaf(-w, bs[i], a[i]);
+                b[i] = fmaf(v, as[i], b[i]);
+            }
+        }
+        if (h < heads) {
+            uint2 r[2];
+            pack<E, HALF>(a, b, r);
+            uint16_t *at = y + (int64_t)h * D;
+            if (HALF) {
+                __stcs(reinterpret_cast<uint2 *>(at + ea), r[0]);
+                __stcs(reinterpret_cast<uint2 *>(at + eb), r[1]);
+            } else {
+                __stcs(reinterpret_cast<uint4 *>(at + ea), make_uint4(r[0].x, r[0].y, r[1].x, r[1].y));
+            }
+        }
     }
 }
 

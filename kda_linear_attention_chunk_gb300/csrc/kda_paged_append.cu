@@ -1,7 +1,7 @@
 // kda_paged_append.cu -- per-head RMS norm and rotation of q and k, with k and v on
 // their way into a paged cache, in one pass.
 //
-// The arithmetic is kda_rotate.cuh's; each element is read and written once, so HBM
+// The arithmetic is kda_norm_rope.cu's; each element is read and written once, so HBM
 // bounds it.  A warp takes one token and kUnroll groups of heads of q, k or v, and
 // has all its loads on their way before it looks for the token's sequence, position
 // and page.
@@ -44,15 +44,29 @@ paged_append_kernel(const __grid_constant__ AppendParams p)
     while (chunk >= p.chunks[which]) chunk -= p.chunks[which++];
     const int c = lane % kLanes, heads = p.heads[which];
     const int head0 = chunk * kPer * kUnroll + lane / kLanes;
-    Turn<E, D, HALF, FULL> turn(c, p.rotary);
+    const int half = FULL ? D / 2 : p.rotary / 2;
+    const bool turns = FULL || 4 * c < half;             // this lane's pairs
+    // elements ea .. ea + 3 and eb .. eb + 3 of a head
+    const int ea = HALF && turns ? 4 * c : 8 * c, eb = HALF && turns ? 4 * c + half : 8 * c + 4;
 
     const uint16_t *x = p.x[which] + t * p.stride[which];
     uint2 raw[kUnroll][2];
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
         const int h = head0 + u * kPer;
-        if (h < heads) turn.load(x + (int64_t)h * D, raw[u]);
-        else raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        const uint16_t *at = x + (int64_t)h * D;
+        if (h < heads) {
+            if (HALF) {
+                raw[u][0] = __ldcs(reinterpret_cast<const uint2 *>(at + ea));
+                raw[u][1] = __ldcs(reinterpret_cast<const uint2 *>(at + eb));
+            } else {
+                const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(at + ea));
+                raw[u][0] = make_uint2(r.x, r.y);
+                raw[u][1] = make_uint2(r.z, r.w);
+            }
+        } else {
+            raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        }
     }
     const bool reports = lane == 0 && which == 1 && chunk == 0;
     const int n = p.cu ? sequence_with(p.cu, p.N, (int)t, lane) : (int)t;
@@ -75,19 +89,82 @@ paged_append_kernel(const __grid_constant__ AppendParams p)
         to = p.cache.pages + ((int64_t)id * 2 + (which - 1)) * heads * apart +
                 (int64_t)(pos & ((1 << p.cache.page_log2) - 1)) * D;
     }
+    // a' = rs (a ac - b bs),  b' = rs (b bc + a as): weights and angles are folded once
+    // for the warp's heads
+    float ac[4], as[4], bc[4], bs[4];
     if (which < 2) {
-        const float *row = nullptr;
-        if (turn.half) {
+        float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (turns && half) {
             if (pos >= p.max_pos && reports) atomicOr(p.err, kErrBadPosition);
-            row = p.angles + (int64_t)min(pos, p.max_pos - 1) * 2 * turn.half + 4 * c;
+            const float *row = p.angles + (int64_t)min(pos, p.max_pos - 1) * 2 * half + 4 * c;
+            cs = __ldg(reinterpret_cast<const float4 *>(row));
+            sn = __ldg(reinterpret_cast<const float4 *>(row + half));
         }
-        turn.fold(row, p.weight[which]);
+        float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+        if (p.weight[which]) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(p.weight[which] + ea));
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(p.weight[which] + eb));
+            if (HALF) {
+                wa[0] = v.x; wa[1] = v.y; wa[2] = v.z; wa[3] = v.w;
+                wb[0] = w.x; wb[1] = w.y; wb[2] = w.z; wb[3] = w.w;
+            } else {
+                wa[0] = v.x; wb[0] = v.y; wa[1] = v.z; wb[1] = v.w;
+                wa[2] = w.x; wb[2] = w.y; wa[3] = w.z; wb[3] = w.w;
+            }
+        }
+        const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            ac[i] = wa[i] * cv[i];
+            as[i] = wa[i] * sv[i];
+            bc[i] = wb[i] * cv[i];
+            bs[i] = wb[i] * sv[i];
+        }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
         const int h = head0 + u * kPer;
-        if (which < 2) turn.apply(raw[u], p.norm, p.eps);
-        if (h < heads) turn.store(to + h * apart, raw[u]);
+        if (which < 2) {                                 // (values go as they are)
+            float a[4], b[4];
+            unpack<E, HALF>(raw[u], a, b);
+            if (p.norm) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    s0 = fmaf(a[i], a[i], s0);
+                    s1 = fmaf(b[i], b[i], s1);
+                }
+                float ss = s0 + s1;
+#pragma unroll
+                for (int k = kLanes / 2; k > 0; k /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+                const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    a[i] *= rs;
+                    b[i] *= rs;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float v = a[i], w = b[i];
+                a[i] = v * ac[i];
+                b[i] = w * bc[i];
+                if (turns) {                             // 0 times an infinity would not be 0
+                    a[i] = fmaf(-w, bs[i], a[i]);
+                    b[i] = fmaf(v, as[i], b[i]);
+                }
+            }
+            pack<E, HALF>(a, b, raw[u]);
+        }
+        if (h < heads) {
+            uint16_t *at = to + h * apart;
+            if (HALF) {
+                __stcs(reinterpret_cast<uint2 *>(at + ea), raw[u][0]);
+                __stcs(reinterpret_cast<uint2 *>(at + eb), raw[u][1]);
+            } else {
+                __stcs(reinterpret_cast<uint4 *>(at + ea), make_uint4(raw[u][0].x, raw[u][0].y, raw[u][1].x, raw[u][1].y));
+            }
+        }
     }
 }
 
