@@ -49,13 +49,12 @@ __device__ __forceinline__ int sequence_with(const int32_t *cu, int N, int t, in
 struct RowsAt {
     int bos, len, start;
 };
-__device__ __forceinline__ RowsAt rows_at(const int32_t *cu, const int32_t *starts, const PagedCache &c, int n, int T, int least,
-                                          int *err)
+// cu0, cu1, was: the sequence's table entries as they are.
+__device__ __forceinline__ RowsAt rows_at(int cu0, int cu1, int was, const PagedCache &c, int T, int least, int *err)
 {
     RowsAt r;
-    r.bos = cu ? clamp_row(__ldg(cu + n), T, err) : n;
-    r.len = cu ? max(0, clamp_row(__ldg(cu + n + 1), T, err) - r.bos) : 1;
-    const int was = starts ? __ldg(starts + n) : 0;
+    r.bos = clamp_row(cu0, T, err);
+    r.len = max(0, clamp_row(cu1, T, err) - r.bos);
     r.start = max(least, min(was, capacity(c) - min(r.len, capacity(c))));
     if (err && r.len && (r.start != was || r.len > capacity(c) - r.start)) atomicOr(err, kErrBadPosition);
     return r;

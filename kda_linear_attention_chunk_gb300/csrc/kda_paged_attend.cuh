@@ -195,7 +195,8 @@ __device__ __forceinline__ Part make_part(const AttendParams &p, int i)
             }
         }
         if (x.entry >= 0) {
-            const RowsAt r = rows_at(p.cu, p.starts, p.cache, n, p.T, least, p.err);
+            const RowsAt r = rows_at(p.cu ? p.cu[n] : n, p.cu ? p.cu[n + 1] : n + 1, p.starts ? p.starts[n] : 0, p.cache, p.T,
+                                     least, p.err);
             x.t0 = r.bos;
             x.tokens = min(r.len, capacity(p.cache) - r.start);
             x.first = r.start;

@@ -93,7 +93,8 @@ class Batch:
                 assert off <= 1, (n, off)              # NaN fails too
 
 
-def attention64(q, k, v, pos, scale, dtype):
+def attention64(q, k, v, pos, scale, dtype, whole=False):
+    """whole: the scores are whole numbers that fp32 holds, which leaves no error of theirs."""
     import torch
     u, tiny = BITS[dtype]
     n, Hk, d = k.shape
@@ -103,7 +104,7 @@ def attention64(q, k, v, pos, scale, dtype):
     for h in range(q.shape[1]):
         kk, vv = k[:, h // G], v[:, h // G]
         s = (scale * (q[:, h] @ kk.T)).masked_fill(hide, -math.inf)
-        size = (scale * (q[:, h].abs() @ kk.abs().T)).masked_fill(hide, 0.0).amax(-1, keepdim=True)
+        size = 0.0 if whole else (scale * (q[:, h].abs() @ kk.abs().T)).masked_fill(hide, 0.0).amax(-1, keepdim=True)
         p = torch.softmax(s, -1)
         out[:, h] = p @ vv
         A = p @ vv.abs()

@@ -106,6 +106,12 @@ def test_beams(B, dtype, V):
     check(x, scores, slots=slots)
 
 
+@pytest.mark.parametrize("G,B,V", [(1, 2, 3000001), (5000, 4, 33), (700, 1, 40), (1, 64, 100000)])
+def test_few_long_and_many_short_rows(G, B, V):
+    x, scores, slots = draw(G, B, V, "fp16" if V > 100 else "fp32", seed=G)
+    check(x, scores, slots=slots)
+
+
 @pytest.mark.parametrize("dead", [0, 1, 3, 4])
 def test_beams_without_a_hypothesis(dead):
     """As in the first step, where only one beam of a prompt is live, and of padded prompts, where none is."""

@@ -8,7 +8,7 @@ import pytest
 import kda_linear_attention_chunk_gb300 as kda
 from gpu_util import torch
 from hybrid_util import beside_pending_work, torch_dtype
-from paged_util import Batch
+from paged_util import Batch, attention64
 
 pytestmark = pytest.mark.gpu
 
@@ -76,10 +76,12 @@ def test_long_contexts(own, groups):
     b.check(b.call())
 
 
-def test_many_short_sequences():
+@pytest.mark.parametrize("N", [700, 2500])
+def test_many_short_sequences(N):
+    """More of them than the plan takes at a time."""
     r = random.Random(8)
-    own = [(r.randint(0, 40), r.choice([0, 1, 1, 1, 2, 7])) for _ in range(700)]
-    b = Batch(own, [(100, 60), (50, 7)], Hq=4, Hk=2, d=64, seed=8)
+    own = [(r.randint(0, 40), r.choice([0, 1, 1, 1, 2, 7])) for _ in range(N)]
+    b = Batch(own, [(100, 60), (50, 7)] + [(3, 20)] * (N // 4 - 60), Hq=4, Hk=2, d=64, seed=8)
     b.check(b.call())
 
 
@@ -335,3 +337,49 @@ def test_infinite_scores_are_masked():
     b.pool[p, 0, :, r] = -math.inf
     got = b.call()
     assert t.equal(got[:15], want[:15]) and t.equal(got[20:], want[20:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [1e-30, 0.01, 1e10, 1e30, 9e36])
+def test_scores_times_scales_of_any_size(dtype, scale):
+    """Whole numbers, so that the scores are exact: the largest one takes all where the scale is large, equal ones share."""
+    b = Batch([(300, 1), (700, 40), (2000, 1), (0, 3)], [(2, 260)], dtype=dtype, seed=17, scale=scale)
+    t = b.t
+    b.q.copy_(t.randint(-2, 3, b.q.shape, device="cuda"))
+    live = ~b.pool[:, 0].isnan()
+    b.pool[:, 0] = t.where(live, t.randint(-2, 3, live.shape, device="cuda").to(b.pool.dtype), b.pool[:, 0])
+    out = b.call()
+    for n, L in enumerate(b.lens):
+        k, v = b.keys(n)
+        pos = t.arange(b.start[n], b.start[n] + L, device="cuda")
+        ref, bound = attention64(b.q[b.cu[n]:b.cu[n + 1]].double(), k, v, pos, scale, dtype, whole=True)
+        off = ((out[b.cu[n]:b.cu[n + 1]].double() - ref).abs() / bound).max().item()
+        assert off <= 1, (n, off)
+
+
+def test_a_query_that_is_not_finite_keeps_to_its_row():
+    """Also where rows of other sequences are in its tile, as of a shared prefix."""
+    b = Batch([(20, 1), (300, 1), (7, 30), (40, 1)] + [(9, 1)] * 6, [(2, 500), (7, 90)], seed=18)
+    t, want = b.t, b.call()
+    q = b.q.clone()
+    rows = [1, 10, 34]
+    q[rows] = math.nan
+    q[rows[1], 0] = math.inf
+    got = b.call(q=q)
+    others = [i for i in range(b.T) if i not in rows]
+    assert t.equal(got[others], want[others]) and got[rows].isnan().all()
+
+
+def test_a_member_may_own_the_prefix():
+    """The prompt's own slot goes on as one of the group."""
+    b = Batch([(30, 1), (12, 2), (0, 1)], [(3, 150)], page=64, seed=19)
+    t, want = b.t, b.call()
+    table, pool = b.table.clone(), b.pool.clone()
+    kept, own = b.kept[0], b.ids[0]
+    for j in range(150 // 64 + 1, table.shape[1]):
+        table[kept, j] = table[own, j]
+    tail = b.rows[kept][150 // 64]                     # the page that the prefix ends in goes on with the member's rows
+    pool[tail, :, :, 150 % 64:] = pool[b.rows[own][150 // 64], :, :, 150 % 64:]
+    slots = b.slots.clone()
+    slots[0] = kept
+    assert t.equal(b.call(page_table=table, kv_pages=pool, slots=slots), want)
