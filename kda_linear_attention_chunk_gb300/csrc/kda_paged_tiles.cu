@@ -22,8 +22,8 @@
 // pages without visible positions are boxes outside the tensor, which read as zeros
 // without a trip to memory.
 //
-// Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 the items and loads (a
-// ring of four key and value tiles), warps 9 and 11 the MMAs of the two query tiles, warp 10
+// Roles: warps 0-3 and 4-7 the softmax of the two query tiles, warp 8 the items and loads (room
+// for two tiles of keys and three of values), warps 9 and 11 the MMAs of the two query tiles, warp 10
 // the zeros in place of values that no row sees.
 #include <stdint.h>
 
@@ -45,10 +45,11 @@ using namespace sm100;
 using namespace tiles;
 
 constexpr int kThreads = 384;
-constexpr int kStages = 4;           // tiles of the ring: keys in the even ones, values in the odd ones
-constexpr int kAhead = 2;            // tiles that are on their way into L2 before a stage of the ring is free for them
-constexpr int kBars = 3 * kStages + 23;
-constexpr int kStage = 4096;         // bytes in which a softmax warp turns its rows of O around
+// Room for tiles of keys and of values, which stay longer: until the exponentials are done.  (With room
+// for two of them it takes prefetches into L2 to be as fast, 160 us for 167 without, 64 samples.)
+constexpr int kKeyRoom = 2, kValueRoom = 3, kRoom = kKeyRoom + kValueRoom;
+constexpr int kBars = 3 * kRoom + 23;
+constexpr int kStage = 4096;         // bytes of the query tile in which a softmax warp turns its rows of O around
 // Registers: a softmax thread holds a row of 128 scores.  The block starts with
 // kRegs for each thread and hands them out anew: 2 x 128 x 216 + 128 x 72 of its
 // 384 x 168 (the launch checks that the kernel was built with that number).
@@ -60,15 +61,16 @@ constexpr float kLag = 8.f;          // log2 of what the running maximum may lag
 struct Item {
     int tokens;                      // rows of the span; 0: there are no more items
     int t0, first;                   // its first row and that row's position
-    int hk, shared, entry;
+    int hk, shared;
     int tile0, tiles;                // key tiles
     int key0, end;                   // visible positions: key0 .. end - 1, and up to the row's own (not shared)
     int where;                       // goes_to(), and the first row of a cut piece
     int64_t cut;
     // One query tile only: its key tiles are dealt to both pipelines, which are joined in the end.
-    // Pipeline q takes the tiles in the q-th half of the ring, so that it sees every phase of its
-    // barriers there, and need not see the others'.
-    int turn;                        // the half with the item's first tile
+    // Pipeline q takes the tiles whose keys have the q-th room, so that it sees every phase of its
+    // barriers there, and need not see the other's.  (Of values it sees some, but always after the
+    // one before: the patch warp takes them one after the other.)
+    int turn;                        // the room of the item's first keys
     __device__ bool dealt(int tile_tokens) const { return tokens <= tile_tokens && tiles > 1; }
 };
 
@@ -86,31 +88,36 @@ constexpr int kTmS = 0, kTmO = 256;
 template <typename E, int D> struct Layout {
     static constexpr int kTile = 128 * D * 2;            // bytes of a query, key or value tile
     static constexpr int kHalf = 128 * 128;              // bytes of its 64 leftmost columns
-    static constexpr int kOut = (2 + kStages) * kTile, kCtl = kOut + 8 * kStage;
+    static constexpr int kCtl = (2 + kRoom) * kTile;
+    static_assert(4 * kStage <= kTile, "the rows of O are turned around in the query tile");
     static constexpr int kSmem = 1024 + kCtl + sizeof(Ctl);
     static_assert(kSmem <= 227 * 1024, "more shared memory than a CTA has");
     static constexpr bool kF16 = !__is_same(E, __nv_bfloat16);
 };
 
-// The barriers; q is a query tile, s a stage of the key / value ring, i a place of
-// the item ring.
+// The place of the g-th tile of keys (kv 0) or of values (1), and which use of it that is.
+__device__ __forceinline__ int place(int kv, int g) { return kv ? kKeyRoom + g % kValueRoom : g % kKeyRoom; }
+__device__ __forceinline__ int use(int kv, int g) { return kv ? g / kValueRoom : g / kKeyRoom; }
+
+// The barriers; q is a query tile, s a place of the key / value ring, i one of the item
+// ring.
 struct Bars {
     uint32_t at;
     __device__ uint32_t full(int s) const { return at + 8 * s; }                    // tile loaded
-    __device__ uint32_t empty(int s) const { return at + 8 * (kStages + s); }       // tile consumed by both products
-    __device__ uint32_t values(int s) const { return at + 8 * (2 * kStages + s); }  // value tile without garbage
-    __device__ uint32_t q_full(int q) const { return at + 8 * (3 * kStages + q); }
-    __device__ uint32_t q_empty(int q) const { return at + 8 * (3 * kStages + 2 + q); }
-    __device__ uint32_t s_full(int q) const { return at + 8 * (3 * kStages + 4 + q); }    // scores in TMEM
-    __device__ uint32_t p_half(int q) const { return at + 8 * (3 * kStages + 6 + q); }    // probabilities of 64 keys
-    __device__ uint32_t p_ready(int q) const { return at + 8 * (3 * kStages + 8 + q); }   // of all
-    __device__ uint32_t o_done(int q) const { return at + 8 * (3 * kStages + 10 + q); }   // O complete
-    __device__ uint32_t o_free(int q) const { return at + 8 * (3 * kStages + 12 + q); }   // O read
-    __device__ uint32_t turn(int q) const { return at + 8 * (3 * kStages + 14 + q); }
-    __device__ uint32_t drained(int q) const { return at + 8 * (3 * kStages + 16 + q); }
-    __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kStages + 18 + i); }
-    __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kStages + 20 + i); }
-    __device__ uint32_t other_done() const { return at + 8 * (3 * kStages + 22); }    // a dealt item's second pipeline is
+    __device__ uint32_t empty(int s) const { return at + 8 * (kRoom + s); }       // tile consumed by both products
+    __device__ uint32_t values(int s) const { return at + 8 * (2 * kRoom + s); }  // value tile without garbage
+    __device__ uint32_t q_full(int q) const { return at + 8 * (3 * kRoom + q); }
+    __device__ uint32_t q_empty(int q) const { return at + 8 * (3 * kRoom + 2 + q); }
+    __device__ uint32_t s_full(int q) const { return at + 8 * (3 * kRoom + 4 + q); }    // scores in TMEM
+    __device__ uint32_t p_half(int q) const { return at + 8 * (3 * kRoom + 6 + q); }    // probabilities of 64 keys
+    __device__ uint32_t p_ready(int q) const { return at + 8 * (3 * kRoom + 8 + q); }   // of all
+    __device__ uint32_t o_done(int q) const { return at + 8 * (3 * kRoom + 10 + q); }   // O complete
+    __device__ uint32_t o_free(int q) const { return at + 8 * (3 * kRoom + 12 + q); }   // O read
+    __device__ uint32_t turn(int q) const { return at + 8 * (3 * kRoom + 14 + q); }
+    __device__ uint32_t drained(int q) const { return at + 8 * (3 * kRoom + 16 + q); }
+    __device__ uint32_t item_full(int i) const { return at + 8 * (3 * kRoom + 18 + i); }
+    __device__ uint32_t item_empty(int i) const { return at + 8 * (3 * kRoom + 20 + i); }
+    __device__ uint32_t other_done() const { return at + 8 * (3 * kRoom + 22); }    // a dealt item's second pipeline is
 };
 constexpr int kItemReaders = 8 + 2 + 1;   // softmax warps, product warps, patch warp
 
@@ -173,7 +180,8 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
     const int64_t total = lines.total[0], share = lines.share[0];
     const int64_t from = blockIdx.x * share, to = min(total * p.Hk, from + share);
     int64_t at = from;
-    int it = 0, item = 0, qs[2] = {0, 0};                // tiles and query tiles loaded, items written
+    int g = 0, item = 0, qs[2] = {0, 0};                 // tiles (of keys and of values each) and query tiles loaded, items written
+    int drain[2] = {0, 0};                               // tiles of keys, of values on their way at least once
     bool ok = true;
     for (;; item++) {
         Item &now = x.c.items[item & 1];
@@ -203,12 +211,11 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             now.first = shared ? 0 : y.first + j * span;
             now.hk = hk;
             now.shared = shared;
-            now.entry = y.entry;
             now.tile0 = tile0;
             now.tiles = n;
             now.key0 = y.key0;
             now.end = end;
-            now.turn = it / 2 & 1;
+            now.turn = g & 1;
             now.where = goes_to(y, shared, begin, stop, from, to);
             now.cut = cut_piece(blockIdx.x, begin, from) * kPieceRows;
             mbar_arrive(x.bars.item_full(item & 1));
@@ -224,10 +231,26 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             const int j = (tile * kTileKeys + lb * box) >> cache.page_log2;
             return lb * box < kTileKeys && j < cache.max_pages ? __ldg(table + j) : -1;
         };
-        int id = entry_at(tile0);
-        bool queries = false;
+        auto load_queries = [&]() {
 #pragma unroll 1
-        for (int i = 0; i < n && ok; i++) {
+            for (int q = 0; q < 2 && ok; q++) {
+                if (!seen[q]) continue;
+                if (qs[q]) ok = x.wait(x.bars.q_empty(q), qs[q] - 1);
+                if (ok && elect_one()) {
+                    // half a query tile is G tile_tokens rows of 128 bytes
+                    mbar_arrive_expect_tx(x.bars.q_full(q), (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64)));
+#pragma unroll
+                    for (int h = 0; h < D / 64; h++)
+                        tma_load_3d(sq + q * L::kTile + h * L::kHalf, &maps.q, 64 * h, hk * p.G, t0 + q * p.tile_tokens,
+                                    x.bars.q_full(q));
+                }
+                __syncwarp();
+                if (ok) qs[q]++;
+            }
+        };
+        int id = entry_at(tile0);
+#pragma unroll 1
+        for (int i = 0; i < n && ok; i++, g++) {
             const int pos = (tile0 + i) * kTileKeys, at_b = pos + lb * box;
             const int boxes = (tile_keys(end, tile0 + i) + box - 1) / box;
             const bool mine = lb < boxes, needed = mine && at_b + box > y.key0, there = id >= 0 && id < cache.num_pages;
@@ -236,8 +259,8 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             if (i + 1 < n) id = entry_at(tile0 + i + 1);
 #pragma unroll 1
             for (int kv = 0; kv < 2; kv++) {
-                const int s = it % kStages;
-                if (it >= kStages) ok = x.wait(x.bars.empty(s), it / kStages - 1);
+                const int s = place(kv, g), k = use(kv, g);
+                if (k) ok = x.wait(x.bars.empty(s), k - 1);
                 if (!ok) break;
                 const uint32_t bar = x.bars.full(s), dst = skv + s * L::kTile;
                 if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * (D / 64)));
@@ -246,30 +269,17 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
                     tma_load_3d(dst + lh * L::kHalf + lb * box * 128, &maps.pages, 64 * lh, c1,
                                 c2 == outside ? outside : c2 + kv * p.Hk, bar);
                 __syncwarp();
-                it++;
-                if (queries) continue;
-                queries = true;                          // after the first keys, which need not wait for their room
-#pragma unroll 1
-                for (int q = 0; q < 2 && ok; q++) {
-                    if (!seen[q]) continue;
-                    if (qs[q]) ok = x.wait(x.bars.q_empty(q), qs[q] - 1);
-                    if (ok && elect_one()) {
-                        // half a query tile is G tile_tokens rows of 128 bytes
-                        mbar_arrive_expect_tx(x.bars.q_full(q), (uint32_t)(p.G * p.tile_tokens * 128 * (D / 64)));
-#pragma unroll
-                        for (int h = 0; h < D / 64; h++)
-                            tma_load_3d(sq + q * L::kTile + h * L::kHalf, &maps.q, 64 * h, hk * p.G,
-                                        t0 + q * p.tile_tokens, x.bars.q_full(q));
-                    }
-                    __syncwarp();
-                    if (ok) qs[q]++;
-                }
+                drain[kv]++;
+                // The first item's queries come behind the first keys; later ones' room is free only when
+                // the output is written, and two tiles need not wait for that.
+                if (kv == 0 && i == 0 && item == 0) load_queries();
             }
+            if (ok && i == min(1, n - 1) && item) load_queries();
         }
         // The first keys of the next item may be for a pipeline that did not see the tile before them in
-        // their room (as of values, the patch warp takes those one after the other).
+        // their room.
         if (n > 1 && !seen[1])
-            for (int i = it - 4; i < it && ok; i += 2) ok = x.wait(x.bars.full(i % kStages), i / kStages);
+            for (int i = g - kKeyRoom; i < g && ok; i++) ok = x.wait(x.bars.full(place(0, i)), use(0, i));
         if (!ok) break;
     }
     if (!ok && x.lane == 0) x.give_up();
@@ -278,7 +288,9 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
     for (int q = 0; q < 2; q++)
         if (qs[q]) mbar_wait_drain(x.bars.q_full(q), (qs[q] - 1) & 1);
 #pragma unroll 1
-    for (int i = it < kStages ? 0 : it - kStages; i < it; i++) mbar_wait_drain(x.bars.full(i % kStages), (i / kStages) & 1);
+    for (int kv = 0; kv < 2; kv++)
+        for (int i = max(0, drain[kv] - (kv ? kValueRoom : kKeyRoom)); i < drain[kv]; i++)
+            mbar_wait_drain(x.bars.full(place(kv, i)), use(kv, i) & 1);
 }
 
 // ---- products of one query tile ---------------------------------------------------
@@ -296,7 +308,7 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
     const uint32_t ts = tm + kTmS + 128 * q, to = tm + kTmO + 128 * q;
     const uint32_t qs = x.base + q * L::kTile, skv = x.base + 2 * L::kTile;
     // tiles consumed; products P V issued; turns taken; items with rows; query tiles used
-    int it = 0, parts = 0, turns = 0, mine = 0, queries[2] = {0, 0};
+    int g = 0, parts = 0, turns = 0, mine = 0, queries[2] = {0, 0};
     bool ok = true;
     for (int item = 0; ok; item++) {
         const Item &now = x.c.items[item & 1];
@@ -313,8 +325,8 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
             ok = x.wait(x.bars.q_full(0), queries[0]);
 #pragma unroll 1
             for (int i = (q + __shfl_sync(0xffffffffu, now.turn, 0)) & 1; i < n && ok; i += 2) {
-                const int g = it + 2 * i, sk = g % kStages, sv = (g + 1) % kStages, phase = g / kStages;
-                ok = x.wait(x.bars.full(sk), phase);
+                const int sk = place(0, g + i), sv = place(1, g + i);
+                ok = x.wait(x.bars.full(sk), use(0, g + i));
                 const int keys = tile_keys(end, tile0 + i);
                 const bool last = i + 2 >= n;
                 if (ok && elect_one()) {
@@ -322,10 +334,9 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
                     mma_commit(x.bars.s_full(q));
                     mma_commit(x.bars.empty(sk));        // for both pipelines
                     mma_commit(x.bars.empty(sk));
-                    if (last) mma_commit(x.bars.q_empty(0));
                 }
                 __syncwarp();
-                ok = ok && x.wait(x.bars.values(sv), phase);
+                ok = ok && x.wait(x.bars.values(sv), use(1, g + i));
                 if (ok && i < 2 && mine > 0) ok = x.wait(x.bars.o_free(q), mine - 1);
                 ok = ok && x.wait(x.bars.p_half(q), parts);
                 if (ok) {
@@ -345,32 +356,26 @@ __device__ __forceinline__ void product_role(const Ctx &x, int which)
                 }
                 __syncwarp();
             }
-            it += 2 * n;
+            g += n;
         } else {
             int keys = tile_keys(end, tile0);
-            ok = x.wait(x.bars.full(it % kStages), it / kStages) && (!any || x.wait(x.bars.q_full(q), queries[q]));
+            ok = x.wait(x.bars.full(place(0, g)), use(0, g)) && (!any || x.wait(x.bars.q_full(q), queries[q]));
             if (elect_one()) {
                 if (ok && any) {
-                    mma_scores<D>(ts, qs, skv + it % kStages * L::kTile, idesc(keys, 0, L::kF16));
+                    mma_scores<D>(ts, qs, skv + place(0, g) * L::kTile, idesc(keys, 0, L::kF16));
                     mma_commit(x.bars.s_full(q));
                 }
-                mma_commit(x.bars.empty(it % kStages));
+                mma_commit(x.bars.empty(place(0, g)));
             }
             __syncwarp();
-            it++;
-            for (int i = 0; i < n && ok; i++) {
-                const int sv = it % kStages, steps = keys / 16;   // this tile's values
-                ok = x.wait(x.bars.values(sv), it / kStages);
-                it++;
-                const int sk = it % kStages;             // the next tile's keys
+            for (int i = 0; i < n && ok; i++, g++) {
+                const int sv = place(1, g), steps = keys / 16;    // this tile's values
+                ok = x.wait(x.bars.values(sv), use(1, g));
+                const int sk = place(0, g + 1);          // the next tile's keys
                 const bool have = i + 1 < n;
                 if (have) {
                     keys = tile_keys(end, tile0 + i + 1);
-                    ok = ok && x.wait(x.bars.full(sk), it / kStages);
-                    it++;
-                } else if (any && elect_one()) {
-                    mma_commit(x.bars.q_empty(q));       // every product with the query tile is issued
-                    mma_commit(x.bars.q_empty(q));       // (two, as of a dealt item's pipelines)
+                    ok = ok && x.wait(x.bars.full(sk), use(0, g + 1));
                 }
                 __syncwarp();
                 if (both && ok && (q || turns)) ok = x.wait(x.bars.turn(q), q ? turns : turns - 1);
@@ -421,29 +426,15 @@ template <typename E, int D>
 __device__ __forceinline__ void patch_role(const Ctx &x)
 {
     using L = Layout<E, D>;
-    const PagedCache &cache = x.p.cache;
-    const int page = 1 << cache.page_log2, box = min(page, kTileKeys);
     bool ok = true;
-    for (int item = 0, it = 1; ok; item++) {
+    for (int item = 0, g = 0; ok; item++) {
         const Item &now = x.c.items[item & 1];
         ok = x.wait(x.bars.item_full(item & 1), item / 2);
         if (!ok || now.tokens == 0) break;
         const int n = now.tiles;
-        const int32_t *table = cache.table + (int64_t)now.entry * cache.max_pages;
-        for (int i = 0; i < n && ok; i++, it += 2) {
-            const int s = it % kStages;
-            if (kAhead && i + kAhead < n) {              // on its way into L2
-                const int t = now.tile0 + i + kAhead, b = x.lane >> 1, at_b = t * kTileKeys + b * box, kv = x.lane & 1;
-                if (b < (tile_keys(now.end, t) + box - 1) / box) {
-                    const int id = __ldg(table + (at_b >> cache.page_log2));
-                    if (id >= 0 && id < cache.num_pages)
-                        prefetch_l2(cache.pages + (((int64_t)id * 2 + kv) * x.p.Hk + now.hk) * ((int64_t)D << cache.page_log2) +
-                                        (int64_t)(at_b & (page - 1)) * D,
-                                    (uint32_t)box * D * 2);
-                }
-                __syncwarp();
-            }
-            ok = x.wait(x.bars.full(s), it / kStages);
+        for (int i = 0; i < n && ok; i++, g++) {
+            const int s = place(1, g);
+            ok = x.wait(x.bars.full(s), use(1, g));
             if (!ok) break;
             const int pos = (now.tile0 + i) * kTileKeys, keys = tile_keys(now.end, now.tile0 + i);
             if (pos < now.key0 || pos + keys > now.end) {
@@ -476,7 +467,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
     const uint32_t lanes = x.tmem + ((uint32_t)(warp & 3) << 21);
     const uint32_t ts = lanes + kTmS + 128 * q, to = lanes + kTmO + 128 * q;
     const float c2 = p.scale_log2;
-    uint8_t *stage = x.smem + L::kOut + warp * kStage;
+    uint8_t *stage = x.smem + q * L::kTile + (warp & 3) * kStage;   // (every product with the queries is done by then)
     int it = 0, mine = 0, joined = 0;                    // score tiles, items with rows, dealt ones
     bool ok = true;
     for (int item = 0; ok; item++) {
@@ -622,6 +613,12 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             *ml = make_float2(m, sum);
         }
         if (!rows.seen) continue;                        // nothing visible in this piece: no O
+        // the room of the query tile, written and read here, for the next one's copy
+        auto free_queries = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x.bars.q_empty(q));
+        };
         // 32 columns of O, multiplied by f; after the last ones it is free for the next item
         auto load_o = [&](int h, float f, uint32_t (&o)[32]) {
             tmem_ld32(to + 32 * h, o);
@@ -668,6 +665,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
                 }
                 __syncwarp();
             }
+            free_queries();
             continue;
         }
         // O / sum in 16 bits, 64 columns at a time
@@ -698,6 +696,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             }
             __syncwarp();
         }
+        free_queries();
     }
     if (!ok) x.give_up();
 }
@@ -715,14 +714,14 @@ paged_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ At
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == 8 && lane == 0) {
         c.abort = 0;
-        for (int s = 0; s < kStages; s++) {
+        for (int s = 0; s < kRoom; s++) {
             mbar_init(bars.full(s), 1);
             mbar_init(bars.empty(s), 2);
             mbar_init(bars.values(s), 1);
         }
         for (int q = 0; q < 2; q++) {
             mbar_init(bars.q_full(q), 1);
-            mbar_init(bars.q_empty(q), 2);
+            mbar_init(bars.q_empty(q), 4);
             mbar_init(bars.s_full(q), 1);
             mbar_init(bars.p_half(q), 4);
             mbar_init(bars.p_ready(q), 4);
