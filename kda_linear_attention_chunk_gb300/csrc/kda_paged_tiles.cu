@@ -10,11 +10,17 @@
 //     O += P V             (P from TMEM in place of S, V MN-major as loaded)
 //
 // The two query tiles take turns on the tensor core: while one's scores are exponentiated,
-// the other's products run.  Where a span is only one query tile (a small group's prefix, drafts),
-// the key tiles are dealt to the two pipelines instead, each with a maximum, sum and O of its
-// own, and the first joins them: a tile's chain of products and exponentials, 1.9 us, would
-// be longer than its way from HBM, 1.5.  The maximum m only follows the true one when it falls behind by
-// more than 2^8, so O is rarely rescaled, and the threads that own the rows do it.
+// the other's products run.  Where a span is only one query
+// tile (a small group's prefix, drafts) and has several key tiles, these are dealt to the two
+// pipelines instead, each with a maximum, sum and O of its own, and the first joins them: one
+// pipeline's chain of products and exponentials, 1.9 us a tile, is longer than the tile's way
+// from HBM, 1.5.  The maximum m only follows the true one when it falls behind by more than
+// 2^8, so O is rarely rescaled, and the threads that own the rows do it.
+//
+// On a GB300, 32 query heads on 8 key heads of 128: 16 x 8 beams over prefixes of 8192 positions
+// 80 us, 5.5 TB/s; 64 samples over 131,072 positions 109 us, 4.9 TB/s and 1.26 PFLOP/s (without
+// its exponentials 96: loads and products); 2048 rows behind 32,768 735 us, 1.54 PFLOP/s.  An item's
+// first scores come 4 us after its start: the plan's entry, the page table's, the first keys.
 //
 // One CTA an SM takes an equal share of the line of all tiles, so a long prefix is spread
 // over the card and short parts share a CTA; what it computes of a span whose keys it
@@ -55,6 +61,7 @@ constexpr int kStage = 4096;         // bytes of the query tile in which a softm
 // 384 x 168 (the launch checks that the kernel was built with that number).
 constexpr int kRegs = 168, kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegs, "more registers than the block has");
+constexpr int kDealt = 8;            // key tiles from which one query tile's are dealt
 constexpr float kLag = 8.f;          // log2 of what the running maximum may lag behind
 
 // One item of work: a span's rows, one key head, some of the span's key tiles.
@@ -67,11 +74,13 @@ struct Item {
     int where;                       // goes_to(), and the first row of a cut piece
     int64_t cut;
     // One query tile only: its key tiles are dealt to both pipelines, which are joined in the end.
+    // Worth it from some tiles on (16 x 8 beams over 8192 positions 111.8 us without, 108.1 with;
+    // three to five tiles of small heads 36.2 and 36.8).
     // Pipeline q takes the tiles whose keys have the q-th room, so that it sees every phase of its
     // barriers there, and need not see the other's.  (Of values it sees some, but always after the
     // one before: the patch warp takes them one after the other.)
     int turn;                        // the room of the item's first keys
-    __device__ bool dealt(int tile_tokens) const { return tokens <= tile_tokens && tiles > 1; }
+    __device__ bool dealt(int tile_tokens) const { return tokens <= tile_tokens && tiles >= kDealt; }
 };
 
 struct Ctl {
@@ -221,6 +230,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             mbar_arrive(x.bars.item_full(item & 1));
         }
         __syncwarp();
+        const bool now_dealt = now.dealt(p.tile_tokens);
         const int seen[2] = {Span(now, p.tile_tokens, 0).seen, Span(now, p.tile_tokens, 1).seen};
         const int32_t *table = cache.table + (int64_t)y.entry * cache.max_pages;
         // A lane has a box of its own: 64 columns of page rows box lb of a tile.  It loads the entry of
@@ -278,7 +288,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         }
         // The first keys of the next item may be for a pipeline that did not see the tile before them in
         // their room.
-        if (n > 1 && !seen[1])
+        if (now_dealt)
             for (int i = g - kKeyRoom; i < g && ok; i++) ok = x.wait(x.bars.full(place(0, i)), use(0, i));
         if (!ok) break;
     }
