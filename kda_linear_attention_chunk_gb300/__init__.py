@@ -925,7 +925,7 @@ def paged_append(q, k, v, kv_pages, page_table, starts=None, cu_seqlens=None, sl
         out = _new((T, Hq, d), dtype, q.device, stream)
     else:
         _dense("out", out, (T, Hq, d), dtype, at)
-    if not T and cu_seqlens is None:             # no sequence
+    if not T:
         return out
     st = load().kda_paged_append(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, qw, kw, tab, max_pos, cu, first, ids,
                                  *cache, out.data_ptr(), N, T, Hq, Hk, d, rotary, ROPE_LAYOUTS[layout], 1 if norm else 0,
@@ -1033,6 +1033,10 @@ def beam_select(logits, scores, ended=None, end_token: int = -1, slots=None, str
     was = 0 if ended is None else _dense("ended", ended, shape, torch.int32, at)
     ids = 0 if slots is None else _dense("slots", slots, shape, torch.int32, at)
     device = logits.device
+    stops, moves = end_token >= 0, slots is not None
+    if not G:                                    # no prompt
+        none = _new((7, 0, B), torch.int32, device, stream).unbind(0)
+        return (none[0].view(torch.float32), *none[1:3], none[3] if stops else None) + (none[4:] if moves else (None,) * 3)
     lib = load()
     size = lib.kda_beam_select_workspace(G, B, V)
     if size <= 0:
@@ -1040,7 +1044,6 @@ def beam_select(logits, scores, ended=None, end_token: int = -1, slots=None, str
     work = _scratch(size, device, stream)
     best, parents, tokens, stopped, new_slots, src, dst = _new((7, G, B), torch.int32, device, stream).unbind(0)
     best = best.view(torch.float32)              # one allocation for all
-    stops, moves = end_token >= 0, slots is not None
     st = lib.kda_beam_select(logits.data_ptr(), row if rows > 1 else V, kinds[logits.dtype], s, was, end_token, ids,
                              best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), stopped.data_ptr() if stops else 0,
                              *((new_slots.data_ptr(), src.data_ptr(), dst.data_ptr()) if moves else (0, 0, 0)),

@@ -84,20 +84,18 @@ __device__ __forceinline__ float two_sum(float a, float b, float &e)
     return s;
 }
 
-// log l of 0 < l < 2^126 as a sum of two numbers, off by some 2^-25: l = 2^k f with f in
-// [2^-1/2, 2^1/2], and f to 48 bits by the logarithm's slope
+// log l of l > 0 as a sum of two numbers, off by some 2^-25: l = 2^k f with f in [2^-1/2, 2^1/2],
+// and what fp32 leaves of f by the logarithm's slope
 __device__ __forceinline__ float2 log_of(double l)
 {
     const float top = (float)l;
-    const int k = (int)((__float_as_uint(top) - 0x3f3504f3u) >> 23) - (__float_as_uint(top) < 0x3f3504f3u ? 512 : 0);
-    const float unit = __uint_as_float((uint32_t)(127 - k) << 23);
-    const float f = top * unit, rest = (float)(l - (double)top) * unit;
-    const float ln2_hi = 0.693145751953125f, ln2_lo = 1.42860677e-6f;      // k ln2_hi is exact
-    float e;
-    const float s = two_sum(k * ln2_hi, logf(f), e);
-    return make_float2(s, e + fmaf((float)k, ln2_lo, rest / f));
+    int k;
+    float f = frexpf(top, &k);                           // in [1/2, 1)
+    if (f < 0.70710678f) f *= 2.f, k--;
+    const double y = (double)k * 0.6931471805599453 + ((double)logf(f) + (l - (double)top) / (double)top);
+    const float hi = (float)y;
+    return make_float2(hi, (float)(y - (double)hi));
 }
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

@@ -97,7 +97,9 @@ struct Place {
 __device__ __forceinline__ Place place_of(const AttendParams &p, const Lines &lines, const Part &x, bool shared, int t)
 {
     Place r = {};
-    r.any = x.kind != kNoWork;
+    // (a row outside its prefix's part: cu_seqlens or groups broke their contract)
+    r.any = x.kind != kNoWork && t >= x.t0 && t - x.t0 < x.tokens;
+    if (!r.any) return r;
     r.tiles = x.kind == kTilesWork;
     r.total = lines.total[!r.tiles];
     r.share = lines.share[!r.tiles];

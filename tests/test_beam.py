@@ -279,3 +279,12 @@ def test_steps_in_a_row():
             hyps = sorted(every, key=lambda e: -e[0])[:B]
         assert [h for _, h in hyps] == texts[i]
         assert np.allclose([s for s, _ in hyps], scores[i].cpu().numpy(), atol=6 * 2.0 ** -18 + 2.0 ** -18)
+
+
+def test_a_batch_without_prompts():
+    t = torch()
+    got = kda.beam_select(t.empty(0, 50, device="cuda"), t.empty(0, 4, device="cuda"), end_token=3)
+    assert [x if x is None else tuple(x.shape) for x in got] == [(0, 4)] * 4 + [None] * 3
+    got = kda.beam_select(t.empty(0, 50, device="cuda"), t.empty(0, 4, device="cuda"),
+                          slots=t.empty(0, 4, dtype=t.int32, device="cuda"))
+    assert got[0].dtype == t.float32 and got[3] is None and got[4].dtype == t.int32 and got[6].shape == (0, 4)

@@ -383,3 +383,19 @@ def test_a_member_may_own_the_prefix():
     slots = b.slots.clone()
     slots[0] = kept
     assert t.equal(b.call(page_table=table, kv_pages=pool, slots=slots), want)
+
+
+@pytest.mark.parametrize("cu,groups", [((0, 30, 10, 40, 41), (0, 2, 4)), ((0, 1, 21, 40, 41), (2, 1, 4)),
+                                       ((40, 30, 20, 10, 0), (0, 4, 2)), ((0, 20, 41, 20, 41), (4, 0, 4))])
+def test_tables_out_of_order_stay_in_bounds(cu, groups):
+    """cu_seqlens and groups that go back: the results are undefined, but the call ends, writes its rows only, and the next one
+    is right."""
+    b = Batch([(20, 1), (30, 20), (100, 19), (50, 1)], [(2, 200), (2, 90)], seed=20)
+    t = b.t
+    i32 = lambda x: t.tensor(x, dtype=t.int32, device="cuda")   # noqa: E731
+    room = t.full((b.T + 2, b.Hq, b.d), 4.0, dtype=b.q.dtype, device="cuda")
+    b.call(cu_seqlens=i32(cu), prefixes=(i32(groups), *b.prefixes[1:]), out=room[1:-1])
+    t.cuda.synchronize()
+    assert (room[0] == 4).all() and (room[-1] == 4).all()
+    kda.device_error(reset=True)
+    b.check(b.call())
