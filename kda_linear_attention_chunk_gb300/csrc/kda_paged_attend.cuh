@@ -10,7 +10,9 @@
 // whole pages.)
 //
 // All steps of a kernel's parts, of one key head after the other, form a line, which
-// its workers (a warp, or a CTA) share in equal pieces, whatever the lengths.  So a worker
+// its workers (a warp, or a CTA) share in equal pieces, whatever the lengths.  Each span or
+// part takes some more of the line before its steps, for what its beginning costs a worker (a
+// few loads, one after the other), so that short ones spread over more workers.  So a worker
 // has the steps of some (part, span, head) to itself, but for its first and last ones,
 // which it may share with its neighbours.  The row's maxima, sums and unnormalised outputs
 // of every piece that is not a row's whole answer go to the workspace, where the join
@@ -37,7 +39,7 @@ struct alignas(16) Part {
     int entry;                       // whose pages they are in
     int prefix;                      // own keys: the part of the prefix, -1 if there is none
     int kind;
-    int64_t begin, pad;              // its tiles' or steps' place in the line of a key head
+    int64_t begin, pad;              // its place in the line of a key head, with its set-up
 };
 
 // the lines of the tiles and of the rows kernel
@@ -77,7 +79,13 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int Hk, int workers, 
     const int64_t each = quotient(total * Hk + workers - 1, workers);
     return each < least ? least : each;
 }
-constexpr int kLeastTiles = 2, kLeastSteps = 8;
+// What a beginning counts for, in tiles or steps.  With it 40 calls of random sizes, most of them
+// small, took 0.76 of their time without (geometric mean; 224 sequences of 2 keys 13 us in place of
+// 32, 19 drafts over four prefixes 64 in place of 83).  A long part's beginning is little beside its
+// steps, and HBM bounds those: 64 sequences of up to 16k keys took 443 us with it, 437 without.
+constexpr int kTilesSetUp = 3, kStepsSetUp = 4, kShortSteps = 64;
+// A worker's least: a beginning and one tile or step.
+constexpr int kLeastTiles = kTilesSetUp + 1, kLeastSteps = kStepsSetUp + 1;
 
 // Sum of floor((a i + b) / 128) over i < n, for a, b >= 0: the whole parts of a / 128 and b / 128
 // sum up at once, and what is left counts the lattice points below a line, which turns into
@@ -118,15 +126,21 @@ __device__ __forceinline__ int64_t tiles_before(const Part &x, bool shared, int 
     if (shared) return (int64_t)j * span_tiles(x, true, span, 0);
     return sum_of_tiles(j, span, (int64_t)x.first + span + kTileKeys - 1) - (int64_t)j * first_tile(x);
 }
+// the place of span j, with its set-up, in its part's line; that line's length
+__device__ __forceinline__ int64_t span_begin(const Part &x, bool shared, int span, int j)
+{
+    return tiles_before(x, shared, span, j) + (int64_t)j * kTilesSetUp;
+}
 __device__ __forceinline__ int64_t part_tiles(const Part &x, bool shared, int span)
 {
     const int n = spans_of(x, span);
-    return n ? tiles_before(x, shared, span, n - 1) + span_tiles(x, shared, span, n - 1) : 0;
+    return n ? span_begin(x, shared, span, n - 1) + kTilesSetUp + span_tiles(x, shared, span, n - 1) : 0;
 }
 __device__ __forceinline__ int part_steps(const Part &x)
 {
     return (int)(((int64_t)x.key1 + kStepKeys - 1) / kStepKeys) - x.key0 / kStepKeys;
 }
+__device__ __forceinline__ int steps_set_up(const Part &x) { return part_steps(x) <= kShortSteps ? kStepsSetUp : 0; }
 
 __device__ __forceinline__ Part load_part(const Part *p)
 {
@@ -221,13 +235,13 @@ __device__ __forceinline__ int part_at(const int64_t *before, int n, int64_t x, 
     }
     return a;
 }
-// The last span that starts at or before tile x of its part, by a converged warp.
+// The last span that starts at or before place x of its part, by a converged warp.
 __device__ __forceinline__ int span_at(const Part &part, bool shared, int span, int64_t x, int lane)
 {
     int a = 0, n = spans_of(part, span);
     while (n > 1) {
         const int step = (n + 31) / 32, i = lane * step;
-        const bool le = i < n && tiles_before(part, shared, span, a + i) <= x;
+        const bool le = i < n && span_begin(part, shared, span, a + i) <= x;
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, le || lane == 0));
         n = min(step, n - last * step);
         a += last * step;
@@ -238,7 +252,7 @@ __device__ __forceinline__ int span_at(const Part &part, bool shared, int span, 
 // Where a piece goes: to the output (it is all of its rows' keys), to the whole pieces of own
 // keys or of prefixes, or to one of the worker's two cut pieces.
 enum { kToOut = 0, kToOwn = 1, kToPrefix = 2, kToCut = 3 };
-// begin, end: of the (part, span, head) in the line; from, to: the worker's share
+// begin, end: of the steps of the (part, span, head) in the line; from, to: the worker's share
 __device__ __forceinline__ int goes_to(const Part &x, bool shared, int64_t begin, int64_t end, int64_t from, int64_t to)
 {
     if (begin < from || end > to) return kToCut;

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (i < all) {
             x = make_part(p, i);
             if (x.kind == kTilesWork) mine[0] = part_tiles(x, i < p.P, 2 * p.tile_tokens);
-            if (x.kind == kRowsWork) mine[1] = part_steps(x);
+            if (x.kind == kRowsWork) mine[1] = steps_set_up(x) + part_steps(x);
         }
         int64_t upto[2] = {mine[0], mine[1]};
 #pragma unroll
@@ -90,7 +90,7 @@ constexpr int kJoinThreads = 256, kLanes = 8, kGroups = kJoinThreads / kLanes;
 // a row's place in one of its two parts
 struct Place {
     int64_t total, share;            // of the kernel's line
-    int64_t begin, n;                // the row's span in the line of a key head
+    int64_t begin, n;                // the steps of the row's span or part in the line of a key head
     int row, rows;                   // the row's first query head in a piece; rows of a piece
     bool tiles, any;
 };
@@ -107,11 +107,12 @@ __device__ __forceinline__ Place place_of(const AttendParams &p, const Lines &li
     const int i = t - x.t0, span = 2 * p.tile_tokens;
     if (r.tiles) {
         const int j = i / span, u = i - j * span, q = u >= p.tile_tokens;
-        r.begin += tiles_before(x, shared, span, j);
+        r.begin += span_begin(x, shared, span, j) + kTilesSetUp;
         r.n = span_tiles(x, shared, span, j);
         r.row = q * kTileRows + (u - q * p.tile_tokens) * p.G;
         r.rows = kPieceRows;
     } else {
+        r.begin += steps_set_up(x);
         r.n = part_steps(x);
         r.row = i * p.G;
         r.rows = kFewRows;

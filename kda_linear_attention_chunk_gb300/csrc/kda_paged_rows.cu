@@ -56,7 +56,9 @@ paged_rows_kernel(const __grid_constant__ AttendParams p)
         const int hk = (int)quotient(at, total), part = part_at(p.steps, parts, at - hk * total, lane);
         const bool shared = part < p.P;
         const Part x = load_part(p.parts + part);
-        const int64_t begin = hk * total + x.begin, end = begin + part_steps(x);
+        const int64_t begin = hk * total + x.begin + steps_set_up(x), end = begin + part_steps(x);
+        if (at < begin) at = begin;
+        if (at >= to) break;
         const int step0 = x.key0 / kStepKeys + (int)(at - begin);
         const int steps = (int)(min(end, to) - at);
         at += steps;

@@ -196,6 +196,22 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
         Item &now = x.c.items[item & 1];
         if (item >= 2) ok = x.wait(x.bars.item_empty(item & 1), item / 2 - 1);
         if (!ok) break;
+        // the part, span and key head of this place in the line
+        int hk = 0, j = 0;
+        bool shared = false;
+        Part y = {};
+        int64_t begin = 0, stop = 0;
+        if (at < to) {
+            hk = (int)quotient(at, total);
+            const int part = part_at(p.tiles, parts, at - hk * total, x.lane);
+            shared = part < p.P;
+            y = load_part(p.parts + part);
+            begin = hk * total + y.begin;
+            j = span_at(y, shared, span, at - begin, x.lane);
+            begin += span_begin(y, shared, span, j) + kTilesSetUp;
+            stop = begin + span_tiles(y, shared, span, j);
+            at = max(at, begin);
+        }
         if (at >= to) {
             if (x.lane == 0) {
                 now.tokens = 0;
@@ -203,14 +219,6 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             }
             break;
         }
-        // the part, span and key head of this place in the line
-        const int hk = (int)quotient(at, total), part = part_at(p.tiles, parts, at - hk * total, x.lane);
-        const bool shared = part < p.P;
-        const Part y = load_part(p.parts + part);
-        int64_t begin = hk * total + y.begin;
-        const int j = span_at(y, shared, span, at - begin, x.lane);
-        begin += tiles_before(y, shared, span, j);
-        const int64_t stop = begin + span_tiles(y, shared, span, j);
         const int tile0 = first_tile(y) + (int)(at - begin), n = (int)(min(stop, to) - at);
         const int t0 = y.t0 + j * span, end = span_end(y, shared, span, j);
         at += n;

@@ -51,6 +51,25 @@ def test_group_sizes(members):
     assert b.t.equal(b.call(cu_seqlens=None), b.call(cu_seqlens=None))
 
 
+@pytest.mark.parametrize("N", [1, 7, 37, 150, 153, 600])
+@pytest.mark.parametrize("keys", [1, 17, 100, 900, 1100])
+def test_many_short_parts(N, keys):
+    """Few steps a part: workers' shares end before a part's first step, at it and behind it."""
+    r = random.Random(N + keys)
+    own = [(r.randint(0, keys - 1), r.choice([1, 1, 2, 5]) if N < 200 else 1) for _ in range(N)]
+    b = Batch(own, Hq=8, Hk=2, d=64, page=32, seed=N)
+    b.check(b.call())
+    b = Batch(own, [(N // 3, keys), (N // 2, 3)], Hq=8, Hk=2, d=64, page=32, seed=N)
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("tokens", [17, 64, 65, 130])
+def test_many_short_spans(tokens):
+    own = [((i * 37) % 300, tokens - i % 3) for i in range(60)]
+    b = Batch(own, Hq=8, Hk=2, d=64, page=64, seed=tokens)
+    b.check(b.call())
+
+
 def test_groups_of_all_kinds():
     """Empty groups, a group without a prefix, sequences of none, empty sequences inside a group."""
     own = [(3, 1), (0, 0), (9, 5), (0, 1), (40, 1), (0, 0), (7, 30), (300, 1)]
