@@ -81,9 +81,10 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int Hk, int workers, 
 }
 // What a beginning counts for, in tiles or steps.  With it 40 calls of random sizes, most of them
 // small, took 0.76 of their time without (geometric mean; 224 sequences of 2 keys 13 us in place of
-// 32, 19 drafts over four prefixes 64 in place of 83).  A long part's beginning is little beside its
-// steps, and HBM bounds those: 64 sequences of up to 16k keys took 443 us with it, 437 without.
-constexpr int kTilesSetUp = 3, kStepsSetUp = 4, kShortSteps = 64;
+// 32, 19 drafts over four prefixes 66 in place of 83).  A long part's beginning is little beside its
+// steps, and HBM bounds those: 64 sequences of up to 16k keys took 443 us with it, 437 without; the
+// beams of 16 prompts of 8192 109.3 with it, 106.5 without.
+constexpr int kTilesSetUp = 3, kStepsSetUp = 4, kShortTiles = 32, kShortSteps = 64;
 // A worker's least: a beginning and one tile or step.
 constexpr int kLeastTiles = kTilesSetUp + 1, kLeastSteps = kStepsSetUp + 1;
 
@@ -126,15 +127,19 @@ __device__ __forceinline__ int64_t tiles_before(const Part &x, bool shared, int 
     if (shared) return (int64_t)j * span_tiles(x, true, span, 0);
     return sum_of_tiles(j, span, (int64_t)x.first + span + kTileKeys - 1) - (int64_t)j * first_tile(x);
 }
+__device__ __forceinline__ int tiles_set_up(const Part &x)
+{
+    return x.key1 - x.key0 <= kShortTiles * kTileKeys ? kTilesSetUp : 0;
+}
 // the place of span j, with its set-up, in its part's line; that line's length
 __device__ __forceinline__ int64_t span_begin(const Part &x, bool shared, int span, int j)
 {
-    return tiles_before(x, shared, span, j) + (int64_t)j * kTilesSetUp;
+    return tiles_before(x, shared, span, j) + (int64_t)j * tiles_set_up(x);
 }
 __device__ __forceinline__ int64_t part_tiles(const Part &x, bool shared, int span)
 {
     const int n = spans_of(x, span);
-    return n ? span_begin(x, shared, span, n - 1) + kTilesSetUp + span_tiles(x, shared, span, n - 1) : 0;
+    return n ? span_begin(x, shared, span, n - 1) + tiles_set_up(x) + span_tiles(x, shared, span, n - 1) : 0;
 }
 __device__ __forceinline__ int part_steps(const Part &x)
 {

@@ -107,7 +107,7 @@ __device__ __forceinline__ Place place_of(const AttendParams &p, const Lines &li
     const int i = t - x.t0, span = 2 * p.tile_tokens;
     if (r.tiles) {
         const int j = i / span, u = i - j * span, q = u >= p.tile_tokens;
-        r.begin += span_begin(x, shared, span, j) + kTilesSetUp;
+        r.begin += span_begin(x, shared, span, j) + tiles_set_up(x);
         r.n = span_tiles(x, shared, span, j);
         r.row = q * kTileRows + (u - q * p.tile_tokens) * p.G;
         r.rows = kPieceRows;

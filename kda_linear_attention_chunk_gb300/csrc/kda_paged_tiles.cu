@@ -208,7 +208,7 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             y = load_part(p.parts + part);
             begin = hk * total + y.begin;
             j = span_at(y, shared, span, at - begin, x.lane);
-            begin += span_begin(y, shared, span, j) + kTilesSetUp;
+            begin += span_begin(y, shared, span, j) + tiles_set_up(y);
             stop = begin + span_tiles(y, shared, span, j);
             at = max(at, begin);
         }
