@@ -235,10 +235,15 @@ __device__ __forceinline__ void load_role(const Ctx &x, const Maps &maps)
             now.turn = g & 1;
             now.where = goes_to(y, shared, begin, stop, from, to);
             now.cut = cut_piece(blockIdx.x, begin, from) * kPieceRows;
-            mbar_arrive(x.bars.item_full(item & 1));
         }
         __syncwarp();
         const bool now_dealt = now.dealt(p.tile_tokens);
+        // The second pipeline waits for the first query tile's queries in dealt items alone: those before
+        // these must have come when it does, or it would take their phase, still open, for the one it wants.
+        if (now_dealt && qs[0]) ok = x.wait(x.bars.q_full(0), qs[0] - 1);
+        if (!ok) break;
+        if (x.lane == 0) mbar_arrive(x.bars.item_full(item & 1));
+        __syncwarp();
         const int seen[2] = {Span(now, p.tile_tokens, 0).seen, Span(now, p.tile_tokens, 1).seen};
         const int32_t *table = cache.table + (int64_t)y.entry * cache.max_pages;
         // A lane has a box of its own: 64 columns of page rows box lb of a tile.  It loads the entry of
