@@ -611,7 +611,10 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             tc_fence_after();
             mine++;
         }
-        float f0 = 1.f, f1 = 0.f;                        // what O, and that of the second pipeline, is multiplied by
+        // What O, and that of the second pipeline, is multiplied by.  Pieces with other maxima are joined by
+        // exact ones: the weights lose what slope m was rounded by, up to 2^-24 of its size.
+        float f0 = 1.f, f1 = 0.f;
+        auto exactly = [&](float m) { return m == -INFINITY ? 0.f : residue(m, slope<E>(m, c2)); };
         if (dealt) {
             if (q) {
                 x.c.other_ml[row] = make_float2(m, sum);
@@ -625,10 +628,13 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
             tc_fence_after();
             const float2 other = x.c.other_ml[row];
             const float top = fmaxf(m, other.x);
-            f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2);
-            f1 = other.x == -INFINITY ? 0.f : ex2((other.x - top) * c2);
+            f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2 - exactly(m));
+            f1 = other.x == -INFINITY ? 0.f : ex2((other.x - top) * c2 - exactly(other.x));
             sum = sum * f0 + other.y * f1;
             m = top;
+        } else if (where != kToOut) {
+            f0 = ex2(-exactly(m));
+            sum *= f0;
         }
         if (where != kToOut && lane < live) {            // the row's maximum (or what stands for it) and sum
             float2 *ml = where == kToCut ? p.cut_tiles_ml + cut + row
@@ -655,7 +661,7 @@ __device__ __forceinline__ void softmax_role(const Ctx &x, int warp)
                     o[j] = __float_as_uint(fmaf(__uint_as_float(other[j]), f1 * f, __uint_as_float(o[j]) * (f0 * f)));
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * (f0 * f));
             }
             if (h == D / 32 - 1) {
                 tc_fence_before();
