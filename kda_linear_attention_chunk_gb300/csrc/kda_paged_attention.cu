@@ -202,7 +202,10 @@ __global__ void __launch_bounds__(kJoinThreads, 6 / kBatch) join_kernel(const __
                     }
 #pragma unroll
                     for (int k = 0; k < kBatch; k++) {
-                        if (ml[k].x == -INFINITY) continue;      // nothing visible there: o may not even be written
+                        if (ml[k].x == -INFINITY) {      // nothing visible there, and o may not even be written,
+                            l += ml[k].y;                // or nothing but NaN, which maxima pass over: the sum has it
+                            continue;
+                        }
                         const float top = fmaxf(m, ml[k].x);
                         const float was = m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
                         const float f = ex2((ml[k].x - top) * p.scale_log2);
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6 / kBatch) join_kernel(const __
         float top = -INFINITY, sum = 0.f;
         for (int w = 0; w < team; w++) top = fmaxf(top, ms[first + w]);
         for (int w = 0; w < team; w++)
-            if (ms[first + w] != -INFINITY) sum = fmaf(ex2((ms[first + w] - top) * p.scale_log2), ls[first + w], sum);
+            sum = fmaf(ms[first + w] == -INFINITY ? 1.f : ex2((ms[first + w] - top) * p.scale_log2), ls[first + w], sum);
         const float inv = 1.f / sum;
         for (int c = threadIdx.x - first * kLanes; c < D / 2; c += team * kLanes) {
             float2 x = make_float2(0.f, 0.f);
