@@ -1,0 +1,52 @@
+"""Beam selection over vocabularies whose last slice is short (a CTA whose threads do not all have a logit)."""
+import pytest
+
+import kda_linear_attention_chunk_gb300 as kda
+from gpu_util import torch
+from test_beam import check, draw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("V", [505, 511, 513, 518, 600, 1023, 1300, 1789, 1795, 2047, 32000])
+@pytest.mark.parametrize("B", [1, 4, 8, 9, 16, 32, 33, 64])
+def test_short_slices(V, B):
+    for dtype in ("bf16", "fp16", "fp32")[:1 if V > 5000 else 3]:
+        x, scores, slots = draw(1, B, V, dtype, seed=V + B)
+        check(x, scores, slots=slots)
+
+
+@pytest.mark.parametrize("V", [50257, 128256])
+@pytest.mark.parametrize("B", [4, 8])
+def test_usual_vocabularies(V, B):
+    x, scores, slots = draw(2, B, V, "bf16", seed=B)
+    check(x, scores, slots=slots)
+
+
+def a_call(V, B, dtype):
+    """Microseconds of a call, of 20 captured ones."""
+    t = torch()
+    x, scores, _ = draw(1, B, V, dtype, seed=1)
+    s = t.tensor(scores, dtype=t.float32, device="cuda")
+    kda.beam_select(x, s)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        for _ in range(20):
+            kda.beam_select(x, s)
+    best = float("inf")
+    for _ in range(8):
+        a, b = t.cuda.Event(enable_timing=True), t.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 50)
+    return best
+
+
+@pytest.mark.parametrize("B", [16, 32])
+@pytest.mark.parametrize("V,full", [(1300, 2048), (513, 2048)])
+def test_a_short_slice_takes_no_longer_than_a_full_one(V, full, B):
+    """Fewer logits in as many CTAs: at most the time of the full slices, and half of it more for what a clock does."""
+    short, whole = a_call(V, B, "bf16"), a_call(full, B, "bf16")
+    assert short <= 1.5 * whole, (short, whole)
