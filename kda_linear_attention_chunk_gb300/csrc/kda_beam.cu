@@ -11,15 +11,18 @@
 // unevaluated sums of two fp32 numbers (the card's fp64 rate, a 64th of fp32's, made this
 // kernel take 23-37 us in fp64).
 //
-// The best B of many values: the values fall into at least B groups by threads; the
-// smallest of the groups' maxima has at least B values at or above it, and mostly few
-// more (B groups of equal size: about B ln B).  Only the threads whose own maximum
-// reaches it look at their values again and collect those that do, and these are ranked by
-// counting.  Where equal or unevenly spread values make them too many, B rounds of a
-// maximum below the one before find the same.  Ties go to the lowest index either way.
+// The best B of many values: the values fall into at least B groups; the smallest of the
+// groups' maxima has at least B values at or above it, and mostly few more (B groups of equal
+// size: about B ln B).  In a slice threads make up the groups, and only those whose own
+// maximum reaches it look at their values again and collect the ones that do, which are
+// ranked by counting.  Where equal or unevenly spread values make them too many, B rounds of
+// a maximum below the one before find the same.  A prompt's candidates, where they are
+// few, go the same way; where they are many, or too many of them are collected, the best of
+// the slices' sorted lists is taken B times.  Ties go to the lowest index either way.
 //
-// On a GB300, 16 prompts of 8 beams and 131,072 16-bit logits: 15 us and 8 us (of 28 MB, 4 us); one
-// prompt of 4 beams and 32,000 fp32 logits 5 us and 7 us: latencies, one after the other.
+// On a GB300, captured: 16 prompts of 8 beams and 131,072 16-bit logits 21 us a call (of 28 MB, 4 us); one
+// prompt of 4 beams and 32,000 logits 8.5 us, of 16, 32, 64 beams 24, 58, 119: latencies, one
+// after the other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -39,9 +42,10 @@ using tiles::fma2;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kAtOnce = 4;                   // 16-byte loads of a thread on their way
 constexpr int kLeast = 2048, kLongest = 32768;   // logits of a slice
-// Candidates that are ranked by counting: also all of a slice that leaves one of 64 groups without a value,
-// 63 vectors of 8 logits and 14 single ones.
-constexpr int kMost = 520;
+// Candidates that are ranked by counting, of a slice and of a prompt.  Of 64 beams the bound leaves 266 on
+// average and more than 520 in 2 % of the cases (a slice's rounds are long, and a call has many slices); a slice that
+// leaves one of 64 groups without a value has 63 vectors of 8 logits and 14 single ones at most.
+constexpr int kMost = 1024, kMostChosen = 520;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct BeamParams {
@@ -358,18 +362,39 @@ __device__ __forceinline__ bool better(const Candidate &a, const Candidate &b)
     return a.beam != b.beam ? a.beam < b.beam : a.key > b.key;
 }
 
+// The best of a converged warp's, in every lane.
+__device__ __forceinline__ Candidate best_of(const Candidate &c)
+{
+    const uint32_t all = 0xffffffffu, high = (uint32_t)(c.score >> 32), top = __reduce_max_sync(all, high);
+    bool in = high == top;
+    const uint32_t low = __reduce_max_sync(all, in ? (uint32_t)c.score : 0);
+    in = in && (uint32_t)c.score == low;
+    const int beam = __reduce_min_sync(all, in ? c.beam : 0x7fffffff);
+    in = in && c.beam == beam;
+    const uint32_t value = __reduce_max_sync(all, in ? (uint32_t)(c.key >> 32) : 0);
+    in = in && (uint32_t)(c.key >> 32) == value;
+    const uint32_t token = __reduce_max_sync(all, in ? (uint32_t)c.key : 0);
+    return {(uint64_t)top << 32 | low, (uint64_t)value << 32 | token, beam};
+}
+
 constexpr int kMaxBeams = 64;
+// Candidates of a beam up to which a prompt's are looked at all, twice: some 1.2 us for each 256 of the prompt,
+// as much as one of B rounds over the lists' first ones takes.  One prompt of 16 beams: 128 of a beam 18.8 us a call
+// and 22.7 in rounds, 256 29.4 and 23.9; of 64 beams, 256 122 and 84, 1024 227 and 119.
+constexpr int kFew = 128;
 
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ BeamParams p)
 {
-    __shared__ Candidate found[kMost], best_w[kWarps], best[kMaxBeams];
+    extern __shared__ uint8_t taken[];                   // of each list: candidates that are among the best already
+    __shared__ Candidate found[kMostChosen], best_w[2][kWarps], best[kMaxBeams];
     __shared__ float2 lse[kMaxBeams];
     __shared__ float score[kMaxBeams];
     __shared__ uint32_t low_w[kWarps];
+    __shared__ int count;
     __shared__ int kind[kMaxBeams];                      // 0 no hypothesis, 1 extends, 2 ended
     __shared__ int parent[kMaxBeams], slot[kMaxBeams];
-    __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.B, first = blockIdx.x * B;
+    const int lists = B * p.slices;                      // of a beam's slices, one beam after the other
     if (tid == 0) count = 0;
     if (tid < B) {
         const float s = p.scores[first + tid];
@@ -401,62 +426,71 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    const int per = p.slices * B, all = B * per;         // places of a beam's candidates
-    // The candidate at place e.  Warp w's places are w, w + 8, ..., and the beams' order moves on by
-    // one with each of a beam's places, so that the groups, whose maxima bound the best, get
-    // beams and ranks alike (a beam a group: nearly all candidates are above the bound).
-    auto candidate = [&](int e) {
-        const int i = e % kThreads, at = (e - i + i % 32 * kWarps + i / 32) / B, turn = (e - i + i % 32 * kWarps + i / 32) % B;
-        const int b = (turn + at) % B;
+    // candidate n of list i, which is slice s of beam b
+    auto candidate = [&](int i, int b, int s, int n) {
         Candidate c = {0, 0, b};
         float high = -INFINITY, low = 0.f;
-        if (at >= per) return c;                         // behind the last place
-        if (kind[b] == 2 && at == 0) {
+        if (kind[b] == 2 && s == 0 && n == 0) {
             high = score[b];
             c.key = key_of(0.f, p.end_token);
-        } else if (kind[b] == 1) {
-            c.key = __ldcg(p.best + (int64_t)(first + b) * per + at);
+        } else if (kind[b] == 1 && n < B) {
+            c.key = __ldcg(p.best + ((int64_t)first * p.slices + i) * B + n);
             if (c.key) {
                 float e1, e2;
-                const float2 n = lse[b];
-                const float sum = two_sum(two_sum(score[b], value_of(c.key), e1), -n.x, e2), rest = e1 + (e2 - n.y);
+                const float2 z = lse[b];
+                const float sum = two_sum(two_sum(score[b], value_of(c.key), e1), -z.x, e2), rest = e1 + (e2 - z.y);
                 high = sum + rest;                       // (NaN where the normaliser is)
                 low = rest - (high - sum);
                 if (isinf(sum)) high = sum, low = 0.f;
-                if (n.x != n.x || isinf(n.x)) high = -INFINITY;
+                if (z.x != z.x || isinf(z.x)) high = -INFINITY;
             }
         }
         if (high > -INFINITY) c.score = (uint64_t)rank_of(high) << 32 | rank_of(low);   // (not NaN)
         return c;
     };
-    uint32_t top = 0;
-    constexpr int kKept = 4;
-    Candidate kept[kKept];                               // the thread's first ones
+    int n = kMostChosen + 1;
+    if (B * p.slices <= kFew) {
+        // Place e holds the candidate of a scattered number, so that the groups, whose maxima bound the best, get
+        // beams, slices and ranks alike: an odd factor and a shift, which are one to one below a power of two.
+        const int all = lists * B, bits = 32 - __clz(all - 1), places = all > 1 ? 1 << bits : 1;
+        auto scattered = [&](int e) {
+            const uint32_t mask = places - 1, h = (bits + 1) / 2;
+            uint32_t x = (uint32_t)e * 0x9e3779b1u & mask;
+            x = (x ^ x >> h) * 0x85ebca6bu & mask;
+            x ^= x >> h;
+            if (e >= places || x >= all) return Candidate{0, 0, 0};
+            const int i = x / B, b = i / p.slices;
+            return candidate(i, b, i - b * p.slices, x - i * B);
+        };
+        uint32_t top = 0;
+        constexpr int kKept = 4;
+        Candidate kept[kKept];                           // the thread's first ones
 #pragma unroll
-    for (int i = 0; i < kKept; i++) {
-        kept[i] = i * kThreads < all ? candidate(tid + i * kThreads) : Candidate{0, 0, 0};
-        top = max(top, (uint32_t)(kept[i].score >> 32));
-    }
-    for (int e = tid + kKept * kThreads; e - tid < all; e += kThreads) top = max(top, (uint32_t)(candidate(e).score >> 32));
-    for (int o = 1; o < kThreads / p.groups; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = __reduce_min_sync(0xffffffffu, top);
-    if (lane == 0) low_w[warp] = top;
-    __syncthreads();
-    uint32_t bound = low_w[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; w++) bound = min(bound, low_w[w]);
-    auto collect = [&](const Candidate &c) {
-        if (c.score && (uint32_t)(c.score >> 32) >= bound) {
-            const int k = atomicAdd(&count, 1);
-            if (k < kMost) found[k] = c;
+        for (int i = 0; i < kKept; i++) {
+            kept[i] = i * kThreads < places ? scattered(tid + i * kThreads) : Candidate{0, 0, 0};
+            top = max(top, (uint32_t)(kept[i].score >> 32));
         }
-    };
+        for (int e = tid + kKept * kThreads; e < places; e += kThreads) top = max(top, (uint32_t)(scattered(e).score >> 32));
+        for (int o = 1; o < kThreads / p.groups; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = __reduce_min_sync(0xffffffffu, top);
+        if (lane == 0) low_w[warp] = top;
+        __syncthreads();
+        uint32_t bound = low_w[0];
 #pragma unroll
-    for (int i = 0; i < kKept; i++) collect(kept[i]);
-    for (int e = tid + kKept * kThreads; e - tid < all; e += kThreads) collect(candidate(e));
-    __syncthreads();
-    const int n = count;
-    if (n <= kMost) {
+        for (int w = 1; w < kWarps; w++) bound = min(bound, low_w[w]);
+        auto collect = [&](const Candidate &c) {
+            if (c.score && (uint32_t)(c.score >> 32) >= bound) {
+                const int k = atomicAdd(&count, 1);
+                if (k < kMostChosen) found[k] = c;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kKept; i++) collect(kept[i]);
+        for (int e = tid + kKept * kThreads; e < places; e += kThreads) collect(scattered(e));
+        __syncthreads();
+        n = count;
+    }
+    if (n <= kMostChosen) {
         // eight lanes count for a candidate
         for (int i0 = tid / 8; i0 - tid / 8 < max(n, B); i0 += kThreads / 8) {
             const bool there = i0 < n;
@@ -475,27 +509,32 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
             }
         }
     } else {
-        Candidate last = {~(uint64_t)0, 0, -1};
+        // B times the best of the lists' first candidates: a thread has every 256th list
+        for (int i = tid; i < lists; i += kThreads) taken[i] = 0;
+        const int b0 = tid / p.slices, s0 = tid - b0 * p.slices, db = kThreads / p.slices, ds = kThreads - db * p.slices;
+        Candidate own, of_warp;                          // the best of the thread's lists, and of the warp's
+        int list = 0;                                    // whose it is
+        auto look = [&]() {
+            own = {0, 0, B};
+            for (int i = tid, b = b0, s = s0; i < lists; i += kThreads, b += db, s += ds) {
+                if (s >= p.slices) s -= p.slices, b++;
+                const Candidate c = candidate(i, b, s, taken[i]);
+                if (c.score && better(c, own)) own = c, list = i;
+            }
+        };
+        look();
+        of_warp = best_of(own);
         for (int k = 0; k < B; k++) {
-            Candidate mine = {0, 0, B};
-            for (int e = tid; e - tid < all; e += kThreads) {
-                const Candidate c = candidate(e);
-                if (c.score && better(last, c) && better(c, mine)) mine = c;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) {
-                const Candidate other = {__shfl_xor_sync(0xffffffffu, mine.score, o), __shfl_xor_sync(0xffffffffu, mine.key, o),
-                                         __shfl_xor_sync(0xffffffffu, mine.beam, o)};
-                if (better(other, mine)) mine = other;
-            }
+            if (lane == 0) best_w[k & 1][warp] = of_warp;
             __syncthreads();
-            if (lane == 0) best_w[warp] = mine;
-            __syncthreads();
-            last = best_w[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; w++)
-                if (better(best_w[w], last)) last = best_w[w];
-            if (tid == 0) best[k] = last;
+            const Candidate next = best_of(best_w[k & 1][lane % kWarps]);
+            if (tid == 0) best[k] = next;
+            const bool is_own = next.score && own.score == next.score && own.beam == next.beam && own.key == next.key;
+            if (is_own) {
+                taken[list]++;
+                look();
+            }
+            if (__any_sync(0xffffffffu, is_own)) of_warp = best_of(own);
         }
     }
     __syncthreads();
@@ -583,6 +622,7 @@ cudaError_t launch_beam_select(const BeamArgs &a)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.G);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)(a.B * p.slices);     // at most 64 x 512
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

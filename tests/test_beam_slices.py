@@ -1,4 +1,5 @@
 """Beam selection over vocabularies whose last slice is short (a CTA whose threads do not all have a logit)."""
+import numpy as np
 import pytest
 
 import kda_linear_attention_chunk_gb300 as kda
@@ -50,3 +51,32 @@ def test_a_short_slice_takes_no_longer_than_a_full_one(V, full, B):
     """Fewer logits in as many CTAs: at most the time of the full slices, and half of it more for what a clock does."""
     short, whole = a_call(V, B, "bf16"), a_call(full, B, "bf16")
     assert short <= 1.5 * whole, (short, whole)
+
+
+@pytest.mark.parametrize("B", [16, 32, 64])
+def test_many_slices_take_no_rounds_over_all_their_candidates(B):
+    """Sixteen slices of 2048 logits for one, in other CTAs: a round has more lists to look at, and as many rounds."""
+    many, one = a_call(32768, B, "bf16"), a_call(2048, B, "bf16")
+    assert many <= 4 * one, (many, one)
+
+
+@pytest.mark.parametrize("V", [32768, 100000])
+@pytest.mark.parametrize("B", [16, 31, 64])
+def test_many_slices(V, B):
+    """Steps with one hypothesis, with ended beams, and with equal logits, whose candidates are taken from the lists."""
+    r = np.random.RandomState(V)
+    x, scores, slots = draw(1, B, V, "bf16", seed=B)
+    check(x, scores, (r.rand(1, B) < 0.3).astype(np.int32), 17, slots)
+    x[1:] = x[:1]
+    check(x, 0 * scores, slots=slots)
+    scores[:, 1:] = -np.inf
+    check(x, scores, slots=slots)
+
+
+@pytest.mark.parametrize("V", [300, 4096, 40000])
+def test_equal_logits_of_many_beams(V):
+    """More equal candidates than are ranked by counting, few of a beam and many."""
+    x, scores, slots = draw(2, 32, V, "bf16", seed=3)
+    x[:] = 0
+    check(x, 0 * scores, slots=slots)
+    check(x, -0.25 * np.arange(64).reshape(2, 32) % 2, slots=slots)
