@@ -44,7 +44,7 @@ constexpr int kAtOnce = 4;                   // 16-byte loads of a thread on the
 constexpr int kLeast = 2048, kLongest = 32768;   // logits of a slice
 // Candidates that are ranked by counting, of a slice and of a prompt.  Of 64 beams the bound leaves 266 on
 // average and more than 520 in 2 % of the cases (a slice's rounds are long, and a call has many slices); a slice that
-// leaves one of 64 groups without a value has 63 vectors of 8 logits and 14 single ones at most.
+// leaves one of 64 groups without a value has 63 vectors of 8 logits and 7 single ones at most.
 constexpr int kMost = 1024, kMostChosen = 520;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -178,7 +178,96 @@ __device__ __forceinline__ bool extends(const BeamParams &p, int beam)
     return p.scores[beam] > -INFINITY && !(p.ended && p.ended[beam]);
 }
 
-template <typename E>
+// A row of logits in vectors of 16 bytes from its first one on, wherever in memory it begins: which
+// logits a thread has, and so the order of the row's sum, are the same for equal rows, whose
+// candidates have to be equal.  kShifted: it may begin inside 16 bytes (20 registers more).
+template <typename E, bool kShifted> struct Row {
+    static constexpr int kN = Vec<E>::kN;
+    const E *row;
+    const uint4 *body;               // the 16 bytes in which the row begins,
+    int shift;                       // at this byte of them
+    int last;                        // the last vector whose bytes lie in two pieces of 16 that are all the row's
+    __device__ Row(const BeamParams &p, int beam)
+    {
+        row = (const E *)p.logits + (int64_t)beam * p.row_stride;
+        shift = (int)((uintptr_t)row & 15);
+        body = reinterpret_cast<const uint4 *>((uintptr_t)row - shift);
+        last = (int)(((int64_t)p.V * (int)sizeof(E) + shift) / 16) - 2;
+    }
+    // vectors v, v + kThreads, ...: those below end
+    __device__ __forceinline__ void load(int v, int end, uint4 (&r)[kAtOnce]) const
+    {
+        const uint32_t none = Vec<E>::kLowest;
+        if (!kShifted || shift == 0) {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++)
+                r[i] = v + i * kThreads < end ? __ldg(body + v + i * kThreads) : make_uint4(none, none, none, none);
+        } else if (shift < 4) {
+            load_shifted<0>(v, end, r);
+        } else if (shift < 8) {
+            load_shifted<1>(v, end, r);
+        } else if (shift < 12) {
+            load_shifted<2>(v, end, r);
+        } else {
+            load_shifted<3>(v, end, r);
+        }
+    }
+    // kWords: 32-bit words of a piece before the row begins
+    template <int kWords> __device__ __forceinline__ void load_shifted(int v, int end, uint4 (&r)[kAtOnce]) const
+    {
+        if (v >= 1 && v + (kAtOnce - 1) * kThreads < min(end, last + 1)) {
+            uint4 next[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                r[i] = __ldg(body + v + i * kThreads);
+                next[i] = first_words<kWords + 1>(body + v + i * kThreads + 1);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) r[i] = joined<kWords>(r[i], next[i]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; i++) {
+            const int at = v + i * kThreads;
+            const uint32_t none = Vec<E>::kLowest;
+            if (at >= end) r[i] = make_uint4(none, none, none, none);
+            else if (at >= 1 && at <= last) r[i] = joined<kWords>(__ldg(body + at), first_words<kWords + 1>(body + at + 1));
+            else r[i] = single(at);
+        }
+    }
+    template <int n> static __device__ __forceinline__ uint4 first_words(const uint4 *x)
+    {
+        if (n == 1) return make_uint4(__ldg(reinterpret_cast<const uint32_t *>(x)), 0, 0, 0);
+        if (n == 2) {
+            const uint2 y = __ldg(reinterpret_cast<const uint2 *>(x));
+            return make_uint4(y.x, y.y, 0, 0);
+        }
+        return __ldg(x);
+    }
+    // the 16 bytes of a, then b, from `shift` on
+    template <int kWords> __device__ __forceinline__ uint4 joined(const uint4 &a, const uint4 &b) const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int bits = (shift & 2) * 8;
+        return make_uint4(__funnelshift_r(w[kWords], w[kWords + 1], bits), __funnelshift_r(w[kWords + 1], w[kWords + 2], bits),
+                          __funnelshift_r(w[kWords + 2], w[kWords + 3], bits), __funnelshift_r(w[kWords + 3], w[kWords + 4], bits));
+    }
+    // a vector, logit by logit: one at an end of the row, which may be that of the memory
+    __device__ __forceinline__ uint4 single(int v) const
+    {
+        if (sizeof(E) == 4) {
+            const uint32_t *x = reinterpret_cast<const uint32_t *>(row) + v * kN;
+            return make_uint4(__ldg(x), __ldg(x + 1), __ldg(x + 2), __ldg(x + 3));
+        }
+        const uint16_t *x = reinterpret_cast<const uint16_t *>(row) + v * kN;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = __ldg(x + 2 * i) | (uint32_t)__ldg(x + 2 * i + 1) << 16;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <typename E, bool kShifted>
 __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int kN = Vec<E>::kN;
@@ -190,16 +279,12 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
     const int beam = blockIdx.x / p.slices, slice = blockIdx.x - beam * p.slices;
     if (!extends(p, beam)) return;
     if (tid == 0) count = 0;
-    // the row: elements before the first 16-byte boundary, vectors, elements behind them
-    const E *row = (const E *)p.logits + (int64_t)beam * p.row_stride;
-    const int before = min(p.V, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(E));
-    const int vecs = (p.V - before) / kN, behind = p.V - before - vecs * kN;
-    const uint4 *body = reinterpret_cast<const uint4 *>(row + before);
+    const Row<E, kShifted> row(p, beam);
+    const int vecs = p.V / kN, behind = p.V - vecs * kN;
     const int first = slice * (p.slice / kN) + tid, end = min(vecs, (slice + 1) * (p.slice / kN));
-    // the few others are the first slice's, one to a thread
-    int odd = -1;
-    if (slice == 0) odd = tid < before ? tid : tid >= 32 && tid - 32 < behind ? before + vecs * kN + tid - 32 : -1;
-    const float single = odd >= 0 ? Vec<E>::one(row[odd]) : -INFINITY;
+    // the few logits behind the vectors are the first slice's, one to a thread
+    const int odd = slice == 0 && tid < behind ? vecs * kN + tid : -1;
+    const float single = odd >= 0 ? Vec<E>::one(row.row[odd]) : -INFINITY;
 
     // the thread's maximum (without NaN) and the sum of exponentials relative to it, or to
     // 0 where nothing is finite; a NaN among the logits makes the sum NaN, and with it the
@@ -208,11 +293,7 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
     if (top > -INFINITY) base = top, base2 = base * kLog2e;
     for (int v = first; v < end; v += kAtOnce * kThreads) {
         uint4 r[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; i++) {
-            const uint32_t none = Vec<E>::kLowest;
-            r[i] = v + i * kThreads < end ? __ldg(body + v + i * kThreads) : make_uint4(none, none, none, none);
-        }
+        row.load(v, end, r);
         uint32_t most = Vec<E>::kLowest;
 #pragma unroll
         for (int i = 0; i < kAtOnce; i++)
@@ -291,16 +372,14 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
         if (odd >= 0) use(single, odd);
         for (int v = first; v < end; v += kAtOnce * kThreads) {
             uint4 r[kAtOnce];
-#pragma unroll
-            for (int i = 0; i < kAtOnce; i++)
-                if (v + i * kThreads < end) r[i] = __ldg(body + v + i * kThreads);
+            row.load(v, end, r);
 #pragma unroll
             for (int i = 0; i < kAtOnce; i++) {
                 if (v + i * kThreads >= end) break;
                 float x[kN];
                 Vec<E>::up(r[i], x);
 #pragma unroll
-                for (int j = 0; j < kN; j++) use(x[j], before + (v + i * kThreads) * kN + j);
+                for (int j = 0; j < kN; j++) use(x[j], (v + i * kThreads) * kN + j);
             }
         }
     };
@@ -621,8 +700,10 @@ cudaError_t launch_beam_select(const BeamArgs &a)
     const int64_t parts = (int64_t)a.G * a.B * p.slices;
     p.best = (uint64_t *)a.workspace;
     p.sums = (float2 *)(p.best + parts * a.B);
-    auto *kernel = a.dtype == KDA_F32 ? slice_kernel<float>
-                   : a.dtype == KDA_F16 ? slice_kernel<__half> : slice_kernel<__nv_bfloat16>;
+    const bool shifted = (((uintptr_t)a.logits | (uint64_t)a.row_stride * (a.dtype == KDA_F32 ? 4 : 2)) & 15) != 0;
+    auto *kernel = a.dtype == KDA_F32 ? (shifted ? slice_kernel<float, true> : slice_kernel<float, false>)
+                   : a.dtype == KDA_F16 ? (shifted ? slice_kernel<__half, true> : slice_kernel<__half, false>)
+                                        : (shifted ? slice_kernel<__nv_bfloat16, true> : slice_kernel<__nv_bfloat16, false>);
     kernel<<<(unsigned)parts, kThreads, 0, a.stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

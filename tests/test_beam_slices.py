@@ -80,3 +80,35 @@ def test_equal_logits_of_many_beams(V):
     x[:] = 0
     check(x, 0 * scores, slots=slots)
     check(x, -0.25 * np.arange(64).reshape(2, 32) % 2, slots=slots)
+
+
+@pytest.mark.parametrize("V", [33, 3001, 100003])
+@pytest.mark.parametrize("B", [2, 16, 31, 64])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_equal_beams_whose_rows_begin_anywhere(V, B, dtype):
+    """Rows of odd length, at different places of 16 bytes: their candidates are equal all the same, the lower beam's first."""
+    x, scores, slots = draw(1, B, V, dtype, seed=B)
+    x[1:] = x[:1]
+    if B * V < 200 * 20000:
+        check(x, 0 * scores, slots=slots)
+        check(x, -0.5 * (np.arange(B)[None] // 3), slots=slots)
+    else:                                              # (the plain form would take long)
+        best, parents, tokens = kda.beam_select(x, torch().zeros(1, B, device="cuda"))[:3]
+        assert parents[0].tolist() == list(range(B)) and (tokens == x[0].float().argmax()).all() and (best == best[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V", [7, 9, 16, 17, 24, 25, 8191, 8192, 8193])
+def test_rows_at_every_place_of_16_bytes(V, dtype):
+    """The same bytes in and out, whatever the place; nothing before or behind a row enters."""
+    t = torch()
+    x, scores, slots = draw(2, 3, V, dtype, seed=V)
+    want = check(x, scores, slots=slots)
+    for at in range(16 // x.element_size()):
+        for apart in (V + 3, V + 16, -(-V // 8) * 8 + 8):
+            wide = t.full((6 * apart + 16,), float("nan"), dtype=x.dtype, device="cuda")
+            rows = wide[at:at + 6 * apart].view(6, apart)[:, :V]
+            rows.copy_(x)
+            got = kda.beam_select(rows, t.tensor(scores, dtype=t.float32, device="cuda"),
+                                  slots=t.tensor(slots, dtype=t.int32, device="cuda"))
+            assert all(a is b is None or t.equal(a, b) for a, b in zip(got, want))
