@@ -662,6 +662,7 @@ int kda_paged_append(const void *q, int64_t q_stride, const void *k, int64_t k_s
  *   workspace     device memory of at least kda_paged_attention_workspace(...) bytes,
  *                 16-byte aligned, of this call until it has run: calls that may run at
  *                 the same time, captured ones too, need one each.
+ * A row that sees a key whose score is NaN gets NaN, however its keys are cut into pieces.
  * A value row that is not finite reaches, besides the rows that see it, rows of the same
  * sequence or group in the same tile (up to 128 keys by 256 query rows).  Probabilities are
  * rounded to 16 bits as in kda_window_prefill, sums and joins are fp32; the same call
@@ -728,8 +729,11 @@ int kda_pages_copy(const kda_pool *caches, int num_caches, int num_pages, int pa
  *   workspace   device memory of at least kda_beam_select_workspace(...) bytes, 16-byte
  *               aligned, of this call until it has run.
  *   G >= 1; 1 <= B <= 64; 1 <= V <= 2^24; G * B at most 2^20.
- * Sums are fp32 within a row's part of some thousand tokens and fp64 beyond; candidates are
- * compared in fp64.  Logits must be aligned to their element (rows need no alignment).
+ * Sums of exponentials are fp32 within a part of a row of at most 32,768 logits, and these are joined in
+ * fp64; a normaliser is off by less than 2^-18.  Candidates are compared as sums of two fp32 numbers
+ * (the normaliser's rounding decides between beams that are closer); of one beam the larger
+ * logit is the better candidate, however large the score.  Beams of equal scores and logits are equal
+ * wherever their rows begin.  Logits must be aligned to their element (rows need no alignment).
  * Outputs must not overlap an input or each other.  Returns a kda_status.
  */
 int kda_beam_select(const void *logits, int64_t row_stride, int dtype, const float *scores, const int32_t *ended,
