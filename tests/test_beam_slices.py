@@ -112,3 +112,26 @@ def test_rows_at_every_place_of_16_bytes(V, dtype):
             got = kda.beam_select(rows, t.tensor(scores, dtype=t.float32, device="cuda"),
                                   slots=t.tensor(slots, dtype=t.int32, device="cuda"))
             assert all(a is b is None or t.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("V", [1 << 24, (1 << 24) - 5])
+def test_the_largest_vocabulary_and_beams(V):
+    """As many slices and lists as there can be; the plain form a row at a time."""
+    t, B = torch(), 64
+    g = t.Generator(device="cuda")
+    g.manual_seed(5)
+    x = t.empty(B, V, device="cuda")
+    for b in range(B):
+        x[b] = 3 * t.randn(V, generator=g, device="cuda")
+    scores = -0.02 * t.arange(B, device="cuda")[None]
+    got = kda.beam_select(x, scores)
+    every, tokens = [], []
+    for b in range(B):
+        row = x[b].double()
+        top = t.sort(x[b], descending=True, stable=True)
+        every.append(scores[0, b].double() + top.values[:B].double() - t.logsumexp(row, 0))
+        tokens.append(top.indices[:B])
+    best = t.sort(t.cat(every), descending=True, stable=True)
+    at = best.indices[:B]
+    assert t.equal(got[1][0].long(), at // B) and t.equal(got[2][0].long(), t.cat(tokens)[at])
+    assert ((got[0][0].double() - best.values[:B]).abs() <= 2.0 ** -18 + 2.0 ** -24 * best.values[:B].abs()).all()
