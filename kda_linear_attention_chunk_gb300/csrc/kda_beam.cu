@@ -62,8 +62,7 @@ struct BeamParams {
     int groups;                      // of threads, whose maxima bound the best: at least B
 };
 
-// A number that grows with the value, and back; that of -inf is kNone.
-constexpr uint32_t kNone = 0x007fffffu;
+// A number that grows with the value, and back.
 __device__ __forceinline__ uint32_t rank_of(float x)
 {
     const uint32_t b = __float_as_uint(x + 0.f);         // -0 and 0 are equal
